@@ -24,7 +24,8 @@ LIB = os.path.join(HERE, "libopq.so")
 # the benchmark's streaming-ceiling kernel, a library of its own
 CEILING_LIB = os.path.join(HERE, "libopq_ceiling.so")
 
-SOURCES = ["opq_api.cpp", "tables.cpp", "quantize.hip", "dequantize.hip", "linear.hip"]
+SOURCES = ["opq_api.cpp", "tables.cpp", "quantize.hip", "dequantize.hip", "linear.hip",
+           "attention_api.cpp", "rotary.hip", "cache.hip", "attention.hip"]
 CEILING_SOURCES = ["stream_ceiling.hip"]
 ARCH = "gfx950"
 
