@@ -59,6 +59,34 @@ __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh));
 }
 
+// OPQ codes are looked up two at a time: entry (two sign bits, code byte) of a table
+// in LDS is the pair as bfloat16, so eight codes take four reads and twelve
+// VALU instructions (the permutes of decode.hpp take 34, which bounded this
+// kernel).  4 KB.
+// The entries of one sign pair are kSignStride apart, not 256: magnitudes crowd
+// around a few codes, and without the shift their banks coincide for all four
+// sign pairs (9.2 cycles a read measured, 6.3 with it).
+constexpr int kSignStride = 276, kPairs = 4 * kSignStride;
+typedef const uint32_t* PairTable;
+
+__device__ __forceinline__ void build_pairs(const LevelPlanes& lp, uint32_t* pairs) {
+  RowLut t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { t.lo[i] = lp.lo[i]; t.hi[i] = lp.hi[i]; }
+#pragma unroll
+  for (uint32_t sign = 0; sign < 4; ++sign) {
+    uint32_t o[4];
+    decode_word_split(threadIdx.x, sign, t, o);  // a code byte a thread
+    pairs[sign * kSignStride + threadIdx.x] = o[0];
+  }
+}
+// Pairs 0..3 of word w with the signs in bits 0..7 of sb.
+__device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t sb, PairTable t, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = t[((w >> (8 * i)) & 0xFFu) + __umul24((sb >> (2 * i)) & 3u, kSignStride)];
+}
+
 template <int N>
 struct Words {
   uint32_t w[N];
@@ -95,15 +123,15 @@ struct KeyTile<OPQ_CACHE_BF16, D> {
   Words<D / 8> raw;
   // first of the eight dimensions that lane quarter g holds in product step s
   __device__ static int dim_at(int s, int g) { return 32 * s + 8 * g; }
-  __device__ __forceinline__ void load(const char* row, const char*, int g) {
+  __device__ __forceinline__ void load(const char* rows, const char*, uint32_t r, int g) {
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
-      const Words<4> t = load_words<4>(row + 64 * s + 16 * g);
+      const Words<4> t = load_words<4>(rows + (r * 2 * D + 64 * s + 16 * g));
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw.w[4 * s + i] = t.w[i];
     }
   }
-  __device__ __forceinline__ bf16x8_t at(int s, const RowLut&) const {
+  __device__ __forceinline__ bf16x8_t at(int s, PairTable) const {
     return frag(raw.w[4 * s], raw.w[4 * s + 1], raw.w[4 * s + 2], raw.w[4 * s + 3]);
   }
 };
@@ -112,15 +140,15 @@ template <int D>
 struct KeyTile<OPQ_CACHE_FP8, D> {
   Words<D / 16> raw;
   __device__ static int dim_at(int s, int g) { return 64 * (s >> 1) + 16 * g + 8 * (s & 1); }
-  __device__ __forceinline__ void load(const char* row, const char*, int g) {
+  __device__ __forceinline__ void load(const char* rows, const char*, uint32_t r, int g) {
 #pragma unroll
     for (int s = 0; s < D / 64; ++s) {
-      const Words<4> t = load_words<4>(row + 64 * s + 16 * g);
+      const Words<4> t = load_words<4>(rows + (r * D + 64 * s + 16 * g));
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw.w[4 * s + i] = t.w[i];
     }
   }
-  __device__ __forceinline__ bf16x8_t at(int s, const RowLut&) const {
+  __device__ __forceinline__ bf16x8_t at(int s, PairTable) const {
     const uint32_t a = raw.w[2 * s], b = raw.w[2 * s + 1];
     return frag(from_e4m3<false>(a), from_e4m3<true>(a), from_e4m3<false>(b), from_e4m3<true>(b));
   }
@@ -132,16 +160,16 @@ struct KeyTile<OPQ_CACHE_OPQ4, D> {
   Words<kSteps> raw;
   uint64_t sign;  // byte s: signs of step s
   __device__ static int dim_at(int s, int g) { return 8 * (kSteps * g + s); }
-  __device__ __forceinline__ void load(const char* row, const char* signs, int g) {
-    raw = load_words<kSteps>(row + 4 * kSteps * g);
-    const char* p = signs + kSteps * g;
+  __device__ __forceinline__ void load(const char* rows, const char* signs, uint32_t r, int g) {
+    raw = load_words<kSteps>(rows + (r * (D / 2) + 4 * kSteps * g));
+    const char* p = signs + (r * (D / 8) + kSteps * g);
     if (kSteps == 2) sign = *reinterpret_cast<const uint16_t*>(p);
     else if (kSteps == 4) sign = *reinterpret_cast<const uint32_t*>(p);
     else sign = *reinterpret_cast<const uint64_t*>(p);
   }
-  __device__ __forceinline__ bf16x8_t at(int s, const RowLut& lut) const {
+  __device__ __forceinline__ bf16x8_t at(int s, PairTable lut) const {
     uint32_t o[4];
-    decode_word_split(raw.w[s], (uint32_t)(sign >> (8 * s)) & 0xFFu, lut, o);
+    decode_pairs(raw.w[s], (uint32_t)(sign >> (8 * s)), lut, o);
     return frag(o[0], o[1], o[2], o[3]);
   }
 };
@@ -168,10 +196,10 @@ struct ValueTile<OPQ_CACHE_BF16, D> {
   static constexpr int kWords = D / 32;
   static constexpr int kTogether = 2;  // result tiles that one call of tiles() gives
   Words<kWords> raw[8];
-  __device__ __forceinline__ void load(int i, const char* row, const char*, int c) {
-    raw[i] = load_words<kWords>(row + 4 * kWords * c);
+  __device__ __forceinline__ void load(int i, const char* rows, const char*, uint32_t r, int c) {
+    raw[i] = load_words<kWords>(rows + (r * 2 * D + 4 * kWords * c));
   }
-  __device__ __forceinline__ void tiles(int t, const RowLut&, bf16x8_t (&v)[kTogether]) const {
+  __device__ __forceinline__ void tiles(int t, PairTable, bf16x8_t (&v)[kTogether]) const {
     uint32_t p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = raw[i].w[t];
@@ -184,10 +212,10 @@ struct ValueTile<OPQ_CACHE_FP8, D> {
   static constexpr int kWords = D / 64;
   static constexpr int kTogether = 4;
   Words<kWords> raw[8];
-  __device__ __forceinline__ void load(int i, const char* row, const char*, int c) {
-    raw[i] = load_words<kWords>(row + 4 * kWords * c);
+  __device__ __forceinline__ void load(int i, const char* rows, const char*, uint32_t r, int c) {
+    raw[i] = load_words<kWords>(rows + (r * D + 4 * kWords * c));
   }
-  __device__ __forceinline__ void tiles(int t, const RowLut&, bf16x8_t (&v)[kTogether]) const {
+  __device__ __forceinline__ void tiles(int t, PairTable, bf16x8_t (&v)[kTogether]) const {
     uint32_t o[kTogether][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -211,16 +239,17 @@ struct ValueTile<OPQ_CACHE_OPQ4, D> {
   static constexpr int kTogether = 8;
   Words<kWords> raw[8];
   uint32_t sign[8];
-  __device__ __forceinline__ void load(int i, const char* row, const char* signs, int c) {
-    raw[i] = load_words<kWords>(row + 4 * kWords * c);
-    if (kWords == 1) sign[i] = reinterpret_cast<const uint8_t*>(signs)[c];
-    else sign[i] = reinterpret_cast<const uint16_t*>(signs)[c];
+  __device__ __forceinline__ void load(int i, const char* rows, const char* signs, uint32_t r, int c) {
+    raw[i] = load_words<kWords>(rows + (r * (D / 2) + 4 * kWords * c));
+    const char* p = signs + (r * (D / 8) + kWords * c);
+    if (kWords == 1) sign[i] = *reinterpret_cast<const uint8_t*>(p);
+    else sign[i] = *reinterpret_cast<const uint16_t*>(p);
   }
-  __device__ __forceinline__ void tiles(int t, const RowLut& lut, bf16x8_t (&v)[kTogether]) const {
+  __device__ __forceinline__ void tiles(int t, PairTable lut, bf16x8_t (&v)[kTogether]) const {
     uint32_t o[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      decode_word_split(raw[i].w[t], (sign[i] >> (8 * t)) & 0xFFu, lut, o[i]);
+      decode_pairs(raw[i].w[t], sign[i] >> (8 * t), lut, o[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t p[8];
@@ -237,17 +266,17 @@ struct ValueTile<OPQ_CACHE_OPQ4, 64> {
   uint32_t raw[8];   // four codes
   uint32_t sign[8];  // four signs
   int shift;
-  __device__ __forceinline__ void load(int i, const char* row, const char* signs, int c) {
-    raw[i] = reinterpret_cast<const uint16_t*>(row)[c];
-    sign[i] = reinterpret_cast<const uint8_t*>(signs)[c >> 1];
+  __device__ __forceinline__ void load(int i, const char* rows, const char* signs, uint32_t r, int c) {
+    raw[i] = *reinterpret_cast<const uint16_t*>(rows + (r * 32 + 2 * c));
+    sign[i] = *reinterpret_cast<const uint8_t*>(signs + (r * 8 + (c >> 1)));
     shift = 4 * (c & 1);
   }
-  __device__ __forceinline__ void tiles(int, const RowLut& lut, bf16x8_t (&v)[kTogether]) const {
+  __device__ __forceinline__ void tiles(int, PairTable lut, bf16x8_t (&v)[kTogether]) const {
     uint32_t o[4][4];  // of keys 2 i and 2 i + 1
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t s0 = (sign[2 * i] >> shift) & 15u, s1 = (sign[2 * i + 1] >> shift) & 15u;
-      decode_word_split(raw[2 * i] | (raw[2 * i + 1] << 16), s0 | (s1 << 4), lut, o[i]);
+      decode_pairs(raw[2 * i] | (raw[2 * i + 1] << 16), s0 | (s1 << 4), lut, o[i]);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -287,7 +316,11 @@ __device__ __forceinline__ Extent extent(const AttentionArgs& a, int b, int last
 // ------------------------------------------------------------------ the kernel
 
 template <int FMT, int D, int NT>
-__global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
+constexpr int kOccupancy = FMT == OPQ_CACHE_BF16 ? (D == 256 ? 1 : NT * D == 64 ? 3 : 2)
+                                                 : (NT == 1 && D <= 128 ? 3 : 2);
+
+template <int FMT, int D, int NT>
+__global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(AttentionArgs a) {
   constexpr int kSteps = D / 32;  // product steps of a score
   constexpr int kTiles = D / 16;  // result tiles, and dimensions of a value lane
   constexpr int kRow = kRowBytes<FMT, D>;
@@ -308,7 +341,10 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
     unit = (j / a.groups) * 8 + xcd;
     if (unit >= a.batch * a.kv_heads * a.splits) return;
   }
-  const int split = unit % a.splits, bh = unit / a.splits;
+  // Pieces of one sequence are far apart: the ones that a short sequence does not
+  // have would otherwise be every blockIdx of some XCDs, which then stand idle
+  // (32 sequences of half the longest length: 83 against 58 us).
+  const int pairs = a.batch * a.kv_heads, split = unit / pairs, bh = unit - split * pairs;
   const int kvh = bh % a.kv_heads, b = bh / a.kv_heads;
 
   const int r0 = rg * NT * 16;
@@ -320,14 +356,17 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
   const int64_t k1 = split + 1 < a.splits && k0 + a.chunk < ex.end ? k0 + a.chunk : ex.end;
   const bool direct = a.splits == 1 || ex.end <= a.chunk;  // sees all of its rows' keys
 
-  RowLut lut;
+  __shared__ uint32_t lut[FMT == OPQ_CACHE_OPQ4 ? kPairs : 1];
   if (FMT == OPQ_CACHE_OPQ4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { lut.lo[i] = a.lp.lo[i]; lut.hi[i] = a.lp.hi[i]; }
+    build_pairs(a.lp, lut);
+    __syncthreads();
   }
 
-  // Q, the B operand: row c of each tile
-  bf16x8_t q[NT][kSteps];
+  // Q, the B operand: row c of each tile.  Where registers are short the
+  // workgroup's waves share one copy in LDS, in the order of their reads.
+  constexpr bool kShareQ = FMT == OPQ_CACHE_BF16 && D == 128 && NT == 2;
+  __shared__ bf16x8_t q_all[kShareQ ? NT : 1][kShareQ ? kSteps : 1][kShareQ ? kWave : 1];
+  bf16x8_t q[kShareQ ? 1 : NT][kShareQ ? 1 : kSteps];
   int token[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -337,11 +376,19 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
                         (int64_t)(kvh * a.share + (r - t * a.share)) * a.q_head;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
+      if (kShareQ && s % kWaves != wave) continue;
       u32x4_t w = {0u, 0u, 0u, 0u};
       if (r < a.rows) w = *reinterpret_cast<const u32x4_t*>(p + KeyTile<FMT, D>::dim_at(s, g));
-      q[n][s] = __builtin_bit_cast(bf16x8_t, w);
+      const bf16x8_t v = __builtin_bit_cast(bf16x8_t, w ^ a.q_flip);
+      if constexpr (kShareQ) q_all[n][s][lane] = v;
+      else q[n][s] = v;
     }
   }
+  if (kShareQ) __syncthreads();
+  auto q_at = [&](int n, int s) {
+    if constexpr (kShareQ) return q_all[n][s][lane];
+    else return q[n][s];
+  };
 
   floatx4_t o[NT][kTiles];
   float m[NT], l[NT];
@@ -353,42 +400,84 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
     for (int j = 0; j < kTiles; ++j) o[n][j] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
+  // Page ids: lane i holds that of page `held + i`; a step reads its two from there.
   const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
   const int64_t page_mask = ((int64_t)1 << a.page_shift) - 1;
-
-  for (int64_t kk = k0 + wave * kStep; kk < k1; kk += kRound) {
-    // the two 16-key tiles, each inside one page; a tile past the end is read
-    // from the last tile instead, rows past it from the last row
-    KeyTile<FMT, D> kt[2];
-    V vt;
-    floatx4_t ks[2], vs[2];
+  int64_t held = k0 >> a.page_shift;
+  uint32_t ids = 0u;
+  auto hold = [&](int64_t first) {
+    held = first;
+    const int64_t p = first + lane;
+    if (p < a.max_pages) ids = (uint32_t)table[p];
+    // waited for here (vmcnt(0)), where it happens once in many steps: left to its
+    // use, every step would wait for all of its requests in flight
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+  };
+  // A step's keys are two 16-key tiles, each inside one page.  A tile past the end
+  // is read from the last tile instead, and rows past it from the last row
+  // (`row_of`).
+  const int64_t last_tile = (k1 - 1) & ~(int64_t)15;
+  struct Place {
+    int64_t row;    // first row of the tile
+    int left;       // last row of the tile that counts
+    bool lost;      // the page id names no page
+  };
+  auto place = [&](int64_t key) {
+    const int64_t base = key < last_tile ? key : last_tile;
+    const int64_t index = (base >> a.page_shift) - held;
+    const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)index);
+    Place p;
+    p.lost = id >= a.pages;
+    p.row = (((int64_t)(p.lost ? 0u : id) * a.kv_heads + kvh) << a.page_shift) + (base & page_mask);
+    p.left = (int)(k1 - 1 - base < 15 ? k1 - 1 - base : 15);
+    return p;
+  };
+  // Rows past the last one that counts may hold NaN codes, which no weight of 0
+  // takes away; OPQ codes have none.
+  constexpr bool kClamp = FMT != OPQ_CACHE_OPQ4;
+  auto row_of = [](int r, int left) { return (uint32_t)(!kClamp || r < left ? r : left); };
+  KeyTile<FMT, D> kt[2];
+  V vt;
+  floatx4_t ks[2], vs[2];
+  auto load_keys = [&](const Place (&at)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      int64_t base = kk + 16 * u;
-      const int64_t last_tile = (k1 - 1) & ~(int64_t)15;
-      base = base < last_tile ? base : last_tile;
-      const int left = (int)(k1 - 1 - base < 15 ? k1 - 1 - base : 15);  // last row that counts
-      uint32_t page = (uint32_t)table[base >> a.page_shift];
-      const bool lost = page >= a.pages;
-      page = lost ? 0u : page;
-      const int64_t row0 = ((((int64_t)page * a.kv_heads + kvh) << a.page_shift) + (base & page_mask));
-      const int kc = c < left ? c : left;
-      kt[u].load(a.k + (row0 + kc) * kRow,
-                 reinterpret_cast<const char*>(a.k_sign) + (row0 + kc) * (D / 8), g);
+      kt[u].load(a.k + at[u].row * kRow,
+                 reinterpret_cast<const char*>(a.k_sign) + at[u].row * (D / 8),
+                 row_of(c, at[u].left), g);
+      ks[u] = *reinterpret_cast<const floatx4_t*>(a.k_scale + at[u].row + 4 * g);
+    }
+  };
+  auto load_values = [&](const Place (&at)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int vc = 4 * g + i < left ? 4 * g + i : left;
-        vt.load(4 * u + i, a.v + (row0 + vc) * kRow,
-                reinterpret_cast<const char*>(a.v_sign) + (row0 + vc) * (D / 8), c);
+        // unclamped rows differ by a constant from the lane's first
+        const int64_t first = at[u].row + (kClamp ? 0 : i);
+        vt.load(4 * u + i, a.v + first * kRow,
+                reinterpret_cast<const char*>(a.v_sign) + first * (D / 8),
+                kClamp ? row_of(4 * g + i, at[u].left) : 4u * g, c);
       }
-      ks[u] = *reinterpret_cast<const floatx4_t*>(a.k_scale + row0 + 4 * g);
-      vs[u] = *reinterpret_cast<const floatx4_t*>(a.v_scale + row0 + 4 * g);
-      const float sc = lost ? __builtin_nanf("") : a.scale_log2;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ks[u][i] *= sc;
+      vs[u] = *reinterpret_cast<const floatx4_t*>(a.v_scale + at[u].row + 4 * g);
     }
+  };
 
-    floatx4_t st[2][NT];
+  // Software pipeline: a step's keys are requested before the softmax of the step
+  // before it, its values before its own scores.  The requests past the last step
+  // repeat its rows: without a condition around them, the loop waits for nothing
+  // but what it uses.
+  int64_t kk = k0 + wave * kStep;
+  Place at[2];
+  if (kk < k1) {
+    hold(held);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) at[u] = place(kk + 16 * u);
+    load_keys(at);
+  }
+  for (; kk < k1; kk += kRound) {
+    load_values(at);
+    floatx4_t st[2][NT], kscale[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -398,9 +487,22 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
         const bf16x8_t k = kt[u].at(s, lut);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          st[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[n][s], st[u][n], 0, 0, 0);
+          st[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q_at(n, s), st[u][n], 0, 0, 0);
       }
+      const float sc = at[u].lost ? __builtin_nanf("") : a.scale_log2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kscale[u][i] = ks[u][i] * sc;
+      // made here, before the next step's scales are requested: kept for later, the
+      // old and the new scales would change places in registers at the loop's end,
+      // which waits for the new ones
+      asm volatile("" : "+v"(kscale[u]));
     }
+    const int64_t next = kk + kRound;
+    if (((next + 16 < last_tile ? next + 16 : last_tile) >> a.page_shift) - held >= kWave)
+      hold((next < last_tile ? next : last_tile) >> a.page_shift);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) at[u] = place(next + 16 * u);
+    load_keys(at);
 
     // Masks touch only the steps that reach past the cached tokens: bit 4 u + i
     // of `hidden` is the lane's key i of tile u.
@@ -409,57 +511,92 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) hidden[n] = 0u;
     if (masked) {
+      // drafted index of the lane's first key of each tile, and how many of its
+      // four keys there are
+      int j0[2], there[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t key = kk + 16 * u + 4 * g;
+        j0[u] = (int)(key - ex.len < -kStep ? -kStep : key - ex.len);
+        there[u] = (int)clamp64(k1 - key, 0, 4);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const bool counts = token[n] < ex.count;
-        const uint32_t* row =
-            a.mask ? a.mask + (int64_t)b * a.mask_batch + (int64_t)token[n] * a.mask_words : nullptr;
+        uint32_t seen = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t key = kk + 16 * (i >> 2) + 4 * g + (i & 3), j = key - ex.len;
-          bool seen = key < k1 && counts;
-          if (seen && j >= 0) seen = row ? (row[j >> 5] >> (j & 31)) & 1u : j <= token[n];
-          hidden[n] |= seen ? 0u : 1u << i;
+        for (int u = 0; u < 2; ++u) {
+          uint32_t four;
+          if (a.mask) {
+            // the row's bits j0 .. j0 + 3, those before the draft set
+            const uint32_t* row = a.mask + (int64_t)b * a.mask_batch +
+                                  (int64_t)(counts ? token[n] : 0) * a.mask_words;
+            const int last = (int)a.mask_words - 1, j = j0[u] < 0 ? 0 : j0[u];
+            const int w0 = j >> 5 < last ? j >> 5 : last, w1 = w0 < last ? w0 + 1 : last;
+            const uint64_t bits = ((uint64_t)row[w1] << 32 | row[w0]) >> (j & 31);
+            const int before = j - j0[u] < 4 ? j - j0[u] : 4;
+            four = ((uint32_t)bits << before | ((1u << before) - 1u)) & 15u;
+          } else {
+            const int upto = token[n] + 1 - j0[u];  // a chain: j <= token
+            four = (1u << (upto < 0 ? 0 : upto > 4 ? 4 : upto)) - 1u;
+          }
+          four &= (1u << there[u]) - 1u;
+          seen |= four << (4 * u);
         }
+        hidden[n] = counts ? ~seen : 255u;
         // opaque: eight bits in a register, not eight lane masks in scalar ones
         asm volatile("" : "+v"(hidden[n]));
       }
     }
 
+    // No score of the lane's keys exceeds max(acc, 0) * scale_top: while that stays
+    // near the running maximum, the scores themselves are formed only inside
+    // the exponent, one fused multiply-add each.
+    float scale_top = fmaxf(kscale[0][0], kscale[1][0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) scale_top = fmaxf(scale_top, fmaxf(kscale[0][i], kscale[1][i]));
     bf16x8_t p[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float s[8], top = kLowest;
+      float most = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = st[i >> 2][n][i & 3] * ks[i >> 2][i & 3];
-      if (masked) {
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, st[i >> 2][n][i & 3]);
+      if (__builtin_amdgcn_ballot_w64(most * scale_top > m[n] + kSlack)) {
+        float top = kLowest;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = (hidden[n] >> i) & 1u ? -__builtin_inff() : s[i];
+        for (int i = 0; i < 8; ++i) {
+          const float s = st[i >> 2][n][i & 3] * kscale[i >> 2][i & 3];
+          top = fmaxf(top, (hidden[n] >> i) & 1u ? kLowest : s);
+        }
+        if (__builtin_amdgcn_ballot_w64(top > m[n] + kSlack)) {
+          top = fmaxf(top, __shfl_xor(top, 16, kWave));
+          top = fmaxf(top, __shfl_xor(top, 32, kWave));
+          const float raised = fmaxf(m[n], top), f = __builtin_amdgcn_exp2f(m[n] - raised);
+          m[n] = raised;
+          l[n] *= f;
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, s[i]);
-      if (__builtin_amdgcn_ballot_w64(top > m[n] + kSlack)) {
-        top = fmaxf(top, __shfl_xor(top, 16, kWave));
-        top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        const float raised = fmaxf(m[n], top), f = __builtin_amdgcn_exp2f(m[n] - raised);
-        m[n] = raised;
-        l[n] *= f;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
-      }
-      float w[8];
+      float e[8], w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float e = __builtin_amdgcn_exp2f(s[i] - m[n]);
-        l[n] += e;
-        w[i] = e * vs[i >> 2][i & 3];
+        e[i] = __builtin_amdgcn_exp2f(
+            __builtin_fmaf(st[i >> 2][n][i & 3], kscale[i >> 2][i & 3], -m[n]));
+        w[i] = e[i] * vs[i >> 2][i & 3];
       }
-      if (masked) {  // a hidden token's scale may be NaN
+      if (masked) {  // a hidden token may hold anything
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = (hidden[n] >> i) & 1u ? 0.0f : w[i];
+        for (int i = 0; i < 8; ++i) {
+          const bool hide = (hidden[n] >> i) & 1u;
+          e[i] = hide ? 0.0f : e[i];
+          w[i] = hide ? 0.0f : w[i];
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l[n] += e[i];
       p[n] = frag(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]),
                   pack_bf16(w[6], w[7]));
     }
@@ -552,55 +689,83 @@ __global__ __launch_bounds__(kThreads) void attend(AttentionArgs a) {
   }
 }
 
-// Join the pieces of the keys: one wave per row.  Lane i first weighs piece i, then
-// each lane sums dim/64 dimensions over the pieces in order.
-template <int D>
+// Join the pieces of the keys.  A wave holds 256 / D pieces at a time, 16 bytes a
+// lane, and merges them into a running result as the kernel above merges keys; a
+// piece's partial result and its (m, l) are requested together, so nothing waits
+// for a maximum over all pieces first.  kTeam waves share a row (4 where a row has
+// many pieces) and meet in LDS.
+template <int D, int kTeam>
 __global__ __launch_bounds__(kThreads) void join_pieces(AttentionArgs a, int group_rows) {
-  constexpr int kPer = D / kWave;
-  const int lane = threadIdx.x % kWave;
-  const int64_t row = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-  const int64_t all = (int64_t)a.batch * a.kv_heads * a.rows;
-  if (row >= all) return;
-  const int r = (int)(row % a.rows);
-  const int64_t bh = row / a.rows;
-  const int kvh = (int)(bh % a.kv_heads), b = (int)(bh / a.kv_heads);
+  constexpr int kLanes = D / 4, kTogether = kWave / kLanes, kUnroll = 4;
+  const int lane = threadIdx.x % kWave, sub = lane / kLanes, d = (lane % kLanes) * 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int all = a.batch * a.kv_heads * a.rows;  // at most 2^22
+  const int row = (int)blockIdx.x * (kWaves / kTeam) + wave / kTeam;
+  if (row >= all) return;  // all waves of a team
+  const int bh = row / a.rows, r = row - bh * a.rows;
+  const int b = bh / a.kv_heads, kvh = bh - b * a.kv_heads;
   int r_last = (r / group_rows + 1) * group_rows;
   r_last = (r_last < a.rows ? r_last : a.rows) - 1;
   const Extent ex = extent(a, b, r_last);
   if (ex.end <= a.chunk) return;  // one workgroup saw all of it and wrote the result
   const int64_t needed = (ex.end + a.chunk - 1) / a.chunk;
   const int pieces = needed < a.splits ? (int)needed : a.splits;
-  const int t = r / a.share, h = kvh * a.share + (r - t * a.share);
+
   float m = kLowest, l = 0.0f;
-  if (lane < pieces) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (lane * all + row));
-    m = ml.x;
-    l = ml.y;
+  floatx4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto merge = [&](float mi, float li, floatx4_t vi) {
+    const float top = fmaxf(m, mi);
+    const float f = __builtin_amdgcn_exp2f(m - top), fi = __builtin_amdgcn_exp2f(mi - top);
+    m = top;
+    l = l * f + li * fi;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * f + vi[j] * fi;
+  };
+  for (int i0 = wave % kTeam * kTogether; i0 < pieces; i0 += kTeam * kTogether * kUnroll) {
+    float2 ml[kUnroll];
+    floatx4_t po[kUnroll];
+    bool there[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int i = i0 + k * kTeam * kTogether + sub;
+      there[k] = i < pieces;
+      const int64_t at = (int64_t)(there[k] ? i : 0) * all + row;
+      ml[k] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+      po[k] = *reinterpret_cast<const floatx4_t*>(a.part_o + at * D + d);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (there[k]) merge(ml[k].x, ml[k].y, po[k]);
   }
-  const float top = wave_max(m);
-  const float w = __builtin_amdgcn_exp2f(m - top);
-  l *= w;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, kWave);
-  float v[kPer];
+  for (int off = kLanes; off < kWave; off *= 2) {
+    floatx4_t vo;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) v[j] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
-    const float wi = readlane_f(w, i);
-    const float* p = a.part_o + (i * all + row) * D + lane * kPer;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] += p[j] * wi;
+    for (int j = 0; j < 4; ++j) vo[j] = __shfl_xor(v[j], off, kWave);
+    merge(__shfl_xor(m, off, kWave), __shfl_xor(l, off, kWave), vo);
   }
+  if (kTeam > 1) {
+    __shared__ floatx4_t v_all[kTeam][kLanes];
+    __shared__ float m_all[kTeam], l_all[kTeam];
+    if (lane < kLanes) v_all[wave][lane] = v;
+    if (lane == 0) {
+      m_all[wave] = m;
+      l_all[wave] = l;
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 1; w < kTeam; ++w) merge(m_all[w], l_all[w], v_all[w][lane % kLanes]);
+  }
+  if (sub > 0) return;
+  const int t = r / a.share, h = kvh * a.share + (r - t * a.share);
   const bool none = l == 0.0f || t >= ex.count;
   const float inv = none ? 0.0f : 1.0f / l;
   const int64_t at = ((int64_t)b * a.draft + t) * a.heads + h;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    a.out[at * D + lane * kPer + j] =
-        none ? (uint16_t)0 : __builtin_bit_cast(uint16_t, (__bf16)(v[j] * inv));
+  const uint2 w = make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+  *reinterpret_cast<uint2*>(a.out + at * D + d) = none ? make_uint2(0u, 0u) : w;
   if (a.lse && lane == 0)
-    a.lse[at] = none ? -__builtin_inff() : (top + log2f(l)) * 0.69314718055994531f;
+    a.lse[at] = none ? -__builtin_inff() : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int FMT, int D, int NT>
@@ -610,9 +775,15 @@ hipError_t go(const AttentionArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((attend<FMT, D, NT>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
+  // A wave merges 4 x 256 / D pieces in one trip to memory; rows with more, where
+  // rows are few, get a workgroup each.
   const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
-  hipLaunchKernelGGL((join_pieces<D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
-                     dim3(kThreads), 0, stream, a, NT * 16);
+  if (a.splits > 4 * (256 / D) && rows <= 8192)
+    hipLaunchKernelGGL((join_pieces<D, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, stream, a,
+                       NT * 16);
+  else
+    hipLaunchKernelGGL((join_pieces<D, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                       dim3(kThreads), 0, stream, a, NT * 16);
   return hipGetLastError();
 }
 
@@ -620,16 +791,13 @@ template <int FMT>
 hipError_t go_format(const AttentionArgs& a, int dim, int tiles, hipStream_t stream) {
   if (dim == 64) {
     if (tiles == 1) return go<FMT, 64, 1>(a, stream);
-    if (tiles == 2) return go<FMT, 64, 2>(a, stream);
-    return go<FMT, 64, 4>(a, stream);
+    return go<FMT, 64, 2>(a, stream);
   }
   if (dim == 128) {
     if (tiles == 1) return go<FMT, 128, 1>(a, stream);
-    if (tiles == 2) return go<FMT, 128, 2>(a, stream);
-    return go<FMT, 128, 4>(a, stream);
+    return go<FMT, 128, 2>(a, stream);
   }
-  if (tiles == 1) return go<FMT, 256, 1>(a, stream);
-  return go<FMT, 256, 2>(a, stream);
+  return go<FMT, 256, 1>(a, stream);
 }
 
 }  // namespace
@@ -638,13 +806,18 @@ AttentionPlan attention_plan(int64_t batch, int64_t draft, int64_t heads, int64_
                              int64_t dim, int64_t max_len) {
   AttentionPlan p;
   const int64_t rows = draft * (heads / kv_heads);
-  const int most = dim == 256 ? 2 : 4;
-  p.tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
+  const int most = dim == 256 ? 1 : 2;
+  p.tiles = rows <= 16 ? 1 : most;
   p.groups = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
-  // Two workgroups for each of the 256 CUs, and at least one round of keys each.
+  // About 1024 workgroups: four for each of the 256 CUs, so that the last ones
+  // to run are a small part of the whole (32 sequences of up to 8191 tokens: 67 us,
+  // 76 with 512, 69 with 2048).  Pieces of at least 512 keys where that makes 512
+  // workgroups, shorter ones (down to one round) where keys are few.
   const int64_t units = batch * kv_heads * p.groups, keys = max_len + draft;
-  int64_t splits = (512 + units - 1) / units;
-  const int64_t rounds = (keys + kRound - 1) / kRound;
+  const int64_t rounds = (keys + kRound - 1) / kRound, half = (512 + units - 1) / units;
+  int64_t splits = (1024 + units - 1) / units, most_long = (rounds + 3) / 4;
+  most_long = most_long > half ? most_long : half;
+  splits = splits < most_long ? splits : most_long;
   splits = splits < rounds ? splits : rounds;
   splits = splits < 64 ? splits : 64;
   splits = splits < 1 ? 1 : splits;

@@ -87,7 +87,8 @@ struct AttentionArgs {
   int64_t mask_batch, mask_words, max_pages, capacity, chunk;
   uint32_t pages;
   int page_shift, batch, draft, heads, kv_heads, share, rows, splits, groups;
-  float scale_log2;  // scale * log2(e)
+  float scale_log2;  // |scale| * log2(e)
+  uint32_t q_flip;   // sign bits of two bfloat16: set for a negative scale
   uint16_t* out;
   float* lse;
   float* part_o;   // [splits][batch][kv_heads][rows][dim]
