@@ -2,10 +2,12 @@
 positions, a paged key/value cache quantized as it is written, and attention of
 drafted tokens (one, or a tree of them, per sequence) over that cache.
 
-As in ``opq``, this module checks tensors, allocates outputs with torch on the
-caller's device and passes raw pointers plus the current torch stream; every step
-runs in the library's HIP kernels.  Workspaces come from torch's allocator per
-call, so calls on different streams do not share one.
+As in ``opq``, tensors are checked, outputs are allocated with torch on the
+caller's device, and raw pointers go to the library with the current torch stream;
+every step runs in its HIP kernels.  For the calls of a decode step, where Python
+would take longer than the GPU, this is done in C++ (csrc/attention_torch.cpp, built
+as _attention.so).  Workspaces come from torch's allocator per call, so calls on
+different streams do not share one.
 
     table = rotary_table(rotary_frequencies(128, 1e6), 32768, "cuda")
     cache = new_cache(pages=1024, heads=8, page=64, dim=128, fmt="opq4", device="cuda")
@@ -16,7 +18,6 @@ call, so calls on different streams do not share one.
 from __future__ import annotations
 
 import ctypes
-from functools import lru_cache
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import numpy as np
@@ -54,65 +55,33 @@ class _CCache(ctypes.Structure):
 
 
 _ready: Optional[ctypes.CDLL] = None
+_ext = None
 
 
 def load() -> ctypes.CDLL:
-    """libopq.so with the attention side's signatures set."""
-    global _ready
+    """libopq.so with the attention side's signatures set, and the extension that takes
+    tensors to it; raises if either is missing."""
+    global _ready, _ext
     if _ready is None:
         lib = opq.load()
         for name, (res, args) in _SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+        try:
+            from . import _attention
+        except ImportError as e:
+            raise RuntimeError("_attention.so not built: run `python -m w4a16_linear_amd.build`") from e
+        _attention.set_error(opq.OpqError)
+        _ext = _attention
         _ready = lib
     return _ready
 
 
-def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...]) -> int:
-    """Checks a dense device tensor of a known shape; returns its address."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _need_rows(name: str, t: torch.Tensor, ndim: int, like: Optional[torch.device] = None) -> None:
-    """Checks a device tensor whose last dimension is dense; other strides are free."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be {ndim}-d with a dense last dimension")
-    if like is not None and t.device != like:
-        raise ValueError(f"{name} must be on {like}, got {t.device}")
-
-
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-
-
-class _on:
-    """The library launches on the current device: make it the tensors' one."""
-
-    __slots__ = ("dev", "old")
-
-    def __init__(self, dev: torch.device):
-        self.dev = dev.index
-
-    def __enter__(self) -> int:
-        self.old = torch.cuda.current_device()
-        if self.old != self.dev:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc) -> None:
-        if self.old != self.dev:
-            torch.cuda.set_device(self.old)
+def _calls():
+    if _ext is None:
+        load()
+    return _ext
 
 
 # ------------------------------------------------------------------ rotary
@@ -150,7 +119,8 @@ def rotary_table(frequencies, length: int, device, amplitude: Optional[float] = 
     if f.dim() != 1 or not f.is_cuda:
         raise ValueError("frequencies must be one row, and device a CUDA (HIP) device")
     table = torch.empty((length, f.numel(), 2), dtype=torch.float32, device=f.device)
-    with _on(f.device) as stream:
+    with torch.cuda.device(f.device):
+        stream = torch.cuda.current_stream(f.device).cuda_stream
         _check("opq_rotary_table",
                load().opq_rotary_table(f.data_ptr(), f.numel(), length,
                                        1.0 if amplitude is None else amplitude, table.data_ptr(),
@@ -158,41 +128,11 @@ def rotary_table(frequencies, length: int, device, amplitude: Optional[float] = 
     return table
 
 
-@lru_cache(maxsize=64)
-def _sections(sections: Tuple[int, ...]):
-    return (ctypes.c_int32 * len(sections))(*sections)
-
-
 def _rotary(x, positions, table, layout, sections, out, backward):
-    if layout not in LAYOUTS:
+    code = LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {list(LAYOUTS)}, got {layout!r}")
-    _need_rows("x", x, 3)
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
-    tokens, heads, dim = x.shape
-    if table.dim() != 3:
-        raise ValueError("table must be [length, pairs, 2]")
-    pairs = table.shape[1]
-    pt = _need("table", table, torch.float32, (table.shape[0], pairs, 2))
-    sections = (pairs,) if sections is None else tuple(sections)
-    axes = len(sections)
-    if positions.dim() == 1 and axes == 1:
-        positions = positions.unsqueeze(1)
-    pp = _need("positions", positions, torch.int32, (tokens, axes))
-    if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
-    else:
-        _need_rows("out", out, 3)
-        if out.shape != x.shape or out.dtype != x.dtype:
-            raise ValueError(f"out must be {x.dtype} of shape {tuple(x.shape)}")
-    _same_device(x.device, positions=positions, table=table, out=out)
-    xs, os = x.stride(), out.stride()
-    with _on(x.device) as stream:
-        st = load().opq_rotary(x.data_ptr(), _DTYPES[x.dtype], tokens, heads, dim, xs[0], xs[1], pp,
-                               axes, _sections(sections), pt, table.shape[0], 2 * pairs,
-                               LAYOUTS[layout], backward, out.data_ptr(), os[0], os[1], stream)
-    _check("opq_rotary", st)
-    return out
+    return (_ext or _calls()).rotary(x, positions, table, code, sections, out, backward)
 
 
 def rotary(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: str = "half",
@@ -290,50 +230,10 @@ def new_cache(pages: int, heads: int, page: int, dim: int, fmt: str = "fp8", alp
     return PagedCache(fmt, alpha, *side(), *side())
 
 
-def _c_cache(cache: PagedCache) -> _CCache:
-    fmt = cache.fmt
-    if fmt not in FORMATS:
-        raise ValueError(f"fmt must be one of {list(FORMATS)}, got {fmt!r}")
-    if cache.k.dim() != 4:
-        raise ValueError("cache codes must be [pages, heads, page, ...]")
-    pages, heads, page, words = cache.k.shape
-    dt = _CODE_TYPES[fmt]
-    shape, rows = (pages, heads, page, words), (pages, heads, page)
-    ks = vs = None
-    dim = words
-    if fmt == "opq4":
-        dim = 8 * words
-        signs = (pages, heads, page, dim // 32)
-        ks = _need("k_sign", cache.k_sign, torch.int32, signs)
-        vs = _need("v_sign", cache.v_sign, torch.int32, signs)
-        _same_device(cache.k.device, k_sign=cache.k_sign, v_sign=cache.v_sign)
-    _same_device(cache.k.device, k_scale=cache.k_scale, v=cache.v, v_scale=cache.v_scale)
-    return _CCache(_need("k", cache.k, dt, shape), ks,
-                   _need("k_scale", cache.k_scale, torch.float32, rows),
-                   _need("v", cache.v, dt, shape), vs,
-                   _need("v_scale", cache.v_scale, torch.float32, rows),
-                   pages, heads, page, dim, FORMATS[fmt], cache.alpha)
-
-
 def cache_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantize k, v [tokens, heads, dim] (float32 or bfloat16; token and head
     strides free) into the rows of `slots` (int32 [tokens]; -1 skips a token)."""
-    cc = _c_cache(cache)
-    _need_rows("k", k, 3, cache.device)
-    _need_rows("v", v, 3, cache.device)
-    tokens = k.shape[0]
-    if k.dtype not in _DTYPES or v.dtype != k.dtype:
-        raise ValueError(f"k and v must both be float32 or bfloat16, got {k.dtype} and {v.dtype}")
-    if k.shape != v.shape or tuple(k.shape[1:]) != (cc.heads, cc.dim):
-        raise ValueError(f"k and v must be [tokens, {cc.heads}, {cc.dim}], got {tuple(k.shape)} "
-                         f"and {tuple(v.shape)}")
-    sp = _need("slots", slots, torch.int32, (tokens,))
-    _same_device(cache.device, slots=slots)
-    a, b = k.stride(), v.stride()
-    with _on(cache.device) as stream:
-        st = load().opq_cache_write(ctypes.byref(cc), k.data_ptr(), a[0], a[1], v.data_ptr(), b[0],
-                                    b[1], _DTYPES[k.dtype], tokens, sp, stream)
-    _check("opq_cache_write", st)
+    (_ext or _calls()).cache_write(cache, k, v, slots)
 
 
 def cache_read(cache: PagedCache, slots: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
@@ -341,22 +241,11 @@ def cache_read(cache: PagedCache, slots: torch.Tensor, out_dtype: torch.dtype = 
                ) -> Tuple[torch.Tensor, torch.Tensor]:
     """(k, v) [tokens, heads, dim] of the rows of `slots` (int32 [tokens]; -1
     gives zeros), as bfloat16 or float32."""
-    cc = _c_cache(cache)
-    if out_dtype not in _DTYPES:
+    dtype = _DTYPES.get(out_dtype)
+    if dtype is None:
         raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-    if slots.dim() != 1:
-        raise ValueError("slots must be [tokens]")
-    shape = (slots.shape[0], cc.heads, cc.dim)
-    sp = _need("slots", slots, torch.int32, shape[:1])
-    if out is None:
-        out = (torch.empty(shape, dtype=out_dtype, device=cache.device),
-               torch.empty(shape, dtype=out_dtype, device=cache.device))
-    kp, vp = _need("out[0]", out[0], out_dtype, shape), _need("out[1]", out[1], out_dtype, shape)
-    _same_device(cache.device, slots=slots, k_out=out[0], v_out=out[1])
-    with _on(cache.device) as stream:
-        st = load().opq_cache_read(ctypes.byref(cc), shape[0], sp, kp, vp, _DTYPES[out_dtype], stream)
-    _check("opq_cache_read", st)
-    return out[0], out[1]
+    k, v = (None, None) if out is None else out
+    return (_ext or _calls()).cache_read(cache, slots, dtype, k, v)
 
 
 # --------------------------------------------------------------- attention
@@ -385,52 +274,8 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
     holds less the draft).  Returns bfloat16 [batch, draft, heads, dim], with
     return_lse also float32 [batch, draft, heads].
     """
-    cc = _c_cache(cache)
-    dev = cache.device
-    _need_rows("q", q, 4, dev)
-    if q.dtype != torch.bfloat16:
-        raise ValueError(f"q must be bfloat16, got {q.dtype}")
-    batch, draft, heads, dim = q.shape
-    if dim != cc.dim or heads % cc.heads:
-        raise ValueError(f"q has {heads} heads of {dim}, the cache {cc.heads} of {cc.dim}")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [batch, max_pages]")
-    max_pages = page_table.shape[1]
-    tp = _need("page_table", page_table, torch.int32, (batch, max_pages))
-    lp = _need("lens", lens, torch.int32, (batch,))
-    mp, mask_batch = None, 0
-    if mask is not None:
-        words = (draft + 31) // 32
-        mask_batch = draft * words if mask.dim() == 3 else 0
-        mp = _need("mask", mask, torch.int32,
-                   (batch, draft, words) if mask.dim() == 3 else (draft, words))
-    cp = None if counts is None else _need("counts", counts, torch.int32, (batch,))
-    _same_device(dev, page_table=page_table, lens=lens, mask=mask, counts=counts)
-    if max_len is None:
-        max_len = max(0, max_pages * cc.page - draft)
-    if out is None:
-        out = torch.empty((batch, draft, heads, dim), dtype=torch.bfloat16, device=dev)
-    else:
-        _need("out", out, torch.bfloat16, (batch, draft, heads, dim))
-        _same_device(dev, out=out)
-    lse = torch.empty((batch, draft, heads), dtype=torch.float32, device=dev) if return_lse else None
-    lib = load()
-    need = lib.opq_cache_attention_workspace_bytes(batch, draft, heads, cc.heads, dim, max_len)
-    if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    s = q.stride()
-    with _on(dev) as stream:
-        st = lib.opq_cache_attention(
-            ctypes.byref(cc), q.data_ptr(), batch, draft, heads, s[0], s[1], s[2], tp, max_pages, lp,
-            cp, max_len, mp, mask_batch, dim ** -0.5 if scale is None else scale, out.data_ptr(),
-            None if lse is None else lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
-    _check("opq_cache_attention", st)
-    return (out, lse) if return_lse else out
+    return (_ext or _calls()).attention(q, cache, page_table, lens, mask, counts, scale, max_len, out,
+                                        return_lse, workspace)
 
 
 def tree_mask(parents: torch.Tensor) -> torch.Tensor:

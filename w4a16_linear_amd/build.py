@@ -5,7 +5,8 @@
 HIP sources are compiled for gfx950 only, without fast-math (the quantizer
 relies on correctly rounded binary32 division and kept subnormals) and with
 packed fp32 instructions disabled.  Host-only C++ (the ABI layer and the
-binary128 table code, which needs libquadmath) is compiled with g++.
+binary128 table code, which needs libquadmath) is compiled with g++, as is the
+extension that takes torch tensors to the attention side (_attention.so).
 """
 from __future__ import annotations
 
@@ -27,6 +28,9 @@ CEILING_LIB = os.path.join(HERE, "libopq_ceiling.so")
 SOURCES = ["opq_api.cpp", "tables.cpp", "quantize.hip", "dequantize.hip", "linear.hip",
            "attention_api.cpp", "rotary.hip", "cache.hip", "attention.hip"]
 CEILING_SOURCES = ["stream_ceiling.hip"]
+# the attention side's calls on torch tensors, a CPython extension over libopq.so
+EXT_SOURCE = "attention_torch.cpp"
+EXT_LIB = os.path.join(HERE, "_attention.so")
 ARCH = "gfx950"
 
 
@@ -86,15 +90,59 @@ def _link(objs, lib: str, libs, verbose: bool) -> None:
     os.replace(tmp, lib)
 
 
+def _compile_extension(verbose: bool) -> str:
+    import sysconfig
+
+    import torch
+
+    here = os.path.dirname(torch.__file__)
+    obj = os.path.join(OBJDIR, EXT_SOURCE + ".o")
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-DNDEBUG", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE, "-I", CSRC,
+           "-isystem", os.path.join(here, "include"),
+           "-isystem", os.path.join(here, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
+           "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {EXT_SOURCE}\n{r.stdout}{r.stderr}")
+    return obj
+
+
+def _link_extension(obj: str, verbose: bool) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT_LIB + ".tmp"
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    # torch's libraries are loaded by `import torch`; libopq.so lies beside the extension
+    cmd = [cxx, "-shared", "-fPIC", "-o", tmp, obj, "-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", "-L", HERE, "-l:libopq.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed\n" + r.stdout + r.stderr)
+    os.replace(tmp, EXT_LIB)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source, link libopq.so and libopq_ceiling.so; returns the
-    path of libopq.so."""
+    """Compile every source, link libopq.so, libopq_ceiling.so and the torch
+    extension; returns the path of libopq.so."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = SOURCES + CEILING_SOURCES
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        ext = ex.submit(_compile_extension, verbose)
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
+        ext_obj = ext.result()
     _link([objs[s] for s in SOURCES], LIB, ["-lquadmath"], verbose)
     _link([objs[s] for s in CEILING_SOURCES], CEILING_LIB, [], verbose)
+    _link_extension(ext_obj, verbose)
     return LIB
 
 
