@@ -190,8 +190,10 @@ int opq_cache_write(const opq_cache* cache, const void* k, int64_t k_token_strid
     if (!opq::decision_points(c.alpha, cc.t)) return OPQ_ERR_ALPHA;
     cc.alpha = c.alpha;
     // Error of 15 u^alpha through log2 and exp2 in binary32: at most about
-    // 5e-6 + 8e-6 alpha (one ulp each, 3 ulps of |x| fl(1/m)); twice that and more.
-    cc.guard = 1e-4f + 2e-5f * c.alpha;
+    // 8e-6 + 8e-6 alpha (an ulp each of log2, its product with alpha, exp2 and the
+    // final sum, 3 ulps of |x| fl(1/m)).  The guard is three times that: it decides
+    // how many elements take the slow way (5 % of the waves for alpha = 0.73).
+    cc.guard = 3e-5f + 2.5e-5f * c.alpha;
   }
   const opq::CacheRows side[2] = {{k, k_token_stride, k_head_stride, c.k, c.k_sign, c.k_scale},
                                   {v, v_token_stride, v_head_stride, c.v, c.v_sign, c.v_scale}};

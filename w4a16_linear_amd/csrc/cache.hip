@@ -24,6 +24,7 @@ constexpr float kSmallest = 0x1p-100f;  // rows below it are stored as zeros
 
 typedef float floatx2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const floatx2_t f = {a, b};
@@ -32,34 +33,65 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Eight values of a row; `wide` when their address is a multiple of 16 bytes.
-__device__ __forceinline__ void load8(const uint16_t* p, bool wide, float (&x)[8]) {
+// Eight raw values of a row.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
   uint32_t w[4];
-  if (wide) {
-    const u32x4_t v = load_stream16(p);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  } else {
+  // `wide`: p is a multiple of 16 bytes
+  __device__ __forceinline__ void load(const uint16_t* p, bool wide) {
+    if (wide) {
+      const u32x4_t v = load_stream16(p);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+    }
   }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = low_half(w[i]);
-    x[2 * i + 1] = high_half(w[i]);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = low_half(w[i]);
+      x[2 * i + 1] = high_half(w[i]);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, bool wide, float (&x)[8]) {
-  if (wide) {
-    const u32x4_t a = load_stream16(p), b = load_stream16(p + 4);
-    x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y);
-    x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
-    x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y);
-    x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
-  } else {
+  // bits of the largest magnitude, as binary32 (NaN above infinity above the rest)
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p[i];
+    for (int i = 0; i < 4; ++i)
+      t = __builtin_bit_cast(uint32_t,
+                             __builtin_elementwise_max(
+                                 __builtin_bit_cast(u16x2_t, t),
+                                 __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu)));
+    return max(t << 16, t & 0xFFFF0000u);
   }
-}
+};
+template <>
+struct Eight<float> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* p, bool wide) {
+    if (wide) {
+      const u32x4_t a = load_stream16(p), b = load_stream16(p + 4);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(p[i]);
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, w[i] & 0x7FFFFFFFu);
+    return t;
+  }
+};
 
 // Largest of v over each group of kLanes (8, 16 or 32) lanes, in every lane of
 // it.  Within four lanes by quad permutes; then the mirrored halves of eight and
@@ -84,23 +116,30 @@ __device__ uint32_t code_exact(float a, float m, const CacheCodes& cc) {
   return q;
 }
 
-// Nibbles of eight magnitudes.  The power comes from the hardware's log2 and exp2
-// on |x| * fl(1/m): its error is far below cc.guard, so a result farther than
-// that from a half-integer rounds to the exact code, and the few others (and
-// every row whose 1/m is not a normal number) are decided by code_exact.
+// Nibbles of eight magnitudes.  15 u^alpha comes from the hardware's log2 and exp2
+// on |x| * fl(1/m): its error is far below cc.guard, so the nearest integer is the
+// exact code unless a half-integer is within the guard; those few (and every row
+// whose 1/m is not a normal number) are decided by code_exact.
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float m, const CacheCodes& cc) {
+  constexpr float kLog15 = 3.90689059560851853f;
   const float r = __builtin_amdgcn_rcpf(m);
   uint32_t word = 0u;
-  bool sure = r >= 0x1p-126f;
+  float low = 1.0f, high = 0.0f;  // of the distances above the half-integer below
+  auto code = [&](float v, float& f) {
+    const float lg = __builtin_amdgcn_logf(fabsf(v) * r);
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(cc.alpha, lg, kLog15)) + 0.5f;
+    f = __builtin_amdgcn_fractf(p);
+    return (uint32_t)p;
+  };
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float lg = __builtin_amdgcn_logf(fabsf(x[i]) * r);
-    const float p = fminf(15.0f * __builtin_amdgcn_exp2f(cc.alpha * lg), 15.0f);
-    const float n = __builtin_rintf(p);
-    sure = sure && fabsf(p - n) < 0.5f - cc.guard;
-    word = (word << 4) + (uint32_t)n;
+  for (int i = 7; i >= 0; i -= 2) {
+    float f0, f1;
+    word = (word << 4) + code(x[i], f0);
+    word = (word << 4) + code(x[i - 1], f1);
+    low = fminf(low, fminf(f0, f1));
+    high = fmaxf(high, fmaxf(f0, f1));
   }
-  if (!sure) {
+  if (!(low > cc.guard && high < 1.0f - cc.guard && r >= 0x1p-126f)) {
     word = 0u;
 #pragma unroll 1
     for (int i = 7; i >= 0; --i) {
@@ -113,34 +152,32 @@ __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float m, const 
   return word;
 }
 
+// x / s, correctly rounded, from ri = fl(1/s): q = fl(x ri) is within an ulp, its
+// remainder x - q s is exact in a fused multiply-add, and fl(q + rem ri) is then the
+// rounded quotient (Markstein's theorem; it needs s's significand not to be all
+// ones, and no underflow, which only quotients far below the smallest code have).
+__device__ __forceinline__ float quotient(float x, float s, float ri) {
+  const float q = x * ri;
+  return __builtin_fmaf(__builtin_fmaf(-q, s, x), ri, q);
+}
+
 struct WriteArgs {
   CacheRows side[2];
   const int32_t* slots;
-  uint32_t rows;  // tokens * heads of this launch
+  uint32_t tokens;  // of this launch
   uint32_t heads;
   uint32_t slot_end;  // pages * page
   int page_shift;
   bool wide;
 };
 
-// Row (token, head) of keys (blockIdx.y = 0) or values (1).
+// One row: eight values a lane; `at` is its place in the cache.
 template <typename T, int FMT, int D>
-__global__ __launch_bounds__(kThreads) void write_rows(WriteArgs a, CacheCodes cc) {
+__device__ __forceinline__ void write_row(const Eight<T>& raw, const CacheRows& s, int64_t at,
+                                          int lane, const CacheCodes& cc) {
   constexpr int kLanes = D / 8;
-  const uint32_t row = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  if (row >= a.rows) return;  // whole groups of lanes
-  const uint32_t token = row / a.heads, head = row - token * a.heads;
-  const uint32_t slot = (uint32_t)a.slots[token];
-  if (slot >= a.slot_end) return;  // -1 among them
-  const CacheRows s = blockIdx.y ? a.side[1] : a.side[0];
   float x[8];
-  load8(static_cast<const T*>(s.x) + token * s.token_stride + head * s.head_stride + lane * 8,
-        a.wide, x);
-  const uint32_t page = slot >> a.page_shift;
-  const int64_t at = ((((int64_t)page * a.heads + head) << a.page_shift) +
-                      (slot & ((1u << a.page_shift) - 1u)));
-
+  raw.values(x);
   if (FMT == OPQ_CACHE_BF16) {
     uint32_t w[4], top = 0u;
 #pragma unroll
@@ -154,27 +191,30 @@ __global__ __launch_bounds__(kThreads) void write_rows(WriteArgs a, CacheCodes c
     if (lane == 0) s.scale[at] = bad ? __builtin_nanf("") : 1.0f;
     return;
   }
-  uint32_t top = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = group_max<kLanes>(top);
+  const uint32_t top = group_max<kLanes>(raw.top());
   const bool bad = top >= 0x7F800000u;
   const float m = __uint_as_float(top);
   const bool zero = !bad && m < kSmallest;
-  if (bad || zero) {
+  if (__builtin_amdgcn_ballot_w64(bad || zero)) {  // rare: no selects on every row's way
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) x[i] = bad || zero ? 0.0f : x[i];
   }
   const float mm = bad || zero ? 1.0f : m;  // what the codes are taken against
   if (FMT == OPQ_CACHE_FP8) {
-    const float sc = mm / 448.0f;
+    const float sc = mm / 448.0f, ri = 1.0f / sc;
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(x[i] / sc, -448.0f, 448.0f);
+    for (int i = 0; i < 8; ++i) y[i] = quotient(x[i], sc, ri);
+    if ((__float_as_uint(sc) & 0x7FFFFFu) == 0x7FFFFFu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = x[i] / sc;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(y[i], -448.0f, 448.0f);
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+      const int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
       w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], v, true);
     }
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.codes) + at * D + lane * 8) =
@@ -182,17 +222,42 @@ __global__ __launch_bounds__(kThreads) void write_rows(WriteArgs a, CacheCodes c
     if (lane == 0) s.scale[at] = bad ? __builtin_nanf("") : zero ? 0.0f : sc;
     return;
   }
-  const uint32_t word = encode8(x, mm, cc);
-  static_cast<uint32_t*>(s.codes)[at * (D / 8) + lane] = word;
+  static_cast<uint32_t*>(s.codes)[at * (D / 8) + lane] = encode8(x, mm, cc);
   uint32_t sb = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sb |= (x[i] < 0.0f ? 1u : 0u) << i;
+  for (int i = 7; i >= 0; --i) sb = sb + sb + (x[i] < 0.0f ? 1u : 0u);
   uint32_t s32 = sb << (8 * (lane & 3));
   // OR over each group of four lanes (quad permutes 1,0,3,2 and 2,3,0,1)
   s32 |= (uint32_t)__builtin_amdgcn_mov_dpp((int)s32, 0xB1, 0xF, 0xF, false);
   s32 |= (uint32_t)__builtin_amdgcn_mov_dpp((int)s32, 0x4E, 0xF, 0xF, false);
   if ((lane & 3) == 0) s.sign[at * (D / 32) + (lane >> 2)] = s32;
   if (lane == 0) s.scale[at] = bad ? __builtin_nanf("") : zero ? 0.0f : m;
+}
+
+// A group of dim/8 lanes: HPT heads of one token, of keys (blockIdx.y = 0) or
+// values (1).
+template <typename T, int FMT, int D, int HPT>
+__global__ __launch_bounds__(kThreads) void write_rows(WriteArgs a, CacheCodes cc) {
+  constexpr int kLanes = D / 8;
+  const uint32_t group = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const uint32_t per = (a.heads + HPT - 1) / HPT, token = group / per;
+  if (token >= a.tokens) return;  // whole groups of lanes
+  const uint32_t head = (group - token * per) * HPT;
+  const uint32_t slot = (uint32_t)a.slots[token];
+  const CacheRows s = blockIdx.y ? a.side[1] : a.side[0];
+  const T* x = static_cast<const T*>(s.x) + token * s.token_stride + lane * 8;
+  Eight<T> raw[HPT];
+#pragma unroll
+  for (int h = 0; h < HPT; ++h)
+    if (head + h < a.heads) raw[h].load(x + (int64_t)(head + h) * s.head_stride, a.wide);
+  if (slot >= a.slot_end) return;  // -1 among them
+  const int64_t row0 = (int64_t)(slot >> a.page_shift) * a.heads + head;
+  const uint32_t in_page = slot & ((1u << a.page_shift) - 1u);
+#pragma unroll
+  for (int h = 0; h < HPT; ++h)
+    if (head + h < a.heads)
+      write_row<T, FMT, D>(raw[h], s, ((row0 + h) << a.page_shift) + in_page, lane, cc);
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
@@ -209,62 +274,90 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 struct ReadArgs {
   CacheRows side[2];  // x: the output
   const int32_t* slots;
-  uint32_t rows, heads, slot_end;
+  uint32_t tokens, heads, slot_end;
   int page_shift;
 };
 
-template <typename T, int FMT, int D>
-__global__ __launch_bounds__(kThreads) void read_rows(ReadArgs a, LevelPlanes lp) {
-  constexpr int kLanes = D / 8;
-  const uint32_t row = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  if (row >= a.rows) return;
-  const uint32_t token = row / a.heads, head = row - token * a.heads;
-  const uint32_t slot = (uint32_t)a.slots[token];
-  const CacheRows s = blockIdx.y ? a.side[1] : a.side[0];
-  T* out = static_cast<T*>(const_cast<void*>(s.x)) + (int64_t)row * D + lane * 8;
-  float v[8];
-  if (slot >= a.slot_end) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    store8(out, v);
-    return;
-  }
-  const uint32_t page = slot >> a.page_shift;
-  const int64_t at = ((((int64_t)page * a.heads + head) << a.page_shift) +
-                      (slot & ((1u << a.page_shift) - 1u)));
-  const float sc = s.scale[at];
-  if (FMT == OPQ_CACHE_FP8) {
-    const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.codes) + at * D +
-                                                    lane * 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const floatx2_t f = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)(i < 2 ? c.x : c.y), true)
-                                  : __builtin_amdgcn_cvt_pk_f32_fp8((int)(i < 2 ? c.x : c.y), false);
-      v[2 * i] = f.x * sc;
-      v[2 * i + 1] = f.y * sc;
-    }
-  } else {
-    uint32_t w[4];
-    if (FMT == OPQ_CACHE_BF16) {
+// One lane's stored part of a row.
+template <int FMT, int D>
+struct Stored {
+  uint32_t w[FMT == OPQ_CACHE_BF16 ? 4 : 2];  // OPQ: code word and sign byte
+  float scale;
+  __device__ __forceinline__ void load(const CacheRows& s, int64_t at, int lane) {
+    scale = s.scale[at];
+    if constexpr (FMT == OPQ_CACHE_BF16) {
       const u32x4_t c = *reinterpret_cast<const u32x4_t*>(
           static_cast<const uint16_t*>(s.codes) + at * D + lane * 8);
       w[0] = c.x; w[1] = c.y; w[2] = c.z; w[3] = c.w;
+    } else if constexpr (FMT == OPQ_CACHE_FP8) {
+      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.codes) +
+                                                      at * D + lane * 8);
+      w[0] = c.x; w[1] = c.y;
     } else {
-      const uint32_t code = static_cast<const uint32_t*>(s.codes)[at * (D / 8) + lane];
-      const uint32_t sb = reinterpret_cast<const uint8_t*>(s.sign + at * (D / 32))[lane];
-      RowLut t;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { t.lo[i] = lp.lo[i]; t.hi[i] = lp.hi[i]; }
-      decode_word_split(code, sb, t, w);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = low_half(w[i]) * sc;
-      v[2 * i + 1] = high_half(w[i]) * sc;
+      w[0] = static_cast<const uint32_t*>(s.codes)[at * (D / 8) + lane];
+      w[1] = reinterpret_cast<const uint8_t*>(s.sign + at * (D / 32))[lane];
     }
   }
-  store8(out, v);
+  __device__ __forceinline__ void values(const RowLut& lut, float (&v)[8]) const {
+    if constexpr (FMT == OPQ_CACHE_FP8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const floatx2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+        const floatx2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        v[4 * i] = a.x * scale;
+        v[4 * i + 1] = a.y * scale;
+        v[4 * i + 2] = b.x * scale;
+        v[4 * i + 3] = b.y * scale;
+      }
+    } else {
+      uint32_t o[4];
+      if constexpr (FMT == OPQ_CACHE_BF16) {
+        o[0] = w[0]; o[1] = w[1]; o[2] = w[2]; o[3] = w[3];
+      } else {
+        decode_word_split(w[0], w[1], lut, o);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = low_half(o[i]) * scale;
+        v[2 * i + 1] = high_half(o[i]) * scale;
+      }
+    }
+  }
+};
+
+template <typename T, int FMT, int D, int HPT>
+__global__ __launch_bounds__(kThreads) void read_rows(ReadArgs a, LevelPlanes lp) {
+  constexpr int kLanes = D / 8;
+  const uint32_t group = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const uint32_t per = (a.heads + HPT - 1) / HPT, token = group / per;
+  if (token >= a.tokens) return;
+  const uint32_t head = (group - token * per) * HPT;
+  const uint32_t slot = (uint32_t)a.slots[token];
+  const CacheRows s = blockIdx.y ? a.side[1] : a.side[0];
+  T* out = static_cast<T*>(const_cast<void*>(s.x)) + ((int64_t)token * a.heads + head) * D + lane * 8;
+  const bool there = slot < a.slot_end;
+  const int64_t row0 = (int64_t)(slot >> a.page_shift) * a.heads + head;
+  const uint32_t in_page = slot & ((1u << a.page_shift) - 1u);
+  Stored<FMT, D> row[HPT];
+#pragma unroll
+  for (int h = 0; h < HPT; ++h)
+    if (there && head + h < a.heads) row[h].load(s, ((row0 + h) << a.page_shift) + in_page, lane);
+  RowLut lut;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { lut.lo[i] = lp.lo[i]; lut.hi[i] = lp.hi[i]; }
+#pragma unroll
+  for (int h = 0; h < HPT; ++h)
+    if (head + h < a.heads) {
+      float v[8];
+      if (there) {
+        row[h].values(lut, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      }
+      store8(out + h * D, v);
+    }
 }
 
 int page_shift_of(int64_t page) {
@@ -273,10 +366,12 @@ int page_shift_of(int64_t page) {
   return s;
 }
 
-// Whole tokens per launch, so that its work-items count below 2^31.
-template <typename F>
+// Several heads to a group of lanes share one look at the token's slot and keep that
+// many requests in flight; with few rows a head each spreads the launch wider.
+template <int HPT, typename F>
 hipError_t in_launches(const opq_cache& c, int64_t tokens, F one) {
-  const int64_t per = c.heads * (c.dim / 8);
+  // whole tokens per launch, so that its work-items count below 2^31
+  const int64_t per = (c.heads + HPT - 1) / HPT * (c.dim / 8);
   const int64_t step = (kMaxLaunchThreads - kThreads) / per;
   for (int64_t t0 = 0; t0 < tokens; t0 += step) {
     const int64_t n = tokens - t0 < step ? tokens - t0 : step;
@@ -286,8 +381,11 @@ hipError_t in_launches(const opq_cache& c, int64_t tokens, F one) {
   }
   return hipSuccess;
 }
+bool many_rows(const opq_cache& c, int64_t tokens) {
+  return tokens * c.heads * (c.dim / 8) >= int64_t(1) << 19;
+}
 
-template <typename T, int FMT, int D>
+template <typename T, int FMT, int D, int HPT>
 hipError_t write_all(const CacheRows (&side)[2], const opq_cache& c, int64_t tokens,
                      const int32_t* slots, const CacheCodes& cc, hipStream_t stream) {
   bool wide = true;
@@ -295,37 +393,50 @@ hipError_t write_all(const CacheRows (&side)[2], const opq_cache& c, int64_t tok
     wide = wide && reinterpret_cast<uintptr_t>(s.x) % 16 == 0 &&
            s.token_stride % (int64_t)(16 / sizeof(T)) == 0 &&
            s.head_stride % (int64_t)(16 / sizeof(T)) == 0;
-  return in_launches(c, tokens, [&](int64_t t0, int64_t n, dim3 grid) {
-    WriteArgs a{{side[0], side[1]}, slots + t0, (uint32_t)(n * c.heads), (uint32_t)c.heads,
+  return in_launches<HPT>(c, tokens, [&](int64_t t0, int64_t n, dim3 grid) {
+    WriteArgs a{{side[0], side[1]}, slots + t0, (uint32_t)n, (uint32_t)c.heads,
                 (uint32_t)(c.pages * c.page), page_shift_of(c.page), wide};
     for (CacheRows& s : a.side) s.x = static_cast<const T*>(s.x) + t0 * s.token_stride;
-    hipLaunchKernelGGL((write_rows<T, FMT, D>), grid, dim3(kThreads), 0, stream, a, cc);
+    hipLaunchKernelGGL((write_rows<T, FMT, D, HPT>), grid, dim3(kThreads), 0, stream, a, cc);
   });
 }
 
-template <typename T, int FMT, int D>
+template <typename T, int FMT, int D, int HPT>
 hipError_t read_all(const CacheRows (&side)[2], const opq_cache& c, int64_t tokens,
                     const int32_t* slots, const LevelPlanes& lp, hipStream_t stream) {
-  return in_launches(c, tokens, [&](int64_t t0, int64_t n, dim3 grid) {
-    ReadArgs a{{side[0], side[1]}, slots + t0, (uint32_t)(n * c.heads), (uint32_t)c.heads,
+  return in_launches<HPT>(c, tokens, [&](int64_t t0, int64_t n, dim3 grid) {
+    ReadArgs a{{side[0], side[1]}, slots + t0, (uint32_t)n, (uint32_t)c.heads,
                (uint32_t)(c.pages * c.page), page_shift_of(c.page)};
     for (CacheRows& s : a.side)
       s.x = static_cast<const T*>(s.x) + t0 * c.heads * (int64_t)D;
-    hipLaunchKernelGGL((read_rows<T, FMT, D>), grid, dim3(kThreads), 0, stream, a, lp);
+    hipLaunchKernelGGL((read_rows<T, FMT, D, HPT>), grid, dim3(kThreads), 0, stream, a, lp);
   });
+}
+
+template <typename T, int FMT, int D, typename... A>
+hipError_t write_heads(const CacheRows (&side)[2], const opq_cache& c, int64_t tokens, A... a) {
+  if (c.heads > 1 && many_rows(c, tokens))
+    return write_all<T, FMT, D, 2>(side, c, tokens, a...);
+  return write_all<T, FMT, D, 1>(side, c, tokens, a...);
+}
+template <typename T, int FMT, int D, typename... A>
+hipError_t read_heads(const CacheRows (&side)[2], const opq_cache& c, int64_t tokens, A... a) {
+  if (c.heads > 1 && many_rows(c, tokens))
+    return read_all<T, FMT, D, 4>(side, c, tokens, a...);
+  return read_all<T, FMT, D, 1>(side, c, tokens, a...);
 }
 
 template <typename T, int FMT, typename... A>
 hipError_t write_dim(const CacheRows (&side)[2], const opq_cache& c, A... a) {
-  if (c.dim == 64) return write_all<T, FMT, 64>(side, c, a...);
-  if (c.dim == 128) return write_all<T, FMT, 128>(side, c, a...);
-  return write_all<T, FMT, 256>(side, c, a...);
+  if (c.dim == 64) return write_heads<T, FMT, 64>(side, c, a...);
+  if (c.dim == 128) return write_heads<T, FMT, 128>(side, c, a...);
+  return write_heads<T, FMT, 256>(side, c, a...);
 }
 template <typename T, int FMT, typename... A>
 hipError_t read_dim(const CacheRows (&side)[2], const opq_cache& c, A... a) {
-  if (c.dim == 64) return read_all<T, FMT, 64>(side, c, a...);
-  if (c.dim == 128) return read_all<T, FMT, 128>(side, c, a...);
-  return read_all<T, FMT, 256>(side, c, a...);
+  if (c.dim == 64) return read_heads<T, FMT, 64>(side, c, a...);
+  if (c.dim == 128) return read_heads<T, FMT, 128>(side, c, a...);
+  return read_heads<T, FMT, 256>(side, c, a...);
 }
 template <typename T, typename... A>
 hipError_t write_format(const CacheRows (&side)[2], const opq_cache& c, A... a) {
