@@ -31,6 +31,7 @@
 #include "attention_internal.hpp"
 #include "decode.hpp"
 
+
 namespace opq {
 namespace {
 
@@ -73,10 +74,11 @@ __device__ __forceinline__ void build_pairs(const LevelPlanes& lp, uint32_t* pai
   RowLut t;
 #pragma unroll
   for (int i = 0; i < 4; ++i) { t.lo[i] = lp.lo[i]; t.hi[i] = lp.hi[i]; }
+  if (threadIdx.x >= 256) return;  // a code byte a thread
 #pragma unroll
   for (uint32_t sign = 0; sign < 4; ++sign) {
     uint32_t o[4];
-    decode_word_split(threadIdx.x, sign, t, o);  // a code byte a thread
+    decode_word_split(threadIdx.x, sign, t, o);
     pairs[sign * kSignStride + threadIdx.x] = o[0];
   }
 }
@@ -313,6 +315,249 @@ __device__ __forceinline__ Extent extent(const AttentionArgs& a, int b, int last
   return e;
 }
 
+// Which piece of which sequence's keys, for which group of query rows, a workgroup has.
+struct Task {
+  int split, b, kvh, rg;
+};
+__device__ __forceinline__ bool task_of(const AttentionArgs& a, Task& t) {
+  // Workgroups that read the same keys for different query rows sit on one XCD
+  // (blockIdx % 8), next to each other, and share its L2.
+  int unit;
+  if (a.groups == 1) {
+    unit = (int)blockIdx.x;
+    t.rg = 0;
+  } else {
+    const int xcd = (int)blockIdx.x & 7, j = (int)blockIdx.x >> 3;
+    t.rg = j % a.groups;
+    unit = (j / a.groups) * 8 + xcd;
+    if (unit >= a.batch * a.kv_heads * a.splits) return false;
+  }
+  // Pieces of one sequence are far apart: the ones that a short sequence does not
+  // have would otherwise be every blockIdx of some XCDs, which then stand idle
+  // (32 sequences of half the longest length: 83 against 58 us).
+  const int pairs = a.batch * a.kv_heads, bh = unit % pairs;
+  t.split = unit / pairs;
+  t.b = bh / a.kv_heads;
+  t.kvh = bh - t.b * a.kv_heads;
+  return true;
+}
+
+// A wave's walk over the keys k0 .. k1 of one sequence and kv head, 32 at a time.
+template <int FMT, int D>
+struct Walk {
+  static constexpr int kRow = kRowBytes<FMT, D>;
+  // Rows past the last one that counts may hold NaN codes, which no weight of 0
+  // takes away; OPQ codes have none.
+  static constexpr bool kClamp = FMT != OPQ_CACHE_OPQ4;
+  struct Place {
+    int64_t row;  // first row of a 16-key tile
+    int left;     // last row of the tile that counts
+    bool lost;    // the page id names no page
+  };
+  const AttentionArgs& a;
+  const int32_t* table;
+  int64_t k1, last_tile, held;
+  uint32_t ids;  // lane i: id of page `held + i`
+  int kvh, lane, c, g;
+  KeyTile<FMT, D> kt[2];
+  ValueTile<FMT, D> vt;
+  floatx4_t ks[2], vs[2];
+  Place at[2];
+
+  __device__ __forceinline__ Walk(const AttentionArgs& args, const Task& t, int64_t k0, int64_t end,
+                                  int lane_)
+      : a(args), table(args.page_table + (int64_t)t.b * args.max_pages), k1(end),
+        last_tile((end - 1) & ~(int64_t)15), held(k0 >> args.page_shift), ids(0u), kvh(t.kvh),
+        lane(lane_), c(lane_ & 15), g(lane_ >> 4) {}
+
+  __device__ __forceinline__ void hold(int64_t first) {
+    held = first;
+    const int64_t p = first + lane;
+    if (p < a.max_pages) ids = (uint32_t)table[p];
+    // waited for here (vmcnt(0)), where it happens once in many steps: left to its
+    // use, every step would wait for all of its requests in flight
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+  }
+  // Finds the two 16-key tiles at `key`, each inside one page.  A tile past the end
+  // is read from the last tile instead, and rows past it from the last row.
+  __device__ __forceinline__ void find(int64_t key) {
+    const int64_t page_mask = ((int64_t)1 << a.page_shift) - 1;
+    if (((key + 16 < last_tile ? key + 16 : last_tile) >> a.page_shift) - held >= kWave)
+      hold((key < last_tile ? key : last_tile) >> a.page_shift);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t base = key + 16 * u < last_tile ? key + 16 * u : last_tile;
+      const int64_t index = (base >> a.page_shift) - held;
+      const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)index);
+      at[u].lost = id >= a.pages;
+      at[u].row = (((int64_t)(at[u].lost ? 0u : id) * a.kv_heads + kvh) << a.page_shift) +
+                  (base & page_mask);
+      at[u].left = (int)(k1 - 1 - base < 15 ? k1 - 1 - base : 15);
+    }
+  }
+  __device__ __forceinline__ static uint32_t row_of(int r, int left) {
+    return (uint32_t)(!kClamp || r < left ? r : left);
+  }
+  __device__ __forceinline__ void load_keys() {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      kt[u].load(a.k + at[u].row * kRow,
+                 reinterpret_cast<const char*>(a.k_sign) + at[u].row * (D / 8),
+                 row_of(c, at[u].left), g);
+      ks[u] = *reinterpret_cast<const floatx4_t*>(a.k_scale + at[u].row + 4 * g);
+    }
+  }
+  __device__ __forceinline__ void load_values() {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // unclamped rows differ by a constant from the lane's first
+        const int64_t first = at[u].row + (kClamp ? 0 : i);
+        vt.load(4 * u + i, a.v + first * kRow,
+                reinterpret_cast<const char*>(a.v_sign) + first * (D / 8),
+                kClamp ? row_of(4 * g + i, at[u].left) : 4u * g, c);
+      }
+      vs[u] = *reinterpret_cast<const floatx4_t*>(a.v_scale + at[u].row + 4 * g);
+    }
+  }
+  // the loaded keys' scales, times scale log2(e); NaN for a page that is none
+  __device__ __forceinline__ floatx4_t key_scale(int u) const {
+    const float sc = at[u].lost ? __builtin_nanf("") : a.scale_log2;
+    floatx4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = ks[u][i] * sc;
+    return r;
+  }
+};
+
+// Which of a lane's eight keys (bit 4 u + i: key kk + 16 u + 4 g + i) its query
+// row, of drafted token `token`, does not see.
+__device__ __forceinline__ uint32_t hidden_keys(const AttentionArgs& a, const Extent& ex, int b,
+                                                int token, int64_t kk, int64_t k1, int g) {
+  const bool counts = token < ex.count;
+  uint32_t seen = 0u;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    // drafted index of the lane's first key of the tile, and how many of its four
+    // keys there are
+    const int64_t key = kk + 16 * u + 4 * g;
+    const int j0 = (int)(key - ex.len < -kStep ? -kStep : key - ex.len);
+    const int there = (int)clamp64(k1 - key, 0, 4);
+    uint32_t four;
+    if (a.mask) {
+      // the row's bits j0 .. j0 + 3, those before the draft set
+      const uint32_t* row = a.mask + (int64_t)b * a.mask_batch +
+                            (int64_t)(counts ? token : 0) * a.mask_words;
+      const int last = (int)a.mask_words - 1, j = j0 < 0 ? 0 : j0;
+      const int w0 = j >> 5 < last ? j >> 5 : last, w1 = w0 < last ? w0 + 1 : last;
+      const uint64_t bits = ((uint64_t)row[w1] << 32 | row[w0]) >> (j & 31);
+      const int before = j - j0 < 4 ? j - j0 : 4;
+      four = ((uint32_t)bits << before | ((1u << before) - 1u)) & 15u;
+    } else {
+      const int upto = token + 1 - j0;  // a chain: j <= token
+      four = (1u << (upto < 0 ? 0 : upto > 4 ? 4 : upto)) - 1u;
+    }
+    four &= (1u << there) - 1u;
+    seen |= four << (4 * u);
+  }
+  uint32_t hidden = counts ? ~seen : 255u;
+  // opaque: eight bits in a register, not eight lane masks in scalar ones
+  asm volatile("" : "+v"(hidden));
+  return hidden;
+}
+
+// A 16-row tile of queries: lane 16 g + c has the running maximum of row c, its own
+// keys' part of the sum, and dimensions kTiles (4 g + i) + j in o[j][i].
+template <int kTiles>
+struct Rows {
+  floatx4_t o[kTiles];
+  float m, l;
+  __device__ __forceinline__ void clear() {
+    m = kLowest;
+    l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[j] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // Takes the products of 32 keys in and gives their weights, times the values'
+  // scales, as the B operand of the second product.  No score of the lane's keys
+  // exceeds max(acc, 0) * scale_top (the largest of kscale): while that stays near
+  // the running maximum, the scores themselves are formed only inside the
+  // exponent, one fused multiply-add each.
+  __device__ __forceinline__ bf16x8_t weigh(const floatx4_t& s0, const floatx4_t& s1,
+                                            const floatx4_t (&kscale)[2], float scale_top,
+                                            const floatx4_t (&vs)[2], bool masked,
+                                            uint32_t hidden) {
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i] = s0[i];
+      acc[4 + i] = s1[i];
+    }
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, acc[i]);
+    if (__builtin_amdgcn_ballot_w64(most * scale_top > m + kSlack)) {
+      float top = kLowest;
+      // an opaque copy, here and below: the tests of its bits stay on these rare ways
+      uint32_t h = hidden;
+      asm volatile("" : "+v"(h));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float s = acc[i] * kscale[i >> 2][i & 3];
+        top = fmaxf(top, (h >> i) & 1u ? kLowest : s);
+      }
+      if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16, kWave));
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        const float raised = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - raised);
+        m = raised;
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] *= f;
+      }
+    }
+    float e[8], w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i], kscale[i >> 2][i & 3], -m));
+      w[i] = e[i] * vs[i >> 2][i & 3];
+    }
+    if (masked) {  // a hidden token may hold anything
+      uint32_t h = hidden;
+      asm volatile("" : "+v"(h));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool hide = (h >> i) & 1u;
+        e[i] = hide ? 0.0f : e[i];
+        w[i] = hide ? 0.0f : w[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l += e[i];
+    return frag(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]),
+                pack_bf16(w[6], w[7]));
+  }
+};
+__device__ __forceinline__ float top_of(const floatx4_t (&k)[2]) {
+  float t = fmaxf(k[0][0], k[1][0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) t = fmaxf(t, fmaxf(k[0][i], k[1][i]));
+  return t;
+}
+
+// Row r of a kv head's queries: 16 bytes at dimension d, or zeros past the last row.
+__device__ __forceinline__ bf16x8_t query_at(const AttentionArgs& a, const Task& k, int r, int d) {
+  const int t = r / a.share;
+  const uint16_t* p = a.q + (int64_t)k.b * a.q_batch + (int64_t)t * a.q_token +
+                      (int64_t)(k.kvh * a.share + (r - t * a.share)) * a.q_head;
+  u32x4_t w = {0u, 0u, 0u, 0u};
+  if (r < a.rows) w = *reinterpret_cast<const u32x4_t*>(p + d);
+  return __builtin_bit_cast(bf16x8_t, w ^ a.q_flip);
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int FMT, int D, int NT>
@@ -323,37 +568,20 @@ template <int FMT, int D, int NT>
 __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(AttentionArgs a) {
   constexpr int kSteps = D / 32;  // product steps of a score
   constexpr int kTiles = D / 16;  // result tiles, and dimensions of a value lane
-  constexpr int kRow = kRowBytes<FMT, D>;
   typedef ValueTile<FMT, D> V;
 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave, c = lane & 15, g = lane >> 4;
 
-  // Workgroups that read the same keys for different query rows sit on one XCD
-  // (blockIdx % 8), next to each other, and share its L2.
-  int unit, rg;
-  if (a.groups == 1) {
-    unit = (int)blockIdx.x;
-    rg = 0;
-  } else {
-    const int xcd = (int)blockIdx.x & 7, j = (int)blockIdx.x >> 3;
-    rg = j % a.groups;
-    unit = (j / a.groups) * 8 + xcd;
-    if (unit >= a.batch * a.kv_heads * a.splits) return;
-  }
-  // Pieces of one sequence are far apart: the ones that a short sequence does not
-  // have would otherwise be every blockIdx of some XCDs, which then stand idle
-  // (32 sequences of half the longest length: 83 against 58 us).
-  const int pairs = a.batch * a.kv_heads, split = unit / pairs, bh = unit - split * pairs;
-  const int kvh = bh % a.kv_heads, b = bh / a.kv_heads;
-
-  const int r0 = rg * NT * 16;
+  Task k;
+  if (!task_of(a, k)) return;
+  const int r0 = k.rg * NT * 16;
   const int r_last = (r0 + NT * 16 < a.rows ? r0 + NT * 16 : a.rows) - 1;
-  const Extent ex = extent(a, b, r_last);
-  const int64_t k0 = (int64_t)split * a.chunk;
-  if (split > 0 && k0 >= ex.end) return;
+  const Extent ex = extent(a, k.b, r_last);
+  const int64_t k0 = (int64_t)k.split * a.chunk;
+  if (k.split > 0 && k0 >= ex.end) return;
   // the last piece takes what a sequence has past max_len
-  const int64_t k1 = split + 1 < a.splits && k0 + a.chunk < ex.end ? k0 + a.chunk : ex.end;
+  const int64_t k1 = k.split + 1 < a.splits && k0 + a.chunk < ex.end ? k0 + a.chunk : ex.end;
   const bool direct = a.splits == 1 || ex.end <= a.chunk;  // sees all of its rows' keys
 
   __shared__ uint32_t lut[FMT == OPQ_CACHE_OPQ4 ? kPairs : 1];
@@ -370,16 +598,12 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
   int token[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = r0 + 16 * n + c, t = r / a.share;
-    token[n] = t;
-    const uint16_t* p = a.q + (int64_t)b * a.q_batch + (int64_t)t * a.q_token +
-                        (int64_t)(kvh * a.share + (r - t * a.share)) * a.q_head;
+    const int r = r0 + 16 * n + c;
+    token[n] = r / a.share;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       if (kShareQ && s % kWaves != wave) continue;
-      u32x4_t w = {0u, 0u, 0u, 0u};
-      if (r < a.rows) w = *reinterpret_cast<const u32x4_t*>(p + KeyTile<FMT, D>::dim_at(s, g));
-      const bf16x8_t v = __builtin_bit_cast(bf16x8_t, w ^ a.q_flip);
+      const bf16x8_t v = query_at(a, k, r, KeyTile<FMT, D>::dim_at(s, g));
       if constexpr (kShareQ) q_all[n][s][lane] = v;
       else q[n][s] = v;
     }
@@ -390,93 +614,23 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
     else return q[n][s];
   };
 
-  floatx4_t o[NT][kTiles];
-  float m[NT], l[NT];
+  Rows<kTiles> rows[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    m[n] = kLowest;
-    l[n] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[n][j] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  // Page ids: lane i holds that of page `held + i`; a step reads its two from there.
-  const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
-  const int64_t page_mask = ((int64_t)1 << a.page_shift) - 1;
-  int64_t held = k0 >> a.page_shift;
-  uint32_t ids = 0u;
-  auto hold = [&](int64_t first) {
-    held = first;
-    const int64_t p = first + lane;
-    if (p < a.max_pages) ids = (uint32_t)table[p];
-    // waited for here (vmcnt(0)), where it happens once in many steps: left to its
-    // use, every step would wait for all of its requests in flight
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-  };
-  // A step's keys are two 16-key tiles, each inside one page.  A tile past the end
-  // is read from the last tile instead, and rows past it from the last row
-  // (`row_of`).
-  const int64_t last_tile = (k1 - 1) & ~(int64_t)15;
-  struct Place {
-    int64_t row;    // first row of the tile
-    int left;       // last row of the tile that counts
-    bool lost;      // the page id names no page
-  };
-  auto place = [&](int64_t key) {
-    const int64_t base = key < last_tile ? key : last_tile;
-    const int64_t index = (base >> a.page_shift) - held;
-    const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)index);
-    Place p;
-    p.lost = id >= a.pages;
-    p.row = (((int64_t)(p.lost ? 0u : id) * a.kv_heads + kvh) << a.page_shift) + (base & page_mask);
-    p.left = (int)(k1 - 1 - base < 15 ? k1 - 1 - base : 15);
-    return p;
-  };
-  // Rows past the last one that counts may hold NaN codes, which no weight of 0
-  // takes away; OPQ codes have none.
-  constexpr bool kClamp = FMT != OPQ_CACHE_OPQ4;
-  auto row_of = [](int r, int left) { return (uint32_t)(!kClamp || r < left ? r : left); };
-  KeyTile<FMT, D> kt[2];
-  V vt;
-  floatx4_t ks[2], vs[2];
-  auto load_keys = [&](const Place (&at)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      kt[u].load(a.k + at[u].row * kRow,
-                 reinterpret_cast<const char*>(a.k_sign) + at[u].row * (D / 8),
-                 row_of(c, at[u].left), g);
-      ks[u] = *reinterpret_cast<const floatx4_t*>(a.k_scale + at[u].row + 4 * g);
-    }
-  };
-  auto load_values = [&](const Place (&at)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // unclamped rows differ by a constant from the lane's first
-        const int64_t first = at[u].row + (kClamp ? 0 : i);
-        vt.load(4 * u + i, a.v + first * kRow,
-                reinterpret_cast<const char*>(a.v_sign) + first * (D / 8),
-                kClamp ? row_of(4 * g + i, at[u].left) : 4u * g, c);
-      }
-      vs[u] = *reinterpret_cast<const floatx4_t*>(a.v_scale + at[u].row + 4 * g);
-    }
-  };
+  for (int n = 0; n < NT; ++n) rows[n].clear();
 
   // Software pipeline: a step's keys are requested before the softmax of the step
   // before it, its values before its own scores.  The requests past the last step
   // repeat its rows: without a condition around them, the loop waits for nothing
   // but what it uses.
+  Walk<FMT, D> w(a, k, k0, k1, lane);
   int64_t kk = k0 + wave * kStep;
-  Place at[2];
   if (kk < k1) {
-    hold(held);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) at[u] = place(kk + 16 * u);
-    load_keys(at);
+    w.hold(w.held);
+    w.find(kk);
+    w.load_keys();
   }
   for (; kk < k1; kk += kRound) {
-    load_values(at);
+    w.load_values();
     floatx4_t st[2][NT], kscale[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -484,133 +638,40 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
       for (int n = 0; n < NT; ++n) st[u][n] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const bf16x8_t k = kt[u].at(s, lut);
+        const bf16x8_t key = w.kt[u].at(s, lut);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          st[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q_at(n, s), st[u][n], 0, 0, 0);
+          st[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key, q_at(n, s), st[u][n], 0, 0, 0);
       }
-      const float sc = at[u].lost ? __builtin_nanf("") : a.scale_log2;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) kscale[u][i] = ks[u][i] * sc;
+      kscale[u] = w.key_scale(u);
       // made here, before the next step's scales are requested: kept for later, the
       // old and the new scales would change places in registers at the loop's end,
       // which waits for the new ones
       asm volatile("" : "+v"(kscale[u]));
     }
-    const int64_t next = kk + kRound;
-    if (((next + 16 < last_tile ? next + 16 : last_tile) >> a.page_shift) - held >= kWave)
-      hold((next < last_tile ? next : last_tile) >> a.page_shift);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) at[u] = place(next + 16 * u);
-    load_keys(at);
+    w.find(kk + kRound);
+    w.load_keys();
 
-    // Masks touch only the steps that reach past the cached tokens: bit 4 u + i
-    // of `hidden` is the lane's key i of tile u.
+    // masks touch only the steps that reach past the cached tokens
     const bool masked = kk + kStep > (ex.len < k1 ? ex.len : k1);
-    uint32_t hidden[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) hidden[n] = 0u;
-    if (masked) {
-      // drafted index of the lane's first key of each tile, and how many of its
-      // four keys there are
-      int j0[2], there[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t key = kk + 16 * u + 4 * g;
-        j0[u] = (int)(key - ex.len < -kStep ? -kStep : key - ex.len);
-        there[u] = (int)clamp64(k1 - key, 0, 4);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bool counts = token[n] < ex.count;
-        uint32_t seen = 0u;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t four;
-          if (a.mask) {
-            // the row's bits j0 .. j0 + 3, those before the draft set
-            const uint32_t* row = a.mask + (int64_t)b * a.mask_batch +
-                                  (int64_t)(counts ? token[n] : 0) * a.mask_words;
-            const int last = (int)a.mask_words - 1, j = j0[u] < 0 ? 0 : j0[u];
-            const int w0 = j >> 5 < last ? j >> 5 : last, w1 = w0 < last ? w0 + 1 : last;
-            const uint64_t bits = ((uint64_t)row[w1] << 32 | row[w0]) >> (j & 31);
-            const int before = j - j0[u] < 4 ? j - j0[u] : 4;
-            four = ((uint32_t)bits << before | ((1u << before) - 1u)) & 15u;
-          } else {
-            const int upto = token[n] + 1 - j0[u];  // a chain: j <= token
-            four = (1u << (upto < 0 ? 0 : upto > 4 ? 4 : upto)) - 1u;
-          }
-          four &= (1u << there[u]) - 1u;
-          seen |= four << (4 * u);
-        }
-        hidden[n] = counts ? ~seen : 255u;
-        // opaque: eight bits in a register, not eight lane masks in scalar ones
-        asm volatile("" : "+v"(hidden[n]));
-      }
-    }
-
-    // No score of the lane's keys exceeds max(acc, 0) * scale_top: while that stays
-    // near the running maximum, the scores themselves are formed only inside
-    // the exponent, one fused multiply-add each.
-    float scale_top = fmaxf(kscale[0][0], kscale[1][0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) scale_top = fmaxf(scale_top, fmaxf(kscale[0][i], kscale[1][i]));
+    const float scale_top = top_of(kscale);
     bf16x8_t p[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float most = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) most = fmaxf(most, st[i >> 2][n][i & 3]);
-      if (__builtin_amdgcn_ballot_w64(most * scale_top > m[n] + kSlack)) {
-        float top = kLowest;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float s = st[i >> 2][n][i & 3] * kscale[i >> 2][i & 3];
-          top = fmaxf(top, (hidden[n] >> i) & 1u ? kLowest : s);
-        }
-        if (__builtin_amdgcn_ballot_w64(top > m[n] + kSlack)) {
-          top = fmaxf(top, __shfl_xor(top, 16, kWave));
-          top = fmaxf(top, __shfl_xor(top, 32, kWave));
-          const float raised = fmaxf(m[n], top), f = __builtin_amdgcn_exp2f(m[n] - raised);
-          m[n] = raised;
-          l[n] *= f;
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
-        }
-      }
-      float e[8], w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(
-            __builtin_fmaf(st[i >> 2][n][i & 3], kscale[i >> 2][i & 3], -m[n]));
-        w[i] = e[i] * vs[i >> 2][i & 3];
-      }
-      if (masked) {  // a hidden token may hold anything
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool hide = (hidden[n] >> i) & 1u;
-          e[i] = hide ? 0.0f : e[i];
-          w[i] = hide ? 0.0f : w[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) l[n] += e[i];
-      p[n] = frag(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]),
-                  pack_bf16(w[6], w[7]));
+      uint32_t hidden = 0u;
+      if (masked) hidden = hidden_keys(a, ex, k.b, token[n], kk, k1, g);
+      p[n] = rows[n].weigh(st[0][n], st[1][n], kscale, scale_top, w.vs, masked, hidden);
     }
-
 #pragma unroll
     for (int t = 0; t < kTiles / V::kTogether; ++t) {
       bf16x8_t v[V::kTogether];
-      vt.tiles(t, lut, v);
+      w.vt.tiles(t, lut, v);
 #pragma unroll
       for (int j = 0; j < V::kTogether; ++j)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          o[n][t * V::kTogether + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              v[j], p[n], o[n][t * V::kTogether + j], 0, 0, 0);
+          rows[n].o[t * V::kTogether + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              v[j], p[n], rows[n].o[t * V::kTogether + j], 0, 0, 0);
     }
   }
 
@@ -623,11 +684,12 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
   __shared__ float o_all[kWaves][16][kCols + 4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    l[n] += __shfl_xor(l[n], 16, kWave);
-    l[n] += __shfl_xor(l[n], 32, kWave);
+    float l = rows[n].l;
+    l += __shfl_xor(l, 16, kWave);
+    l += __shfl_xor(l, 32, kWave);
     if (g == 0) {
-      m_all[wave][16 * n + c] = m[n];
-      l_all[wave][16 * n + c] = l[n];
+      m_all[wave][16 * n + c] = rows[n].m;
+      l_all[wave][16 * n + c] = l;
     }
   }
   __syncthreads();
@@ -644,8 +706,8 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
       lt += l_all[w][16 * n + rr] * __builtin_amdgcn_exp2f(m_all[w][16 * n + rr] - mt);
-    const float f = __builtin_amdgcn_exp2f(m[n] - top);
-    const int r = r0 + 16 * n + rr, t = r / a.share, h = kvh * a.share + (r - t * a.share);
+    const float f = __builtin_amdgcn_exp2f(rows[n].m - top);
+    const int r = r0 + 16 * n + rr, t = r / a.share, h = k.kvh * a.share + (r - t * a.share);
     const bool none = lt == 0.0f || t >= ex.count;
     const float inv = none ? 0.0f : 1.0f / lt;
 #pragma unroll
@@ -655,7 +717,7 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
       for (int i = 0; i < kSpan; ++i)
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
-          o_all[wave][c][kTiles * (kSpan * g + i) + j] = o[n][j][kSpan * part + i] * f;
+          o_all[wave][c][kTiles * (kSpan * g + i) + j] = rows[n].o[j][kSpan * part + i] * f;
       __syncthreads();
       if (r >= a.rows) continue;
       float v[kOwn];
@@ -668,7 +730,7 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
       const int dim = kParts == 1 ? col : col / (kSpan * kTiles) * (4 * kTiles) +
                                               part * (kSpan * kTiles) + col % (kSpan * kTiles);
       if (direct) {
-        const int64_t at = ((int64_t)b * a.draft + t) * a.heads + h;
+        const int64_t at = ((int64_t)k.b * a.draft + t) * a.heads + h;
         uint32_t* out = reinterpret_cast<uint32_t*>(a.out + at * D + dim);
 #pragma unroll
         for (int j = 0; j < kOwn / 2; ++j)
@@ -676,7 +738,7 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
         if (a.lse && col == 0 && part == 0)
           a.lse[at] = none ? -__builtin_inff() : (mt + log2f(lt)) * 0.69314718055994531f;
       } else {
-        const int64_t at = (((int64_t)split * a.batch + b) * a.kv_heads + kvh) * a.rows + r;
+        const int64_t at = (((int64_t)k.split * a.batch + k.b) * a.kv_heads + k.kvh) * a.rows + r;
         float* po = a.part_o + at * D + dim;
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) po[j] = v[j];
@@ -689,13 +751,15 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
   }
 }
 
+// ------------------------------------------------------------------ joining pieces
+
 // Join the pieces of the keys.  A wave holds 256 / D pieces at a time, 16 bytes a
 // lane, and merges them into a running result as the kernel above merges keys; a
 // piece's partial result and its (m, l) are requested together, so nothing waits
 // for a maximum over all pieces first.  kTeam waves share a row (4 where a row has
 // many pieces) and meet in LDS.
 template <int D, int kTeam>
-__global__ __launch_bounds__(kThreads) void join_pieces(AttentionArgs a, int group_rows) {
+__global__ __launch_bounds__(kThreads) void join_pieces(AttentionArgs a) {
   constexpr int kLanes = D / 4, kTogether = kWave / kLanes, kUnroll = 4;
   const int lane = threadIdx.x % kWave, sub = lane / kLanes, d = (lane % kLanes) * 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -704,7 +768,7 @@ __global__ __launch_bounds__(kThreads) void join_pieces(AttentionArgs a, int gro
   if (row >= all) return;  // all waves of a team
   const int bh = row / a.rows, r = row - bh * a.rows;
   const int b = bh / a.kv_heads, kvh = bh - b * a.kv_heads;
-  int r_last = (r / group_rows + 1) * group_rows;
+  int r_last = (r / a.group_rows + 1) * a.group_rows;
   r_last = (r_last < a.rows ? r_last : a.rows) - 1;
   const Extent ex = extent(a, b, r_last);
   if (ex.end <= a.chunk) return;  // one workgroup saw all of it and wrote the result
@@ -779,25 +843,26 @@ hipError_t go(const AttentionArgs& a, hipStream_t stream) {
   // rows are few, get a workgroup each.
   const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
   if (a.splits > 4 * (256 / D) && rows <= 8192)
-    hipLaunchKernelGGL((join_pieces<D, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, stream, a,
-                       NT * 16);
+    hipLaunchKernelGGL((join_pieces<D, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, stream, a);
   else
     hipLaunchKernelGGL((join_pieces<D, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, stream, a, NT * 16);
+                       dim3(kThreads), 0, stream, a);
   return hipGetLastError();
+}
+
+template <int FMT, int D>
+hipError_t go_tiles(const AttentionArgs& a, int tiles, hipStream_t stream) {
+  if constexpr (D < 256) {
+    if (tiles == 2) return go<FMT, D, 2>(a, stream);
+  }
+  return go<FMT, D, 1>(a, stream);
 }
 
 template <int FMT>
 hipError_t go_format(const AttentionArgs& a, int dim, int tiles, hipStream_t stream) {
-  if (dim == 64) {
-    if (tiles == 1) return go<FMT, 64, 1>(a, stream);
-    return go<FMT, 64, 2>(a, stream);
-  }
-  if (dim == 128) {
-    if (tiles == 1) return go<FMT, 128, 1>(a, stream);
-    return go<FMT, 128, 2>(a, stream);
-  }
-  return go<FMT, 256, 1>(a, stream);
+  if (dim == 64) return go_tiles<FMT, 64>(a, tiles, stream);
+  if (dim == 128) return go_tiles<FMT, 128>(a, tiles, stream);
+  return go_tiles<FMT, 256>(a, tiles, stream);
 }
 
 }  // namespace
@@ -806,19 +871,26 @@ AttentionPlan attention_plan(int64_t batch, int64_t draft, int64_t heads, int64_
                              int64_t dim, int64_t max_len) {
   AttentionPlan p;
   const int64_t rows = draft * (heads / kv_heads);
-  const int most = dim == 256 ? 1 : 2;
-  p.tiles = rows <= 16 ? 1 : most;
-  p.groups = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
-  // About 1024 workgroups: four for each of the 256 CUs, so that the last ones
-  // to run are a small part of the whole (32 sequences of up to 8191 tokens: 67 us,
-  // 76 with 512, 69 with 2048).  Pieces of at least 512 keys where that makes 512
-  // workgroups, shorter ones (down to one round) where keys are few.
+  const int64_t tiles = (rows + 15) / 16;
+  p.tiles = dim == 256 || tiles == 1 ? 1 : 2;
+  p.groups = (int)((tiles + p.tiles - 1) / p.tiles);
+  p.group_rows = 16 * p.tiles;
   const int64_t units = batch * kv_heads * p.groups, keys = max_len + draft;
-  const int64_t rounds = (keys + kRound - 1) / kRound, half = (512 + units - 1) / units;
-  int64_t splits = (1024 + units - 1) / units, most_long = (rounds + 3) / 4;
-  most_long = most_long > half ? most_long : half;
-  splits = splits < most_long ? splits : most_long;
-  splits = splits < rounds ? splits : rounds;
+  const int64_t rounds = (keys + kRound - 1) / kRound;
+  // About 1024 workgroups: four for each of the 256 CUs, so that the last ones to
+  // run are a small part of the whole (32 sequences of up to 8191 tokens: 67 us, 76
+  // with 512, 69 with 2048).  But a piece has to be worth its partial result: 4
+  // rounds of keys where that is 16 rows (8 sequences of 2000 tokens: 13 us in 4
+  // pieces, 16 to 18 in 8 or 16), 12 where a workgroup has 32 (8 sequences of 1000
+  // tokens with 192 rows: 32 us in one piece, 43 in three).  Shorter ones, down to
+  // two rounds, only for workgroups that would leave CUs empty (one sequence of 1000
+  // tokens: 9.4 us in 4 pieces, 11.2 in one).  Joining costs more than splitting up
+  // to 4 rounds saves (16 sequences of 500 tokens: 9.2 us in one, 12.8 in two).
+  const int64_t worth = p.tiles == 1 ? 4 : 12, by_length = rounds / worth;
+  int64_t splits = (1024 + units - 1) / units, fill = (256 + units - 1) / units;
+  fill = fill < rounds / 2 ? fill : rounds / 2;
+  const int64_t bound = rounds <= 4 ? 1 : by_length > fill ? by_length : fill;
+  splits = splits < bound ? splits : bound;
   splits = splits < 64 ? splits : 64;
   splits = splits < 1 ? 1 : splits;
   p.chunk = ((keys + splits - 1) / splits + kRound - 1) / kRound * kRound;

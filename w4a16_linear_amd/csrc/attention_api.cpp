@@ -299,6 +299,7 @@ int opq_cache_attention(const opq_cache* cache, const uint16_t* q, int64_t batch
   a.rows = (int)(draft * (heads / c.heads));
   a.splits = plan.splits;
   a.groups = plan.groups;
+  a.group_rows = plan.group_rows;
   a.scale_log2 = (float)(std::fabs((double)scale) * 1.4426950408889634);
   a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
   a.out = out;

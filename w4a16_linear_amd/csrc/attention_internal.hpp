@@ -63,6 +63,7 @@ hipError_t launch_cache_read(const CacheRows (&side)[2], const opq_cache& c, boo
 // attention.hip
 struct AttentionPlan {
   int tiles;      // 16-row tiles of query rows in a workgroup
+  int group_rows; // query rows of a workgroup
   int groups;     // workgroups that cover a kv head's query rows
   int splits;     // pieces of the keys
   int64_t chunk;  // keys of a piece, a multiple of 128
@@ -86,7 +87,7 @@ struct AttentionArgs {
   const uint32_t* mask;
   int64_t mask_batch, mask_words, max_pages, capacity, chunk;
   uint32_t pages;
-  int page_shift, batch, draft, heads, kv_heads, share, rows, splits, groups;
+  int page_shift, batch, draft, heads, kv_heads, share, rows, splits, groups, group_rows;
   float scale_log2;  // |scale| * log2(e)
   uint32_t q_flip;   // sign bits of two bfloat16: set for a negative scale
   uint16_t* out;
