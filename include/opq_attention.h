@@ -158,6 +158,22 @@ int opq_cache_write(const opq_cache* cache, const void* k, int64_t k_token_strid
 int opq_cache_read(const opq_cache* cache, int64_t tokens, const int32_t* slots, void* k_out,
                    void* v_out, int dtype, void* stream);
 
+/*
+ * Move rows of a cache, codes and scales as they are: token src[b][i] to slot
+ * dst[b][i], for every head, of keys and values.  What a verified tree of drafted
+ * tokens needs: the accepted ones move up to the slots right after the cached
+ * tokens.  Within a sequence b every row is read before any is written, so
+ * slots may be sources and destinations at once (but each at most once a
+ * destination); sequences of one call must not share slots.  A pair with a slot
+ * outside 0..pages*page-1 (such as -1) moves nothing.
+ *   src, dst  device, [batch][count] int32;  count 0..128; batch up to 65535 and
+ *             batch * heads up to 2^22
+ * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALPHA, OPQ_ERR_ALIGN,
+ * OPQ_ERR_DTYPE, OPQ_ERR_UNSUPPORTED (count or batch past their limits), OPQ_ERR_HIP.
+ */
+int opq_cache_move(const opq_cache* cache, int64_t batch, int64_t count, const int32_t* src,
+                   const int32_t* dst, void* stream);
+
 /* --------------------------------------------------------------- attention */
 
 /*

@@ -246,6 +246,19 @@ def test_write_and_read_argument_checks(lib):
     assert r(ref, 0, None, None, None, 1, None) == OK
 
 
+def test_move_argument_checks(lib):
+    ref = ctypes.byref(_cache())
+    m = lib.opq_cache_move
+    assert m(None, 1, 1, FAKE, FAKE, None) == NULL and m(ref, 1, 1, None, FAKE, None) == NULL
+    assert m(ref, -1, 1, FAKE, FAKE, None) == SHAPE and m(ref, 1, -1, FAKE, FAKE, None) == SHAPE
+    assert m(ref, 1, 1, FAKE, ODD, None) == ALIGN
+    for batch, count in ((65536, 1), (1, 129)):
+        assert m(ref, batch, count, FAKE, FAKE, None) == UNSUPPORTED
+    assert m(ref, 0, 1, None, None, None) == OK and m(ref, 1, 0, None, None, None) == OK
+    for kw, status in BAD_CACHES:
+        assert m(ctypes.byref(_cache(**kw)), 1, 1, FAKE, FAKE, None) == status
+
+
 def test_attention_argument_checks(lib):
     c = _cache()
 

@@ -36,6 +36,7 @@ _SIGNATURES = {
     "opq_rotary": (_I, [_P, _I, _L, _L, _L, _L, _L, _P, _L, _P, _P, _L, _L, _I, _I, _P, _L, _L, _P]),
     "opq_cache_write": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _L, _P, _P]),
     "opq_cache_read": (_I, [_P, _L, _P, _P, _P, _I, _P]),
+    "opq_cache_move": (_I, [_P, _L, _L, _P, _P, _P]),
     "opq_cache_attention_workspace_bytes": (ctypes.c_size_t, [_L, _L, _L, _L, _L, _L]),
     "opq_cache_attention": (_I, [_P, _P, _L, _L, _L, _L, _L, _L, _P, _L, _P, _P, _L, _P, _L, _F,
                                  _P, _P, _P, ctypes.c_size_t, _P]),
@@ -246,6 +247,14 @@ def cache_read(cache: PagedCache, slots: torch.Tensor, out_dtype: torch.dtype = 
         raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
     k, v = (None, None) if out is None else out
     return (_ext or _calls()).cache_read(cache, slots, dtype, k, v)
+
+
+def cache_move(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Move rows as they are stored from slots src to slots dst (int32 [batch,
+    count], count up to 128; -1 moves nothing): the accepted tokens of a verified tree
+    to the slots right after the cached ones.  A sequence's rows are all read before
+    any is written; sequences of one call must not share slots."""
+    (_ext or _calls()).cache_move(cache, src, dst)
 
 
 # --------------------------------------------------------------- attention

@@ -1,0 +1,103 @@
+"""A self-attention layer of a served transformer on libopq's kernels, end to end:
+OPQ-quantized QKV projection, rotary positions on queries and keys in one call, keys
+and values quantized into the paged cache, attention of the new tokens (one per
+sequence, a chain, or a tree of drafted ones) over it, OPQ-quantized output projection.
+
+    layer = OPQAttention(3840, heads=30, kv_heads=30).to(torch.bfloat16).cuda()
+    replace_with_opq(layer)                      # quantize both projections
+    cache = layer.new_cache(pages=512, page=64, fmt="opq4")
+    y = layer(x, cache, page_table, lens)        # x [batch, draft, hidden]
+    layer.accept(cache, page_table, lens, kept)  # of a verified tree
+
+Every step but the projections' reshapes runs in libopq; like OPQLinear, a layer whose
+tensors are not on the GPU raises.
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+import torch
+from torch import nn
+
+from . import attention as A
+
+
+def token_slots(page_table: torch.Tensor, positions: torch.Tensor, page: int) -> torch.Tensor:
+    """Cache slots (int32, the shape of `positions` [batch, n]) of positions in each
+    sequence; -1 (no slot) past the page table and for negative positions."""
+    index = torch.div(positions, page, rounding_mode="floor")
+    inside = (positions >= 0) & (index < page_table.shape[1])
+    ids = torch.gather(page_table, 1, index.clamp(0, page_table.shape[1] - 1).long())
+    return torch.where(inside, ids * page + positions % page, -1).to(torch.int32)
+
+
+class OPQAttention(nn.Module):
+    """`qkv` [hidden -> (heads + 2 kv_heads) dim] and `o` [heads dim -> hidden] start as
+    nn.Linear (replace_with_opq makes them OPQLinear); the rotary table, `rope`, covers
+    max_positions.  dim is hidden / heads unless given; 64, 128 or 256."""
+
+    def __init__(self, hidden: int, heads: int, kv_heads: Optional[int] = None,
+                 dim: Optional[int] = None, max_positions: int = 32768, rot: Optional[int] = None,
+                 base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                 original_len: float = 0.0, layout: str = "half"):
+        super().__init__()
+        self.heads, self.kv_heads = heads, kv_heads or heads
+        self.dim = dim or hidden // heads
+        if self.heads % self.kv_heads:
+            raise ValueError(f"heads={heads} must be a multiple of kv_heads={kv_heads}")
+        if self.dim not in (64, 128, 256):
+            raise ValueError(f"dim must be 64, 128 or 256, got {self.dim}")
+        self.layout, self.max_positions = layout, max_positions
+        self.frequencies = A.rotary_frequencies(rot or self.dim, base, scaling, factor, original_len)
+        self.qkv = nn.Linear(hidden, (self.heads + 2 * self.kv_heads) * self.dim, bias=False)
+        self.o = nn.Linear(self.heads * self.dim, hidden, bias=False)
+        self._rope: Optional[torch.Tensor] = None   # float32 whatever the layer's type
+
+    def rope(self, device: torch.device) -> torch.Tensor:
+        """The rotary table on `device`, made once."""
+        if self._rope is None or self._rope.device != device:
+            self._rope = A.rotary_table(self.frequencies, self.max_positions, device)
+        return self._rope
+
+    def new_cache(self, pages: int, page: int = 64, fmt: str = "opq4", alpha: float = 0.73,
+                  device="cuda") -> A.PagedCache:
+        return A.new_cache(pages, self.kv_heads, page, self.dim, fmt, alpha, device)
+
+    def forward(self, x: torch.Tensor, cache: A.PagedCache, page_table: torch.Tensor,
+                lens: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                depths: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                max_len: Optional[int] = None) -> torch.Tensor:
+        """x [batch, draft, hidden] (bfloat16): the tokens after each sequence's lens[b]
+        cached ones, written to the cache here.  mask: tree words as tree_attention
+        takes them, with depths (int32 [batch, draft]): each token's distance from the
+        last cached one, less one, which gives its position; without them a chain."""
+        batch, draft, _ = x.shape
+        steps = torch.arange(draft, dtype=torch.int32, device=x.device)
+        places = lens[:, None] + steps                       # where tokens are stored
+        positions = places if depths is None else lens[:, None] + depths
+        if counts is not None:
+            places = torch.where(steps < counts[:, None], places, -1)
+        slots = token_slots(page_table, places, cache.page)
+        h, k = self.heads, self.kv_heads
+        fused = self.qkv(x).view(batch * draft, h + 2 * k, self.dim)
+        qk = fused[:, :h + k]
+        A.rotary(qk, positions.reshape(-1).contiguous(), self.rope(x.device), self.layout, out=qk)
+        A.cache_write(cache, fused[:, h:h + k], fused[:, h + k:], slots.reshape(-1))
+        q = fused.view(batch, draft, h + 2 * k, self.dim)[:, :, :h]
+        y = A.tree_attention(q, cache, page_table, lens, mask=mask, counts=counts, max_len=max_len)
+        return self.o(y.view(batch, draft, h * self.dim))
+
+    @staticmethod
+    def accept(cache: A.PagedCache, page_table: torch.Tensor, lens: torch.Tensor,
+               kept: torch.Tensor) -> None:
+        """Keep a path of a verified tree: kept int32 [batch, n] holds the accepted drafted
+        tokens' indexes in order (-1 past a path's end); they move up to positions
+        lens[b], lens[b] + 1, ...  The caller adds the path's length to lens."""
+        n = torch.arange(kept.shape[1], dtype=torch.int32, device=kept.device)
+        src = torch.where(kept >= 0, lens[:, None] + kept, -1)
+        dst = torch.where(kept >= 0, lens[:, None] + n, -1)
+        A.cache_move(cache, token_slots(page_table, src, cache.page).contiguous(),
+                     token_slots(page_table, dst, cache.page).contiguous())
+
+
+__all__: Sequence[str] = ["OPQAttention", "token_slots"]

@@ -221,6 +221,25 @@ int opq_cache_read(const opq_cache* cache, int64_t tokens, const int32_t* slots,
                                            static_cast<hipStream_t>(stream)));
 }
 
+int opq_cache_move(const opq_cache* cache, int64_t batch, int64_t count, const int32_t* src,
+                   const int32_t* dst, void* stream) {
+  if (cache_null(cache) || (batch > 0 && count > 0 && (!src || !dst))) return OPQ_ERR_NULL;
+  const opq_cache& c = *cache;
+  if (!cache_shape_ok(c) || batch < 0 || count < 0) return OPQ_ERR_SHAPE;
+  if (!cache_alpha_ok(c)) return OPQ_ERR_ALPHA;
+  if (!cache_aligned(c) || !aligned16(src) || !aligned16(dst)) return OPQ_ERR_ALIGN;
+  if (!format_ok(c.format)) return OPQ_ERR_DTYPE;
+  if (!cache_supported(c) || batch > 65535 || count > opq::kMaxMoves ||
+      !product_within(batch, c.heads, 2, int64_t(1) << 23))
+    return OPQ_ERR_UNSUPPORTED;
+  if (batch == 0 || count == 0 || c.pages == 0) return OPQ_OK;
+  const bool signs = c.format == OPQ_CACHE_OPQ4;
+  const opq::CacheRows side[2] = {{nullptr, 0, 0, c.k, signs ? c.k_sign : nullptr, c.k_scale},
+                                  {nullptr, 0, 0, c.v, signs ? c.v_sign : nullptr, c.v_scale}};
+  return hip_status(opq::launch_cache_move(side, c, batch, count, src, dst,
+                                           static_cast<hipStream_t>(stream)));
+}
+
 static bool attention_shape_ok(int64_t batch, int64_t draft, int64_t heads, int64_t kv_heads,
                                int64_t dim, int64_t max_len) {
   return batch >= 0 && draft >= 0 && heads > 0 && kv_heads > 0 && heads % kv_heads == 0 &&

@@ -60,6 +60,11 @@ hipError_t launch_cache_read(const CacheRows (&side)[2], const opq_cache& c, boo
                              int64_t tokens, const int32_t* slots, const LevelPlanes& lp,
                              hipStream_t stream);
 
+constexpr int64_t kMaxMoves = 128;  // rows that opq_cache_move holds of a sequence and head
+hipError_t launch_cache_move(const CacheRows (&side)[2], const opq_cache& c, int64_t batch,
+                             int64_t count, const int32_t* src, const int32_t* dst,
+                             hipStream_t stream);
+
 // attention.hip
 struct AttentionPlan {
   int tiles;      // 16-row tiles of query rows in a workgroup

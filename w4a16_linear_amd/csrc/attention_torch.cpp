@@ -252,6 +252,23 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// cache, src, dst
+PyObject* cache_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 3);
+  const Cache r = cache_of(a[0]);
+  const Tensor& src = tensor_of(a[1], "src");
+  TORCH_CHECK_VALUE(src.dim() == 2, "src must be [batch, count]");
+  const int64_t batch = src.size(0), count = src.size(1);
+  const void* ps = dense(src, "src", at::kInt, {batch, count}, r.dev);
+  const void* pd = dense(a[2], "dst", at::kInt, {batch, count}, r.dev);
+  const OnDevice on(src);
+  check("opq_cache_move", opq_cache_move(&r.c, batch, count, static_cast<const int32_t*>(ps),
+                                         static_cast<const int32_t*>(pd), on.stream()));
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // --------------------------------------------------------------- attention
 
 // q, cache, page_table, lens, mask|None, counts|None, scale|None, max_len|None, out|None,
@@ -341,6 +358,7 @@ PyObject* set_error(PyObject*, PyObject* type) {
 PyMethodDef kMethods[] = {{"rotary", FAST(rotary), METH_FASTCALL, nullptr},
                           {"cache_write", FAST(cache_write), METH_FASTCALL, nullptr},
                           {"cache_read", FAST(cache_read), METH_FASTCALL, nullptr},
+                          {"cache_move", FAST(cache_move), METH_FASTCALL, nullptr},
                           {"attention", FAST(attention), METH_FASTCALL, nullptr},
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

@@ -360,6 +360,64 @@ __global__ __launch_bounds__(kThreads) void read_rows(ReadArgs a, LevelPlanes lp
     }
 }
 
+struct MoveArgs {
+  CacheRows side[2];
+  const int32_t* src;
+  const int32_t* dst;
+  uint32_t count, heads, slot_end;
+  int page_shift, row_chunks, sign_words;  // of a row: 16-byte chunks of codes, words of signs
+};
+
+// One sequence (blockIdx.x), head (y) and side (z).  All of its rows are in the
+// workgroup's registers before the barrier, and written after it.
+__global__ __launch_bounds__(kThreads) void move_rows(MoveArgs a) {
+  constexpr int kChunks = (int)kMaxMoves * 32 / kThreads, kSigns = (int)kMaxMoves * 8 / kThreads;
+  const int32_t* src = a.src + (int64_t)blockIdx.x * a.count;
+  const int32_t* dst = a.dst + (int64_t)blockIdx.x * a.count;
+  const CacheRows s = blockIdx.z ? a.side[1] : a.side[0];
+  auto row_of = [&](uint32_t slot) {
+    return (((int64_t)(slot >> a.page_shift) * a.heads + blockIdx.y) << a.page_shift) +
+           (slot & ((1u << a.page_shift) - 1u));
+  };
+  // item `e` of `per` a row: its move, or none
+  auto moves = [&](uint32_t e, uint32_t per, int64_t& from, int64_t& to) {
+    const uint32_t i = e / per;
+    if (i >= a.count) return false;
+    const uint32_t f = (uint32_t)src[i], t = (uint32_t)dst[i];
+    if (f >= a.slot_end || t >= a.slot_end) return false;
+    from = row_of(f) * per + (e - i * per);
+    to = row_of(t) * per + (e - i * per);
+    return true;
+  };
+  u32x4_t code[kChunks];
+  uint32_t sign[kSigns];
+  float scale = 0.0f;
+  int64_t from, to;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k)
+    if (moves(threadIdx.x + k * kThreads, a.row_chunks, from, to))
+      code[k] = static_cast<const u32x4_t*>(s.codes)[from];
+  if (s.sign) {
+#pragma unroll
+    for (int k = 0; k < kSigns; ++k)
+      if (moves(threadIdx.x + k * kThreads, a.sign_words, from, to)) sign[k] = s.sign[from];
+  }
+  if (moves(threadIdx.x, 1, from, to)) scale = s.scale[from];
+  // every load has come back before any wave stores
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k)
+    if (moves(threadIdx.x + k * kThreads, a.row_chunks, from, to))
+      static_cast<u32x4_t*>(s.codes)[to] = code[k];
+  if (s.sign) {
+#pragma unroll
+    for (int k = 0; k < kSigns; ++k)
+      if (moves(threadIdx.x + k * kThreads, a.sign_words, from, to)) s.sign[to] = sign[k];
+  }
+  if (moves(threadIdx.x, 1, from, to)) s.scale[to] = scale;
+}
+
 int page_shift_of(int64_t page) {
   int s = 0;
   while ((int64_t(1) << s) < page) ++s;
@@ -458,6 +516,19 @@ hipError_t launch_cache_write(const CacheRows (&side)[2], const opq_cache& c, bo
                               hipStream_t stream) {
   return bf16 ? write_format<uint16_t>(side, c, tokens, slots, cc, stream)
               : write_format<float>(side, c, tokens, slots, cc, stream);
+}
+
+hipError_t launch_cache_move(const CacheRows (&side)[2], const opq_cache& c, int64_t batch,
+                             int64_t count, const int32_t* src, const int32_t* dst,
+                             hipStream_t stream) {
+  const int64_t bytes = c.format == OPQ_CACHE_BF16 ? 2 * c.dim
+                        : c.format == OPQ_CACHE_FP8 ? c.dim : c.dim / 2;
+  const MoveArgs a{{side[0], side[1]}, src, dst, (uint32_t)count, (uint32_t)c.heads,
+                   (uint32_t)(c.pages * c.page), page_shift_of(c.page), (int)(bytes / 16),
+                   (int)(c.dim / 32)};
+  hipLaunchKernelGGL(move_rows, dim3((unsigned)batch, (unsigned)c.heads, 2), dim3(kThreads), 0,
+                     stream, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const CacheRows (&side)[2], const opq_cache& c, bool bf16,
