@@ -212,9 +212,11 @@ size_t opq_cache_attention_workspace_bytes(int64_t batch, int64_t draft, int64_t
  *   lse   device out, dense [batch][draft][heads] float32, or NULL
  *   workspace  at least opq_cache_attention_workspace_bytes(...) bytes, no
  *         initialisation; calls that may overlap need their own
- * Scores, the softmax's maximum and sum, and the accumulators are float32;
- * the weights p v_scale are rounded to bfloat16 for the matrix product with
- * the codes.  Results do not depend on timing and repeat bit for bit.
+ * Scores, the softmax's maximum and sum, and the accumulators are float32.
+ * For the matrix product with the codes the weights p v_scale are rounded to
+ * bfloat16 (with up to 16 query rows a kv head, and for dim 256, on bf16 and fp8
+ * caches: to twice its bits).  Results do not depend on timing and repeat bit for
+ * bit.
  * heads a multiple of kv_heads; batch * draft * heads up to 2^22, batch and heads
  * up to 65535, draft up to 65536 (OPQ_ERR_UNSUPPORTED past them).
  * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALPHA (also scale not finite),

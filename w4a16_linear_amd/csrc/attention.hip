@@ -484,10 +484,12 @@ struct Rows {
   // exceeds max(acc, 0) * scale_top (the largest of kscale): while that stays near
   // the running maximum, the scores themselves are formed only inside the
   // exponent, one fused multiply-add each.
+  // `rest`, where it is asked for (kTwo), is what their rounding to bfloat16 left.
+  template <bool kTwo>
   __device__ __forceinline__ bf16x8_t weigh(const floatx4_t& s0, const floatx4_t& s1,
                                             const floatx4_t (&kscale)[2], float scale_top,
                                             const floatx4_t (&vs)[2], bool masked,
-                                            uint32_t hidden) {
+                                            uint32_t hidden, bf16x8_t& rest) {
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -537,8 +539,18 @@ struct Rows {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) l += e[i];
-    return frag(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]),
-                pack_bf16(w[6], w[7]));
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
+    if (kTwo) {
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = pack_bf16(w[2 * i] - __uint_as_float(p[i] << 16),
+                         w[2 * i + 1] - __uint_as_float(p[i] & 0xFFFF0000u));
+      rest = frag(r[0], r[1], r[2], r[3]);
+    }
+    return frag(p[0], p[1], p[2], p[3]);
   }
 };
 __device__ __forceinline__ float top_of(const floatx4_t (&k)[2]) {
@@ -569,6 +581,10 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
   constexpr int kSteps = D / 32;  // product steps of a score
   constexpr int kTiles = D / 16;  // result tiles, and dimensions of a value lane
   typedef ValueTile<FMT, D> V;
+  // One tile of rows leaves the matrix cores idle: the weights then go in twice, as
+  // their bfloat16 and what that left out, so that only the result is rounded (free
+  // on fp8 and bfloat16 caches; 5 % on OPQ ones, whose 4-bit codes are far coarser).
+  constexpr bool kTwo = NT == 1 && FMT != OPQ_CACHE_OPQ4;
 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave, c = lane & 15, g = lane >> 4;
@@ -631,18 +647,25 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
   }
   for (; kk < k1; kk += kRound) {
     w.load_values();
+    // 2 NT sums side by side: each product of a sum waits for the one before it
     floatx4_t st[2][NT], kscale[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int n = 0; n < NT; ++n) st[u][n] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const bf16x8_t key = w.kt[u].at(s, lut);
+    for (int s = 0; s < kSteps; ++s) {
+      const bf16x8_t key[2] = {w.kt[0].at(s, lut), w.kt[1].at(s, lut)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          st[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key, q_at(n, s), st[u][n], 0, 0, 0);
+      for (int n = 0; n < NT; ++n) {
+        const bf16x8_t query = q_at(n, s);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          st[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key[u], query, st[u][n], 0, 0, 0);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       kscale[u] = w.key_scale(u);
       // made here, before the next step's scales are requested: kept for later, the
       // old and the new scales would change places in registers at the loop's end,
@@ -655,12 +678,13 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
     // masks touch only the steps that reach past the cached tokens
     const bool masked = kk + kStep > (ex.len < k1 ? ex.len : k1);
     const float scale_top = top_of(kscale);
-    bf16x8_t p[NT];
+    bf16x8_t p[NT], rest[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       uint32_t hidden = 0u;
       if (masked) hidden = hidden_keys(a, ex, k.b, token[n], kk, k1, g);
-      p[n] = rows[n].weigh(st[0][n], st[1][n], kscale, scale_top, w.vs, masked, hidden);
+      p[n] = rows[n].template weigh<kTwo>(st[0][n], st[1][n], kscale, scale_top, w.vs, masked, hidden,
+                                          rest[n]);
     }
 #pragma unroll
     for (int t = 0; t < kTiles / V::kTogether; ++t) {
@@ -669,9 +693,11 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<FMT, D, NT>)) void attend(Att
 #pragma unroll
       for (int j = 0; j < V::kTogether; ++j)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          rows[n].o[t * V::kTogether + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              v[j], p[n], rows[n].o[t * V::kTogether + j], 0, 0, 0);
+        for (int n = 0; n < NT; ++n) {
+          floatx4_t& o = rows[n].o[t * V::kTogether + j];
+          if (kTwo) o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[j], rest[n], o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[j], p[n], o, 0, 0, 0);
+        }
     }
   }
 
