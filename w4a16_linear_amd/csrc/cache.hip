@@ -425,7 +425,10 @@ int page_shift_of(int64_t page) {
 }
 
 // Several heads to a group of lanes share one look at the token's slot and keep that
-// many requests in flight; with few rows a head each spreads the launch wider.
+// many requests in flight; with few rows a head each spreads the launch wider.  Rows
+// of 8 heads of 128 from bfloat16, several and one: writing opq4 2048 tokens 8.6 and
+// 7.5 us, 4096 tokens 11.5 and 11.6, 32768 tokens 51 and 58 (fp8 38 and 41, bf16 44
+// and 45); reading opq4 4096 tokens 5.0 and 5.3 us, 32768 tokens 27 and 32.5.
 template <int HPT, typename F>
 hipError_t in_launches(const opq_cache& c, int64_t tokens, F one) {
   // whole tokens per launch, so that its work-items count below 2^31
