@@ -198,7 +198,7 @@ size_t opq_cache_attention_workspace_bytes(int64_t batch, int64_t draft, int64_t
  *   q     device, [batch][draft][heads][dim] bfloat16, strides in elements,
  *         multiples of 8; 16-byte aligned
  *   page_table  device, [batch][max_pages] int32; entries past a sequence's
- *         tokens are not read.  A page id outside the cache makes its tokens' keys
+ *         tokens are not used.  A page id outside the cache makes its tokens' keys
  *         and values NaN
  *   lens  device, [batch] int32; counts: device, [batch] int32 or NULL: how many of
  *         the drafted tokens count (rows past it get out 0 and lse -infinity).

@@ -181,6 +181,29 @@ def test_long_prompt_and_other_stream(gpu_lib):
         assert (off <= step * (top if fmt == "opq4" else k.float().abs()) + 2.0 ** -9 * top).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
+@pytest.mark.parametrize("dim,tokens", [(64, 9500), (128, 4801), (256, 2402)])
+def test_large_calls_equal_small_ones(gpu_lib, fmt, dim, tokens):
+    """Enough rows for several heads a group of lanes, with a number of heads that is no
+    multiple of theirs: the same bits as tokens written and read a few at a time."""
+    heads, page = 7, 32
+    k, v = (torch.randn(tokens, heads, dim, device=DEV).bfloat16() for _ in range(2))
+    slots = torch.randperm(-(-tokens // page) * page, device=DEV)[:tokens].to(torch.int32)
+    slots[100:200] = -1
+    a, b = (A.new_cache(-(-tokens // page), heads, page, dim, fmt, device=DEV) for _ in range(2))
+    A.cache_write(a, k, v, slots)
+    for part in torch.arange(tokens, device=DEV).split(1200):
+        A.cache_write(b, k[part], v[part], slots[part])
+    for s, t in zip(a[2:], b[2:]):
+        assert s is None or torch.equal(s.view(torch.uint8), t.view(torch.uint8))
+    for dtype in (torch.bfloat16, torch.float32):
+        whole = A.cache_read(a, slots, dtype)
+        parts = [A.cache_read(a, slots[part], dtype) for part in torch.arange(tokens, device=DEV).split(1200)]
+        for i in range(2):
+            assert torch.equal(whole[i], torch.cat([q[i] for q in parts]))
+            assert not whole[i][100:200].any()
+
+
 def test_refusals_and_empty(gpu_lib):
     cache = A.new_cache(2, 2, 16, 64, "fp8", device=DEV)
     k = torch.zeros(3, 2, 64, device=DEV)

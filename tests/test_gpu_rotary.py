@@ -70,6 +70,25 @@ def test_strides_and_alignment(gpu_lib, layout, dtype, offset, token_pad, head_p
     _check(view, before[offset:].as_strided((tokens, heads, dim), (ts, hs, 1)), pos, table, layout, (32,))
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_large_calls(gpu_lib, layout, dtype, offset):
+    """Enough work for several heads a thread, a number of heads that is no multiple of
+    theirs, a part of the head that is copied; aligned and not, apart and in place."""
+    tokens, heads, dim, rot = 601, 53, 128, 64
+    rng = np.random.default_rng(7 + offset)
+    table = _table(rng, 40, rot // 2)
+    pos = rng.integers(0, 40, (tokens, 1)).astype(np.int32)
+    flat = torch.from_numpy(rng.standard_normal(offset + tokens * heads * dim).astype(np.float32)).to(DEV, dtype)
+    x = flat[offset:].view(tokens, heads, dim)
+    t, p = torch.from_numpy(table).to(DEV), torch.from_numpy(pos).to(DEV)
+    y = A.rotary(x, p, t, layout)
+    _check(y, x, pos, table, layout, (rot // 2,))
+    A.rotary(x, p, t, layout, out=x)
+    assert torch.equal(x, y)
+
+
 def test_broadcast_head(gpu_lib):
     """A head seen by all (stride 0) is read once per head; its gradient is the sum."""
     rng = np.random.default_rng(4)

@@ -140,6 +140,16 @@ def test_split_over_workgroups(gpu_lib, fmt, page):
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "opq4"])
+@pytest.mark.parametrize("dim,draft", [(64, 1), (128, 1), (256, 1), (128, 9)])
+def test_many_pieces(gpu_lib, fmt, dim, draft):
+    """A sequence in more pieces than a wave joins at once, beside one with fewer."""
+    lens = [12001, 4097]
+    p = Problem(dim + draft, fmt, dim, 6, 1, lens, draft, page=64)
+    out, lse = A.tree_attention(p.q, p.cache, p.table, p.lens_t, return_lse=True)
+    p.check(out, lse, _chain(2, draft))
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
 def test_counts(gpu_lib, fmt):
     lens, draft, counts = [5, 40, 0, 2000, 9], 7, [0, 3, 2, 7, 1]
