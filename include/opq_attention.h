@@ -13,7 +13,8 @@
  *   - queries, keys and values may be cut from a fused projection: their token
  *     and head strides are free (also 0), and the pointers of opq_rotary and
  *     opq_cache_write need only their element's alignment (16-byte aligned
- *     ones run wider loads).  Every other array is 16-byte aligned;
+ *     ones run wider loads).  Index arrays, masks and lse are 4-byte aligned
+ *     (they may start inside a longer array), every other array 16-byte;
  *   - indexes that kernels read from device memory (positions, slots, page
  *     ids, lengths) are checked against their arrays inside the kernels: what
  *     an invalid one does is stated at the call, and no access leaves an array.

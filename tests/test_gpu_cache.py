@@ -181,6 +181,20 @@ def test_long_prompt_and_other_stream(gpu_lib):
         assert (off <= step * (top if fmt == "opq4" else k.float().abs()) + 2.0 ** -9 * top).all()
 
 
+def test_slots_that_start_inside_an_array(gpu_lib):
+    a, b = (A.new_cache(2, 3, 16, 64, "fp8", device=DEV) for _ in range(2))
+    x = torch.randn(20, 3, 64, device=DEV)
+    slots = torch.randperm(32, device=DEV)[:21].to(torch.int32)
+    A.cache_write(a, x, x, slots[1:])
+    A.cache_write(b, x, x, slots[1:].clone())
+    assert torch.equal(a.k.view(torch.uint8), b.k.view(torch.uint8)) and torch.equal(a.v_scale, b.v_scale)
+    for s, t in zip(A.cache_read(a, slots[3:]), A.cache_read(a, slots[3:].clone())):
+        assert torch.equal(s, t)
+    A.cache_move(a, slots[None, 1:4], slots[None, 5:8])
+    A.cache_move(b, slots[None, 1:4].clone(), slots[None, 5:8].clone())
+    assert torch.equal(a.k.view(torch.uint8), b.k.view(torch.uint8)) and torch.equal(a.v_scale, b.v_scale)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
 @pytest.mark.parametrize("dim,tokens", [(64, 9500), (128, 4801), (256, 2402)])
 def test_large_calls_equal_small_ones(gpu_lib, fmt, dim, tokens):

@@ -89,6 +89,13 @@ def test_large_calls(gpu_lib, layout, dtype, offset):
     assert torch.equal(x, y)
 
 
+def test_positions_that_start_inside_an_array(gpu_lib):
+    table = torch.from_numpy(_table(np.random.default_rng(3), 30, 32)).to(DEV)
+    pos = torch.arange(29, -1, -1, dtype=torch.int32, device=DEV)
+    x = torch.randn(30, 2, 64, device=DEV)
+    assert torch.equal(A.rotary(x[3:], pos[3:], table), A.rotary(x, pos, table)[3:])
+
+
 def test_broadcast_head(gpu_lib):
     """A head seen by all (stride 0) is read once per head; its gradient is the sum."""
     rng = np.random.default_rng(4)

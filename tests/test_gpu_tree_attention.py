@@ -295,6 +295,20 @@ def test_long_cache_past_32_bits(gpu_lib, fmt):
     del cache
 
 
+def test_index_arrays_that_start_inside_others(gpu_lib):
+    """A part of a batch, its arrays sliced: the rows of the whole batch's result."""
+    lens, draft = [70, 33, 200], 5
+    p = Problem(77, "fp8", 64, 4, 2, lens, draft)
+    seen = p.rng.random((3, draft, draft)) < 0.5
+    words, counts = _words(seen), torch.tensor([5, 3, 4], dtype=torch.int32, device=DEV)
+    out, lse = A.tree_attention(p.q, p.cache, p.table, p.lens_t, words, counts, return_lse=True)
+    p.check(out, lse, seen, counts.tolist())
+    for b in (1, 2):
+        part, part_lse = A.tree_attention(p.q[b:], p.cache, p.table[b:], p.lens_t[b:], words[b:], counts[b:],
+                                          return_lse=True)
+        assert torch.equal(part, out[b:]) and torch.equal(part_lse, lse[b:])
+
+
 def test_another_stream_and_graph(gpu_lib):
     """Captured once and replayed with eager work between: every replay equals the eager call,
     and follows lengths changed in place."""

@@ -18,6 +18,7 @@ constexpr int64_t kMaxElements = int64_t(1) << 39;
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool aligned4(const void* p) { return aligned(p, 4); }
 bool aligned16(const void* p) { return aligned(p, 16); }
 int hip_status(hipError_t e) { return e == hipSuccess ? OPQ_OK : OPQ_ERR_HIP; }
 bool dtype_ok(int d) { return d == OPQ_F32 || d == OPQ_BF16; }
@@ -143,7 +144,7 @@ int opq_rotary(const void* x, int dtype, int64_t tokens, int64_t heads, int64_t 
   }
   if (end != rot / 2) return OPQ_ERR_SHAPE;
   const uintptr_t element = dtype == OPQ_F32 ? 4 : 2;
-  if (!aligned(x, element) || !aligned(out, element) || !aligned16(positions) || !aligned16(table))
+  if (!aligned(x, element) || !aligned(out, element) || !aligned4(positions) || !aligned16(table))
     return OPQ_ERR_ALIGN;
   if (!dtype_ok(dtype) || (layout != OPQ_ROTARY_HALF && layout != OPQ_ROTARY_INTERLEAVED))
     return OPQ_ERR_DTYPE;
@@ -179,7 +180,7 @@ int opq_cache_write(const opq_cache* cache, const void* k, int64_t k_token_strid
   if (!cache_shape_ok(c) || tokens < 0) return OPQ_ERR_SHAPE;
   if (!cache_alpha_ok(c)) return OPQ_ERR_ALPHA;
   const uintptr_t element = dtype == OPQ_F32 ? 4 : 2;
-  if (!cache_aligned(c) || !aligned(k, element) || !aligned(v, element) || !aligned16(slots))
+  if (!cache_aligned(c) || !aligned(k, element) || !aligned(v, element) || !aligned4(slots))
     return OPQ_ERR_ALIGN;
   if (!dtype_ok(dtype) || !format_ok(c.format)) return OPQ_ERR_DTYPE;
   if (!cache_supported(c) || !product_within(tokens, c.heads, 1, kMaxInt))
@@ -207,7 +208,7 @@ int opq_cache_read(const opq_cache* cache, int64_t tokens, const int32_t* slots,
   const opq_cache& c = *cache;
   if (!cache_shape_ok(c) || tokens < 0) return OPQ_ERR_SHAPE;
   if (!cache_alpha_ok(c)) return OPQ_ERR_ALPHA;
-  if (!cache_aligned(c) || !aligned16(k_out) || !aligned16(v_out) || !aligned16(slots))
+  if (!cache_aligned(c) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(slots))
     return OPQ_ERR_ALIGN;
   if (!dtype_ok(dtype) || !format_ok(c.format)) return OPQ_ERR_DTYPE;
   if (!cache_supported(c) || !product_within(tokens, c.heads, 1, kMaxInt))
@@ -227,7 +228,7 @@ int opq_cache_move(const opq_cache* cache, int64_t batch, int64_t count, const i
   const opq_cache& c = *cache;
   if (!cache_shape_ok(c) || batch < 0 || count < 0) return OPQ_ERR_SHAPE;
   if (!cache_alpha_ok(c)) return OPQ_ERR_ALPHA;
-  if (!cache_aligned(c) || !aligned16(src) || !aligned16(dst)) return OPQ_ERR_ALIGN;
+  if (!cache_aligned(c) || !aligned4(src) || !aligned4(dst)) return OPQ_ERR_ALIGN;
   if (!format_ok(c.format)) return OPQ_ERR_DTYPE;
   if (!cache_supported(c) || batch > 65535 || count > opq::kMaxMoves ||
       !product_within(batch, c.heads, 2, int64_t(1) << 23))
@@ -274,8 +275,8 @@ int opq_cache_attention(const opq_cache* cache, const uint16_t* q, int64_t batch
       max_len > max_pages * c.page || mask_batch_stride < 0)
     return OPQ_ERR_SHAPE;
   if (!cache_alpha_ok(c) || !std::isfinite(scale)) return OPQ_ERR_ALPHA;
-  if (!cache_aligned(c) || !aligned16(q) || !aligned16(page_table) || !aligned16(lens) ||
-      !aligned16(counts) || !aligned16(mask) || !aligned16(out) || !aligned16(lse) ||
+  if (!cache_aligned(c) || !aligned16(q) || !aligned4(page_table) || !aligned4(lens) ||
+      !aligned4(counts) || !aligned4(mask) || !aligned16(out) || !aligned4(lse) ||
       !aligned16(workspace) || q_batch_stride % 8 || q_token_stride % 8 || q_head_stride % 8)
     return OPQ_ERR_ALIGN;
   if (!format_ok(c.format)) return OPQ_ERR_DTYPE;

@@ -10,9 +10,13 @@
 // A row with a NaN or an infinity gets scale NaN and codes 0.
 //
 // A group of dim/8 lanes holds a row, eight values a lane (16 bytes of bf16), so
-// the maximum is a few lane exchanges and nothing is read twice.  Bound by
-// memory for long prompts (2 bytes in, 0.66 to 2 out per value), by the launch for a
-// few tokens.
+// the maximum is a few lane exchanges and nothing is read twice.  With few tokens
+// the launch bounds both ways (48 tokens of 8 heads of 128, fp8: 2.8 us to write, 2.5
+// to read).  Reading long histories is bound by memory: 131072 tokens of 8 heads of 128
+// from opq4, 133 us, 5.3 TB/s.  Writing 16384 such tokens takes 30 us for opq4, bound
+// by the VALU (a logarithm and an exponential, each four issue slots, of some twenty
+// a value); fp8 and bf16 are near memory's bound (32768 tokens: 38 and 45 us, 5.4 and
+// 6.0 TB/s).
 #include "attention_internal.hpp"
 #include "decode.hpp"
 
@@ -369,7 +373,9 @@ struct MoveArgs {
 };
 
 // One sequence (blockIdx.x), head (y) and side (z).  All of its rows are in the
-// workgroup's registers before the barrier, and written after it.
+// workgroup's registers before the barrier, and written after it.  A few KB a
+// workgroup: the launch and two trips to memory bound it (32 sequences,
+// 8 rows of 8 heads each: 4 us).
 __global__ __launch_bounds__(kThreads) void move_rows(MoveArgs a) {
   constexpr int kChunks = (int)kMaxMoves * 32 / kThreads, kSigns = (int)kMaxMoves * 8 / kThreads;
   const int32_t* src = a.src + (int64_t)blockIdx.x * a.count;
