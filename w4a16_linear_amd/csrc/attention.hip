@@ -38,7 +38,10 @@
 // 21 tokens each, fp8: 23 us.  One sequence of 1000 tokens: 6 us, two launches.
 //
 // Measured and not taken: waves that share decoded keys in LDS and split the rows
-// (4 or 8 waves, 91 to 146 us where this takes 70 to 98).
+// (4 or 8 waves, 91 to 146 us where this takes 70 to 98); four tiles of rows to a
+// workgroup, one workgroup a CU (the trees above: 91 us, and 94 for 67 from an fp8
+// cache); the product with the values after the next step's scores, so that values have
+// longer to arrive (trees 92 us, the batch above 71 for 65: registers for it cost waves).
 #include "attention_internal.hpp"
 #include "decode.hpp"
 

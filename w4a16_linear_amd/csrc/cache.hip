@@ -13,10 +13,9 @@
 // the maximum is a few lane exchanges and nothing is read twice.  With few tokens
 // the launch bounds both ways (48 tokens of 8 heads of 128, fp8: 2.8 us to write, 2.5
 // to read).  Reading long histories is bound by memory: 131072 tokens of 8 heads of 128
-// from opq4, 133 us, 5.3 TB/s.  Writing 16384 such tokens takes 30 us for opq4, bound
-// by the VALU (a logarithm and an exponential, each four issue slots, of some twenty
-// a value); fp8 and bf16 are near memory's bound (32768 tokens: 38 and 45 us, 5.4 and
-// 6.0 TB/s).
+// from opq4, 133 us, 5.3 TB/s.  Writing 32768 such tokens takes 47 us for opq4 (3.8
+// TB/s), bound by the VALU (a logarithm and an exponential, each four issue slots, of
+// some twenty a value); fp8 and bf16 by memory: 37 and 41 us, 5.5 and 6.6 TB/s.
 #include "attention_internal.hpp"
 #include "decode.hpp"
 
@@ -123,27 +122,24 @@ __device__ uint32_t code_exact(float a, float m, const CacheCodes& cc) {
 // Nibbles of eight magnitudes.  15 u^alpha comes from the hardware's log2 and exp2
 // on |x| * fl(1/m): its error is far below cc.guard, so the nearest integer is the
 // exact code unless a half-integer is within the guard; those few (and every row
-// whose 1/m is not a normal number) are decided by code_exact.
+// whose 1/m is not a normal number) are decided by code_exact.  The conversion to
+// a byte rounds to nearest; codes gather in bytes, which costs an instruction a value
+// less than shifting nibbles together (16384 tokens of 8 heads of 128: 27 us, 30).
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float m, const CacheCodes& cc) {
   constexpr float kLog15 = 3.90689059560851853f;
   const float r = __builtin_amdgcn_rcpf(m);
-  uint32_t word = 0u;
-  float low = 1.0f, high = 0.0f;  // of the distances above the half-integer below
-  auto code = [&](float v, float& f) {
-    const float lg = __builtin_amdgcn_logf(fabsf(v) * r);
-    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(cc.alpha, lg, kLog15)) + 0.5f;
-    f = __builtin_amdgcn_fractf(p);
-    return (uint32_t)p;
-  };
+  uint32_t even = 0u, odd = 0u;  // codes 0 2 4 6 and 1 3 5 7, a byte each
+  float nearest = 1.0f;          // smallest distance from a half-integer
 #pragma unroll
-  for (int i = 7; i >= 0; i -= 2) {
-    float f0, f1;
-    word = (word << 4) + code(x[i], f0);
-    word = (word << 4) + code(x[i - 1], f1);
-    low = fminf(low, fminf(f0, f1));
-    high = fmaxf(high, fmaxf(f0, f1));
+  for (int i = 0; i < 8; ++i) {
+    const float lg = __builtin_amdgcn_logf(fabsf(x[i]) * r);
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(cc.alpha, lg, kLog15));
+    nearest = fminf(nearest, fabsf(__builtin_amdgcn_fractf(p) - 0.5f));
+    uint32_t& bytes = i & 1 ? odd : even;
+    bytes = __builtin_amdgcn_cvt_pk_u8_f32(p, i >> 1, bytes);
   }
-  if (!(low > cc.guard && high < 1.0f - cc.guard && r >= 0x1p-126f)) {
+  uint32_t word = even | odd << 4;
+  if (!(nearest > cc.guard && r >= 0x1p-126f)) {
     word = 0u;
 #pragma unroll 1
     for (int i = 7; i >= 0; --i) {
@@ -239,15 +235,18 @@ __device__ __forceinline__ void write_row(const Eight<T>& raw, const CacheRows& 
 }
 
 // A group of dim/8 lanes: HPT heads of one token, of keys (blockIdx.y = 0) or
-// values (1).
+// values (1).  A workgroup's groups are consecutive tokens of the same heads: a page
+// keeps a head's tokens together, so codes, signs and scales leave as runs and not
+// as lines that several XCDs write parts of (32768 tokens of 8 heads of 128, bf16:
+// 41 us, 44 with consecutive heads; 5 heads, opq4: 33 and 39).
 template <typename T, int FMT, int D, int HPT>
 __global__ __launch_bounds__(kThreads) void write_rows(WriteArgs a, CacheCodes cc) {
   constexpr int kLanes = D / 8;
-  const uint32_t group = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / kLanes;
   const int lane = threadIdx.x % kLanes;
-  const uint32_t per = (a.heads + HPT - 1) / HPT, token = group / per;
+  const uint32_t per = (a.heads + HPT - 1) / HPT, tile = blockIdx.x / per;
+  const uint32_t token = tile * (kThreads / kLanes) + threadIdx.x / kLanes;
   if (token >= a.tokens) return;  // whole groups of lanes
-  const uint32_t head = (group - token * per) * HPT;
+  const uint32_t head = (blockIdx.x - tile * per) * HPT;
   const uint32_t slot = (uint32_t)a.slots[token];
   const CacheRows s = blockIdx.y ? a.side[1] : a.side[0];
   const T* x = static_cast<const T*>(s.x) + token * s.token_stride + lane * 8;
@@ -430,24 +429,20 @@ int page_shift_of(int64_t page) {
   return s;
 }
 
-// Several heads to a group of lanes share one look at the token's slot and keep that
-// many requests in flight; with few rows a head each spreads the launch wider.  Rows
-// of 8 heads of 128 from bfloat16, several and one: writing opq4 2048 tokens 8.6 and
-// 7.5 us, 4096 tokens 11.5 and 11.6, 32768 tokens 51 and 58 (fp8 38 and 41, bf16 44
-// and 45); reading opq4 4096 tokens 5.0 and 5.3 us, 32768 tokens 27 and 32.5.
-template <int HPT, typename F>
-hipError_t in_launches(const opq_cache& c, int64_t tokens, F one) {
-  // whole tokens per launch, so that its work-items count below 2^31
-  const int64_t per = (c.heads + HPT - 1) / HPT * (c.dim / 8);
-  const int64_t step = (kMaxLaunchThreads - kThreads) / per;
+template <typename F>
+hipError_t in_launches(int64_t tokens, int64_t step, F one) {
   for (int64_t t0 = 0; t0 < tokens; t0 += step) {
-    const int64_t n = tokens - t0 < step ? tokens - t0 : step;
-    one(t0, n, dim3((unsigned)((n * per + kThreads - 1) / kThreads), 2));
+    one(t0, tokens - t0 < step ? tokens - t0 : step);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
+// Several heads to a group of lanes (two to write, four to read) share one look at the
+// token's slot and keep that many requests in flight; with few rows a head each spreads
+// the launch wider.  Rows of 8 heads of 128 from bfloat16, several and one: writing opq4
+// 512 tokens 6.1 and 5.0 us, 4096 tokens 10.4 and 10.5, 32768 tokens 47 and 53 (fp8 37
+// and 40, bf16 41 and 43); reading opq4 4096 tokens 4.4 and 5.0, 32768 tokens 28 and 33.
 bool many_rows(const opq_cache& c, int64_t tokens) {
   return tokens * c.heads * (c.dim / 8) >= int64_t(1) << 19;
 }
@@ -460,7 +455,10 @@ hipError_t write_all(const CacheRows (&side)[2], const opq_cache& c, int64_t tok
     wide = wide && reinterpret_cast<uintptr_t>(s.x) % 16 == 0 &&
            s.token_stride % (int64_t)(16 / sizeof(T)) == 0 &&
            s.head_stride % (int64_t)(16 / sizeof(T)) == 0;
-  return in_launches<HPT>(c, tokens, [&](int64_t t0, int64_t n, dim3 grid) {
+  // whole tiles of tokens per launch, so that its work-items count below 2^31
+  const int64_t per = (c.heads + HPT - 1) / HPT, tile = kThreads / (D / 8);
+  return in_launches(tokens, kMaxLaunchThreads / kThreads / per * tile, [&](int64_t t0, int64_t n) {
+    const dim3 grid((unsigned)((n + tile - 1) / tile * per), 2);
     WriteArgs a{{side[0], side[1]}, slots + t0, (uint32_t)n, (uint32_t)c.heads,
                 (uint32_t)(c.pages * c.page), page_shift_of(c.page), wide};
     for (CacheRows& s : a.side) s.x = static_cast<const T*>(s.x) + t0 * s.token_stride;
@@ -471,7 +469,10 @@ hipError_t write_all(const CacheRows (&side)[2], const opq_cache& c, int64_t tok
 template <typename T, int FMT, int D, int HPT>
 hipError_t read_all(const CacheRows (&side)[2], const opq_cache& c, int64_t tokens,
                     const int32_t* slots, const LevelPlanes& lp, hipStream_t stream) {
-  return in_launches<HPT>(c, tokens, [&](int64_t t0, int64_t n, dim3 grid) {
+  // whole tokens per launch, so that its work-items count below 2^31
+  const int64_t per = (c.heads + HPT - 1) / HPT * (D / 8);
+  return in_launches(tokens, (kMaxLaunchThreads - kThreads) / per, [&](int64_t t0, int64_t n) {
+    const dim3 grid((unsigned)((n * per + kThreads - 1) / kThreads), 2);
     ReadArgs a{{side[0], side[1]}, slots + t0, (uint32_t)n, (uint32_t)c.heads,
                (uint32_t)(c.pages * c.page), page_shift_of(c.page)};
     for (CacheRows& s : a.side)
