@@ -213,7 +213,9 @@ size_t opq_cache_attention_workspace_bytes(int64_t batch, int64_t draft, int64_t
  *   lse   device out, dense [batch][draft][heads] float32, or NULL
  *   workspace  at least opq_cache_attention_workspace_bytes(...) bytes, no
  *         initialisation; calls that may overlap need their own
- * Scores, the softmax's maximum and sum, and the accumulators are float32.
+ * Scores, the softmax's maximum and sum, and the accumulators are float32.  The
+ * accumulators are divided by the weights' sum at the end, and weights are at
+ * most 1: values of up to 2^127 divided by the number of keys cannot overflow.
  * For the matrix product with the codes the weights p v_scale are rounded to
  * bfloat16 (with up to 16 query rows a kv head, and for dim 256, on bf16 and fp8
  * caches: to twice its bits).  Results do not depend on timing and repeat bit for

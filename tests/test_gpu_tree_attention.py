@@ -140,6 +140,26 @@ def test_split_over_workgroups(gpu_lib, fmt, page):
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
+@pytest.mark.parametrize("draft", [1, 20])
+def test_values_near_the_largest(gpu_lib, fmt, draft):
+    """Powers of two pass through: values 2^118 times as large give exactly that much larger
+    results (no weight exceeds 1, so hundreds of keys leave the sums within float32)."""
+    n, dim, page = 500, 64, 16
+    k, v = (torch.randn(n + draft, 2, dim, device=DEV).clamp(-3, 3) for _ in range(2))
+    k = k * 0.1
+    q = torch.randn(1, draft, 4, dim, device=DEV).bfloat16()
+    ids = torch.arange(-(-(n + draft) // page), dtype=torch.int32, device=DEV)
+    slots = torch.arange(n + draft, dtype=torch.int32, device=DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    out = []
+    for grow in (1.0, 2.0 ** 118):
+        cache = A.new_cache(len(ids), 2, page, dim, fmt, device=DEV)
+        A.cache_write(cache, k, v * grow, slots)
+        out.append(A.tree_attention(q, cache, ids[None], lens).float())
+    assert torch.isfinite(out[1]).all() and torch.equal(out[0] * 2.0 ** 118, out[1])
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "opq4"])
 @pytest.mark.parametrize("dim,draft", [(64, 1), (128, 1), (256, 1), (128, 9)])
 def test_many_pieces(gpu_lib, fmt, dim, draft):

@@ -53,9 +53,10 @@ constexpr int kThreads = kWaves * kWave;
 constexpr int kStep = 32;             // keys a wave takes at a time
 constexpr int kRound = kWaves * kStep;  // keys a workgroup takes at a time
 constexpr float kLowest = -3.0e38f;     // running maximum of a row that saw nothing
-// The maximum is raised only when a score exceeds it by more than this (in powers
-// of two): the weights then stay below 2^8, which float32 sums and bfloat16
-// weights hold as well as weights below 1, and most steps skip the rescaling.
+// The running maximum is kept this much (in powers of two) above the largest score seen
+// when it was last raised, and raised again only when a score exceeds it: no weight
+// exceeds 1, float32 sums and bfloat16 weights hold weights of 2^-8 as well as of 1,
+// and most steps skip the rescaling.
 constexpr float kSlack = 8.0f;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -494,7 +495,7 @@ struct Rows {
   }
   // Takes the products of 32 keys in and gives their weights, times the values'
   // scales, as the B operand of the second product.  No score of the lane's keys
-  // exceeds max(acc, 0) * scale_top (the largest of kscale): while that stays near
+  // exceeds max(acc, 0) * scale_top (the largest of kscale): while that stays below
   // the running maximum, the scores themselves are formed only inside the
   // exponent, one fused multiply-add each.
   // `rest`, where it is asked for (kTwo), is what their rounding to bfloat16 left.
@@ -512,7 +513,7 @@ struct Rows {
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = fmaxf(most, acc[i]);
-    if (__builtin_amdgcn_ballot_w64(most * scale_top > m + kSlack)) {
+    if (__builtin_amdgcn_ballot_w64(most * scale_top > m)) {
       float top = kLowest;
       // an opaque copy, here and below: the tests of its bits stay on these rare ways
       uint32_t h = hidden;
@@ -522,10 +523,10 @@ struct Rows {
         const float s = acc[i] * kscale[i >> 2][i & 3];
         top = fmaxf(top, (h >> i) & 1u ? kLowest : s);
       }
-      if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+      if (__builtin_amdgcn_ballot_w64(top > m)) {
         top = fmaxf(top, __shfl_xor(top, 16, kWave));
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        const float raised = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - raised);
+        const float raised = fmaxf(m, top + kSlack), f = __builtin_amdgcn_exp2f(m - raised);
         m = raised;
         l *= f;
 #pragma unroll
