@@ -213,7 +213,9 @@ size_t opq_cache_attention_workspace_bytes(int64_t batch, int64_t draft, int64_t
  *   lse   device out, dense [batch][draft][heads] float32, or NULL
  *   workspace  at least opq_cache_attention_workspace_bytes(...) bytes, no
  *         initialisation; calls that may overlap need their own
- * Scores, the softmax's maximum and sum, and the accumulators are float32.  The
+ * Scores, the softmax's maximum and sum, and the accumulators are float32; scores may
+ * be as large as float32 holds (past 2^26 they are rounded to it before they are
+ * compared, so what differs by less counts as equal or as whole steps apart).  The
  * accumulators are divided by the weights' sum at the end, and weights are at
  * most 1: values of up to 2^127 divided by the number of keys cannot overflow.
  * For the matrix product with the codes the weights p v_scale are rounded to

@@ -370,3 +370,41 @@ def test_refusals_and_empty(gpu_lib):
                 dict(q=p.q.transpose(2, 3))):
         with pytest.raises(ValueError):
             A.tree_attention(**{**args, **bad})
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
+@pytest.mark.parametrize("draft", [1, 20])
+@pytest.mark.parametrize("power", [20, 27, 33, 100])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_large_scores(gpu_lib, fmt, draft, power, sign):
+    """Scores around +-2^power, so far apart that one key takes all: its value comes out,
+    with its score as the log-sum, however coarse float32 is there.  Keys w_j p, queries
+    +-2^power p / dim for a pattern p of signs: the products and their sum are exact but for
+    the stored w_j."""
+    lens, dim, heads, kv = [0, 1, 300, 5000], 64, 4, 2
+    p = Problem(power + draft, fmt, dim, heads, kv, lens, draft, page=64)
+    pattern = p.rng.choice([-1.0, 1.0], dim)
+    for b, n in enumerate(lens):
+        step = np.concatenate([p.rng.integers(70, 117, n), 10 + p.rng.permutation(draft)])
+        if n > 1:
+            step[p.rng.permutation(n)[:2]] = 1, 124           # the prefix's only least and only largest
+        keys = (0.5 + step[:, None] / 256.0) * pattern
+        x = torch.from_numpy(np.repeat(keys[:, None], kv, 1).astype(np.float32)).to(DEV)
+        slots = torch.tensor([p.slots_of(b, a) for a in range(n + draft)], dtype=torch.int32, device=DEV)
+        A.cache_write(p.cache, x, torch.from_numpy(p.values[b]).float().to(DEV), slots)
+        k, v = A.cache_read(p.cache, slots, torch.float32)
+        p.keys[b], p.values[b] = k.double().cpu().numpy(), v.double().cpu().numpy()
+    q = torch.from_numpy(sign * 2.0 ** power / dim * pattern).to(DEV, torch.bfloat16).expand(4, draft, heads, dim)
+    out, lse = A.tree_attention(q.contiguous(), p.cache, p.table, p.lens_t, scale=1.0, return_lse=True)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        for t in range(draft):
+            for h in range(heads):
+                s = p.keys[b][:n + t + 1, h // 2] @ (sign * 2.0 ** power / dim * pattern)
+                best = int(s.argmax())
+                assert len(s) == 1 or s[best] - np.partition(s, -2)[-2] > 100.0
+                v = p.values[b][best, h // 2]
+                # the weight rounded to bfloat16, the result rounded to bfloat16
+                assert (np.abs(out[b, t, h] - v) <= 2.02 * UBF * np.abs(v)).all(), (b, t, h)
+                # dim products summed in float32, two scalings, the factor ln 2
+                assert abs(lse[b, t, h] - s[best]) <= (dim + 16) * 2 * U32 * abs(s[best]), (b, t, h)
