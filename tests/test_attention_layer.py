@@ -1,0 +1,40 @@
+"""CPU tests of the attention layer's host parts: cache slots of positions, what a forward
+refuses before anything is enqueued."""
+import numpy as np
+import pytest
+import torch
+
+from w4a16_linear_amd.attention_module import OPQAttention, token_slots
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+# ------------------------------------------------------------------ slots
+
+@pytest.mark.parametrize("page", [16, 64, 1024])
+def test_slots_equal_their_definition(page):
+    rng = np.random.default_rng(page)
+    pages = 50
+    table = rng.permutation(pages)[:24].reshape(3, 8).astype(np.int32)
+    table[1, 2], table[2, 0], table[0, 7] = -1, pages, 2 ** 31 - 1
+    pos = rng.integers(-page, 9 * page, (3, 200)).astype(np.int32)
+    want = np.full(pos.shape, -1)
+    for b in range(3):
+        for i, p in enumerate(pos[b]):
+            if 0 <= p < 8 * page and 0 <= table[b, p // page] < pages:
+                want[b, i] = int(table[b, p // page]) * page + p % page
+    got = token_slots(torch.from_numpy(table), torch.from_numpy(pos), page, pages)
+    assert got.dtype == torch.int32 and np.array_equal(got.numpy(), want)
+
+
+@pytest.mark.parametrize("pages", [None, 100])
+@pytest.mark.parametrize("page,ids", [(64, 2 ** 26), (64, -2 ** 31), (64, 2 ** 26 + 3), (64, 2 ** 25), (64, 2 ** 31 - 1),
+                                      (1024, 2 ** 22), (1024, -2 ** 31 + 5), (1024, 2 ** 21), (16, 2 ** 28 + 1), (16, -1)])
+def test_a_page_id_outside_every_cache_names_no_slot(page, ids, pages):
+    """Also where id * page + offset wraps around to a small number in 32 bits; a cache holds
+    fewer than 2^31 tokens, so an id of 2^31 / page or more is outside whatever its size."""
+    pos = _i32([[0, 1, page - 1, page, page + 1, 3 * page - 1]])
+    got = token_slots(_i32([[ids, ids, ids]]), pos, page, pages)
+    assert (got == -1).all()

@@ -169,3 +169,22 @@ def test_layer_refusals():
     for bad in (dict(heads=4, kv_heads=3, dim=64), dict(heads=4, dim=80)):
         with pytest.raises(ValueError):
             OPQAttention(256, **bad)
+
+
+@pytest.mark.parametrize("bad", [2 ** 28, -2 ** 31, 2 ** 28 + 1, 4, -1])
+def test_a_page_outside_the_cache_leaves_the_others_alone(gpu_lib, bad):
+    """Page ids that wrap around to pages 0 and 1 in 32 bits, and ids just outside: nothing of
+    another sequence is written over, by a forward or by accept."""
+    layer = _layer(11)
+    cache = layer.new_cache(4, 16, "fp8", device=DEV)
+    good = torch.tensor([[0, 1]], dtype=torch.int32, device=DEV)
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    layer(torch.randn(1, 32, 256, device=DEV).bfloat16(), cache, good, zero)
+    before = [t.view(torch.uint8).clone() for t in cache[2:] if t is not None]
+    table = torch.full((1, 2), bad, dtype=torch.int32, device=DEV)
+    layer(torch.randn(1, 20, 256, device=DEV).bfloat16(), cache, table, zero)
+    layer.accept(cache, table, zero, torch.tensor([[3, 5, 18]], dtype=torch.int32, device=DEV))
+    mixed = torch.tensor([[0, bad]], dtype=torch.int32, device=DEV)
+    layer.accept(cache, mixed, zero + 10, torch.tensor([[-1, 8, 9]], dtype=torch.int32, device=DEV))
+    for t, b in zip((t for t in cache[2:] if t is not None), before):
+        assert torch.equal(t.view(torch.uint8), b)

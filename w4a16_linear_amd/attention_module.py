@@ -22,12 +22,17 @@ from torch import nn
 from . import attention as A
 
 
-def token_slots(page_table: torch.Tensor, positions: torch.Tensor, page: int) -> torch.Tensor:
+def token_slots(page_table: torch.Tensor, positions: torch.Tensor, page: int,
+                pages: Optional[int] = None) -> torch.Tensor:
     """Cache slots (int32, the shape of `positions` [batch, n]) of positions in each
-    sequence; -1 (no slot) past the page table and for negative positions."""
+    sequence; -1 (no slot) past the page table, for negative positions, and where the page
+    id is none of the cache's `pages` (not given: of as many as a cache can have, fewer than
+    2^31 tokens: a larger id must not wrap around to another page's slots)."""
     index = torch.div(positions, page, rounding_mode="floor")
-    inside = (positions >= 0) & (index < page_table.shape[1])
-    ids = torch.gather(page_table, 1, index.clamp(0, page_table.shape[1] - 1).long())
+    at = index.clamp(0, page_table.shape[1] - 1)
+    ids = torch.gather(page_table, 1, at.long())
+    last = ((2 ** 31 - 1) // page if pages is None else pages) - 1
+    inside = (index == at) & (ids == ids.clamp(0, last))
     return torch.where(inside, ids * page + positions % page, -1).to(torch.int32)
 
 
@@ -77,7 +82,7 @@ class OPQAttention(nn.Module):
         positions = places if depths is None else lens[:, None] + depths
         if counts is not None:
             places = torch.where(steps < counts[:, None], places, -1)
-        slots = token_slots(page_table, places, cache.page)
+        slots = token_slots(page_table, places, cache.page, cache.pages)
         h, k = self.heads, self.kv_heads
         fused = self.qkv(x).view(batch * draft, h + 2 * k, self.dim)
         qk = fused[:, :h + k]
@@ -96,8 +101,8 @@ class OPQAttention(nn.Module):
         n = torch.arange(kept.shape[1], dtype=torch.int32, device=kept.device)
         src = torch.where(kept >= 0, lens[:, None] + kept, -1)
         dst = torch.where(kept >= 0, lens[:, None] + n, -1)
-        A.cache_move(cache, token_slots(page_table, src, cache.page).contiguous(),
-                     token_slots(page_table, dst, cache.page).contiguous())
+        A.cache_move(cache, token_slots(page_table, src, cache.page, cache.pages).contiguous(),
+                     token_slots(page_table, dst, cache.page, cache.pages).contiguous())
 
 
 __all__: Sequence[str] = ["OPQAttention", "token_slots"]
