@@ -38,3 +38,12 @@ def test_a_page_id_outside_every_cache_names_no_slot(page, ids, pages):
     pos = _i32([[0, 1, page - 1, page, page + 1, 3 * page - 1]])
     got = token_slots(_i32([[ids, ids, ids]]), pos, page, pages)
     assert (got == -1).all()
+
+
+def test_no_pages_no_slots():
+    """A page table without columns, and a cache without pages: nothing to look up."""
+    pos = _i32([[-1, 0, 5], [0, 70, 2 ** 31 - 1]])
+    assert (token_slots(torch.zeros((2, 0), dtype=torch.int32), pos, 64) == -1).all()
+    assert (token_slots(_i32([[-1, 0], [0, 1]]), pos, 64, 0) == -1).all()
+    assert token_slots(torch.zeros((2, 0), dtype=torch.int32), pos[:, :0], 64).shape == (2, 0)
+    assert token_slots(torch.zeros((0, 3), dtype=torch.int32), pos[:0], 64).shape == (0, 3)

@@ -28,6 +28,8 @@ def token_slots(page_table: torch.Tensor, positions: torch.Tensor, page: int,
     sequence; -1 (no slot) past the page table, for negative positions, and where the page
     id is none of the cache's `pages` (not given: of as many as a cache can have, fewer than
     2^31 tokens: a larger id must not wrap around to another page's slots)."""
+    if page_table.shape[1] == 0 or pages == 0:   # nothing to look up, no index that is inside
+        return torch.full_like(positions, -1, dtype=torch.int32)
     index = torch.div(positions, page, rounding_mode="floor")
     at = index.clamp(0, page_table.shape[1] - 1)
     ids = torch.gather(page_table, 1, at.long())
