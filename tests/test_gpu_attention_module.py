@@ -188,3 +188,59 @@ def test_a_page_outside_the_cache_leaves_the_others_alone(gpu_lib, bad):
     layer.accept(cache, mixed, zero + 10, torch.tensor([[-1, 8, 9]], dtype=torch.int32, device=DEV))
     for t, b in zip((t for t in cache[2:] if t is not None), before):
         assert torch.equal(t.view(torch.uint8), b)
+
+
+def test_first_calls_on_two_streams(gpu_lib):
+    """The first call makes the rotary table; a call on another stream right behind it reads
+    the finished one, however busy the first stream is."""
+    x = torch.randn(2, 9, 256, device=DEV).bfloat16()
+    table = _pages(2, 1)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    ref_layer = _layer(13)
+    ref = ref_layer(x, ref_layer.new_cache(2, 16, "fp8", device=DEV), table, zero)
+    layer = _layer(13)
+    caches = [layer.new_cache(2, 16, "fp8", device=DEV) for _ in range(2)]
+    big = torch.randn(4096, 4096, device=DEV).bfloat16()
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(first):
+        for _ in range(100):
+            big @ big
+        a = layer(x, caches[0], table, zero)
+    with torch.cuda.stream(second):
+        b = layer(x, caches[1], table, zero)
+    torch.cuda.synchronize()
+    assert torch.equal(a, ref) and torch.equal(b, ref)
+    assert layer.rope(x.device) is layer.rope("cuda")
+
+
+def test_layer_in_a_graph(gpu_lib):
+    """A capture that would have to make the table is refused; once it is there the layer's
+    step is captured and replayed, each replay equal to the eager call and following lengths
+    changed in place."""
+    layer = _layer(17)
+    x = torch.randn(2, 1, 256, device=DEV).bfloat16()
+    first = torch.randn(2, 20, 256, device=DEV).bfloat16()
+    table = _pages(2, 4)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    cache = layer.new_cache(8, 16, "opq4", device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with pytest.raises(RuntimeError, match="rotary table"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            layer(x, cache, table, zero)
+    layer(first, cache, table, zero)
+    lens = zero + 20
+    want = [layer(x, cache, table, zero + n) for n in (20, 21, 20, 21)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        y = layer(x, cache, table, lens, max_len=48)
+    for i in range(4):
+        y.zero_()
+        lens.copy_(zero + 20 + i % 2)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+        layer(first, layer.new_cache(8, 16, "opq4", device=DEV), table, zero)

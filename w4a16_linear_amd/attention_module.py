@@ -14,7 +14,7 @@ tensors are not on the GPU raises.
 """
 from __future__ import annotations
 
-from typing import Optional, Sequence
+from typing import Dict, Optional, Sequence
 
 import torch
 from torch import nn
@@ -58,13 +58,24 @@ class OPQAttention(nn.Module):
         self.frequencies = A.rotary_frequencies(rot or self.dim, base, scaling, factor, original_len)
         self.qkv = nn.Linear(hidden, (self.heads + 2 * self.kv_heads) * self.dim, bias=False)
         self.o = nn.Linear(self.heads * self.dim, hidden, bias=False)
-        self._rope: Optional[torch.Tensor] = None   # float32 whatever the layer's type
+        self._ropes: Dict[torch.device, torch.Tensor] = {}   # float32 whatever the layer's type
 
     def rope(self, device: torch.device) -> torch.Tensor:
-        """The rotary table on `device`, made once."""
-        if self._rope is None or self._rope.device != device:
-            self._rope = A.rotary_table(self.frequencies, self.max_positions, device)
-        return self._rope
+        """The rotary table on `device`, made at the first call there and kept.  That call
+        waits for it, so that every stream and thread may use what is kept without asking
+        who made it; it cannot be part of a graph's capture."""
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        table = self._ropes.get(device)
+        if table is None:
+            if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the layer's rotary table is not made yet: call rope(device), or run the "
+                                   "layer once, before capturing it in a graph")
+            table = A.rotary_table(self.frequencies, self.max_positions, device)
+            torch.cuda.current_stream(device).synchronize()
+            self._ropes[device] = table
+        return table
 
     def new_cache(self, pages: int, page: int = 64, fmt: str = "opq4", alpha: float = 0.73,
                   device="cuda") -> A.PagedCache:
@@ -79,6 +90,7 @@ class OPQAttention(nn.Module):
         takes them, with depths (int32 [batch, draft]): each token's distance from the
         last cached one, less one, which gives its position; without them a chain."""
         batch, draft, _ = x.shape
+        rope = self.rope(x.device)
         steps = torch.arange(draft, dtype=torch.int32, device=x.device)
         places = lens[:, None] + steps                       # where tokens are stored
         positions = places if depths is None else lens[:, None] + depths
@@ -88,7 +100,7 @@ class OPQAttention(nn.Module):
         h, k = self.heads, self.kv_heads
         fused = self.qkv(x).view(batch * draft, h + 2 * k, self.dim)
         qk = fused[:, :h + k]
-        A.rotary(qk, positions.reshape(-1).contiguous(), self.rope(x.device), self.layout, out=qk)
+        A.rotary(qk, positions.reshape(-1).contiguous(), rope, self.layout, out=qk)
         A.cache_write(cache, fused[:, h:h + k], fused[:, h + k:], slots.reshape(-1))
         q = fused.view(batch, draft, h + 2 * k, self.dim)[:, :, :h]
         y = A.tree_attention(q, cache, page_table, lens, mask=mask, counts=counts, max_len=max_len)
