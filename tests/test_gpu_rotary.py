@@ -170,3 +170,47 @@ def test_refusals_and_empty(gpu_lib):
                 dict(out=x.bfloat16()), dict(x=x[..., :16])):
         with pytest.raises(ValueError):
             A.rotary(**{**dict(x=x, positions=p, table=t), **bad})
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_gradient_of_a_gradient(gpu_lib, layout):
+    """With y = R x and L = sum(w y^2) / 2 the gradient is g = R' (w y), and the gradient of
+    sum(u g) with respect to x is R' (w (R u)): both turns once more, as a gradient penalty
+    needs them."""
+    rng = np.random.default_rng(16)
+    tokens, heads, dim, sections = 5, 3, 32, (4, 8)
+    table = _table(rng, 20, 12)
+    pos = rng.integers(0, 20, (tokens, 2)).astype(np.int32)
+    t, p = torch.from_numpy(table).to(DEV), torch.from_numpy(pos).to(DEV)
+    x, w, u = (torch.from_numpy(rng.standard_normal((tokens, heads, dim)).astype(np.float32)).to(DEV) for _ in range(3))
+    x.requires_grad_()
+    w.requires_grad_()
+    y = A.apply_rotary(x, p, t, layout, sections)
+    g, = torch.autograd.grad((w * y * y).sum() / 2, x, create_graph=True)
+    gx, gw = torch.autograd.grad((g * u).sum(), (x, w))
+    wd, ud, xd = (v.detach().double().cpu().numpy() for v in (w, u, x))
+    args = (pos, table, layout, sections)
+    ru, mag = AO.rotary(ud, *args)
+    e = 3 * U32 * mag                              # of R u: two products and a sum
+    z, ez = wd * ru, np.abs(wd) * e + U32 * np.abs(wd * ru) * 1.01
+    ref, rmag = AO.rotary(z, *args, backward=True)
+    _, spread = AO.rotary(ez, *args, backward=True)
+    assert (np.abs(gx.double().cpu().numpy() - ref) <= spread + 3.1 * U32 * rmag).all()
+    # with respect to w: y (R u), where the first gradient's own graph has to reach w too
+    ry, ymag = AO.rotary(xd, *args)
+    bound = np.abs(ry) * e + np.abs(ru) * 3 * U32 * ymag + 2 * U32 * np.abs(ry * ru) + 1e-12
+    assert (np.abs(gw.double().cpu().numpy() - ry * ru) <= bound).all()
+
+
+def test_second_differentiation_twice(gpu_lib):
+    """A gradient's graph is kept and used twice, and a third turn goes the first way again."""
+    t = torch.from_numpy(_table(np.random.default_rng(2), 9, 16)).to(DEV)
+    p = torch.arange(4, dtype=torch.int32, device=DEV)
+    x, v = (torch.randn(4, 2, 32, device=DEV, requires_grad=True) for _ in range(2))
+    y = A.apply_rotary(x, p, t)
+    g, = torch.autograd.grad(y, x, v, create_graph=True)          # R' v
+    assert g.requires_grad and torch.equal(g.detach(), A.rotary_backward(v.detach(), p, t))
+    w = torch.randn_like(x)
+    for _ in range(2):
+        gg, = torch.autograd.grad(g, v, w, retain_graph=True)     # R w
+        assert torch.equal(gg, A.rotary(w, p, t))

@@ -153,24 +153,27 @@ def rotary_backward(grad: torch.Tensor, positions: torch.Tensor, table: torch.Te
 
 
 class _Rotary(torch.autograd.Function):
+    """The turn one way; its gradient is the turn the other way, an operation of its own,
+    so gradients of gradients are followed too."""
+
     @staticmethod
-    def forward(ctx, x, positions, table, layout, sections):
+    def forward(ctx, x, positions, table, layout, sections, backward):
         ctx.save_for_backward(positions, table)
-        ctx.how = (layout, sections)
-        return rotary(x, positions, table, layout, sections)
+        ctx.how = (layout, sections, not backward)
+        return _rotary(x, positions, table, layout, sections, None, int(backward))
 
     @staticmethod
     def backward(ctx, grad):
         positions, table = ctx.saved_tensors
         if grad.shape[-1] > 1 and grad.stride(-1) != 1:
             grad = grad.contiguous()
-        return rotary_backward(grad, positions, table, *ctx.how), None, None, None, None
+        return _Rotary.apply(grad, positions, table, *ctx.how), None, None, None, None, None
 
 
 def apply_rotary(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: str = "half",
                  sections: Optional[Sequence[int]] = None) -> torch.Tensor:
-    """rotary() that autograd differentiates with respect to x."""
-    return _Rotary.apply(x, positions, table, layout, None if sections is None else tuple(sections))
+    """rotary() that autograd differentiates with respect to x, as often as asked."""
+    return _Rotary.apply(x, positions, table, layout, None if sections is None else tuple(sections), False)
 
 
 # ------------------------------------------------------------------- cache
