@@ -47,3 +47,27 @@ def test_no_pages_no_slots():
     assert (token_slots(_i32([[-1, 0], [0, 1]]), pos, 64, 0) == -1).all()
     assert token_slots(torch.zeros((2, 0), dtype=torch.int32), pos[:, :0], 64).shape == (2, 0)
     assert token_slots(torch.zeros((0, 3), dtype=torch.int32), pos[:0], 64).shape == (0, 3)
+
+
+# ------------------------------------------------------------------ refusals
+
+def _call(**kw):
+    """A forward with everything in order but what kw says, on the CPU: in order it gets as
+    far as the rotary table, which needs the GPU."""
+    layer = OPQAttention(128, 2, 1, 64, max_positions=64).to(torch.bfloat16)
+    args = dict(x=torch.zeros(2, 3, 128, dtype=torch.bfloat16), cache=layer.new_cache(4, 16, "fp8", device="cpu"),
+                page_table=_i32([[0, 1], [2, 3]]), lens=_i32([0, 5]))
+    with torch.no_grad():
+        layer(**{**args, **kw})
+
+
+def test_in_order_reaches_the_gpu():
+    tree = dict(mask=torch.zeros((2, 3, 1), dtype=torch.int32), depths=torch.zeros((2, 3), dtype=torch.int32))
+    for kw in (dict(), tree, dict(tree, mask=tree["mask"][0]), dict(counts=_i32([3, 0])), dict(max_len=0), dict(max_len=32)):
+        with pytest.raises(ValueError, match="CUDA"):
+            _call(**kw)
+
+
+def test_a_mask_needs_depths():
+    with pytest.raises(ValueError, match="depths"):
+        _call(mask=torch.zeros((2, 3, 1), dtype=torch.int32))

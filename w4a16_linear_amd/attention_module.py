@@ -87,8 +87,10 @@ class OPQAttention(nn.Module):
                 max_len: Optional[int] = None) -> torch.Tensor:
         """x [batch, draft, hidden] (bfloat16): the tokens after each sequence's lens[b]
         cached ones, written to the cache here.  mask: tree words as tree_attention
-        takes them, with depths (int32 [batch, draft]): each token's distance from the
-        last cached one, less one, which gives its position; without them a chain."""
+        takes them, and with it depths (int32 [batch, draft]): each token's distance from the
+        last cached one, less one, which gives its position; without a mask a chain."""
+        if mask is not None and depths is None:
+            raise ValueError("a mask needs depths: a tree's tokens are not at the positions of their places")
         batch, draft, _ = x.shape
         rope = self.rope(x.device)
         steps = torch.arange(draft, dtype=torch.int32, device=x.device)
