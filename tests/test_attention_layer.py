@@ -71,3 +71,27 @@ def test_in_order_reaches_the_gpu():
 def test_a_mask_needs_depths():
     with pytest.raises(ValueError, match="depths"):
         _call(mask=torch.zeros((2, 3, 1), dtype=torch.int32))
+
+
+_TREE = dict(mask=torch.zeros((2, 3, 1), dtype=torch.int32), depths=torch.zeros((2, 3), dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("x", dict(x=torch.zeros(2, 3, 128))), ("x", dict(x=torch.zeros(2, 3, 128, dtype=torch.float16))),
+    ("x", dict(x=torch.zeros(3, 128, dtype=torch.bfloat16))), ("x", dict(x=torch.zeros(2, 3, 64, dtype=torch.bfloat16))),
+    ("page_table", dict(page_table=torch.zeros((2, 2), dtype=torch.int64))),
+    ("page_table", dict(page_table=_i32([[0, 1]]))), ("page_table", dict(page_table=_i32([0, 1]))),
+    ("contiguous", dict(page_table=_i32([[0, 1, 2], [1, 2, 3]])[:, :2])),
+    ("lens", dict(lens=torch.zeros(2, dtype=torch.int64))), ("lens", dict(lens=_i32([0]))),
+    ("mask", dict(_TREE, mask=_TREE["mask"].long())), ("mask", dict(_TREE, mask=_TREE["mask"][:, :2])),
+    ("mask", dict(_TREE, mask=_TREE["mask"][:1])), ("depths", dict(_TREE, depths=_TREE["depths"].long())),
+    ("depths", dict(_TREE, depths=_TREE["depths"][:, :2])), ("counts", dict(counts=_i32([1]))),
+    ("counts", dict(counts=torch.ones(2))), ("max_len", dict(max_len=33)), ("max_len", dict(max_len=-1)),
+    ("heads", dict(cache=OPQAttention(128, 2, 2, 64).new_cache(4, 16, "fp8", device="cpu"))),
+    ("heads", dict(cache=OPQAttention(128, 2, 1, 128).new_cache(4, 16, "fp8", device="cpu")))])
+def test_refused_before_anything_is_enqueued(name, bad):
+    """What a later call of the forward refuses is refused before an earlier one has written
+    to the cache: here, before the GPU is asked for at all."""
+    with pytest.raises(ValueError, match=name) as e:
+        _call(**bad)
+    assert "CUDA" not in str(e.value)

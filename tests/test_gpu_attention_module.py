@@ -244,3 +244,17 @@ def test_layer_in_a_graph(gpu_lib):
         torch.cuda.synchronize()
         assert torch.equal(y, want[i])
         layer(first, layer.new_cache(8, 16, "opq4", device=DEV), table, zero)
+
+
+def test_a_refused_forward_writes_nothing(gpu_lib):
+    layer = _layer(19)
+    cache = layer.new_cache(2, 16, "fp8", device=DEV)
+    x = torch.randn(1, 3, 256, device=DEV).bfloat16()
+    args = dict(x=x, cache=cache, page_table=_pages(1, 2), lens=torch.zeros(1, dtype=torch.int32, device=DEV))
+    for bad in (dict(x=x.float()), dict(page_table=_pages(1, 2).long()), dict(max_len=33),
+                dict(counts=torch.ones(2, dtype=torch.int32, device=DEV))):
+        with pytest.raises(ValueError):
+            layer(**{**args, **bad})
+    assert not any(t.view(torch.uint8).any() for t in cache[2:] if t is not None)
+    layer(**args)
+    assert cache.k_scale.any()

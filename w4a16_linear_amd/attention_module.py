@@ -48,7 +48,7 @@ class OPQAttention(nn.Module):
                  base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
                  original_len: float = 0.0, layout: str = "half"):
         super().__init__()
-        self.heads, self.kv_heads = heads, kv_heads or heads
+        self.hidden, self.heads, self.kv_heads = hidden, heads, kv_heads or heads
         self.dim = dim or hidden // heads
         if self.heads % self.kv_heads:
             raise ValueError(f"heads={heads} must be a multiple of kv_heads={kv_heads}")
@@ -81,6 +81,33 @@ class OPQAttention(nn.Module):
                   device="cuda") -> A.PagedCache:
         return A.new_cache(pages, self.kv_heads, page, self.dim, fmt, alpha, device)
 
+    def _check(self, x, cache, page_table, lens, mask, depths, counts, max_len) -> None:
+        """All that the calls of a forward would refuse, before the first of them writes."""
+        if x.dim() != 3 or x.shape[2] != self.hidden or x.dtype != torch.bfloat16:
+            raise ValueError(f"x must be bfloat16 [batch, draft, {self.hidden}], got {x.dtype} {tuple(x.shape)}")
+        batch, draft, _ = x.shape
+        if (cache.heads, cache.dim) != (self.kv_heads, self.dim):
+            raise ValueError(f"the cache has {cache.heads} heads of {cache.dim}, the layer {self.kv_heads} of "
+                             f"{self.dim}")
+        wanted = [("page_table", page_table, (batch, page_table.shape[-1])), ("lens", lens, (batch,))]
+        if mask is not None:
+            words = (draft, (draft + 31) // 32)
+            wanted.append(("mask", mask, words if mask.dim() == 2 else (batch,) + words))
+        if depths is not None:
+            wanted.append(("depths", depths, (batch, draft)))
+        if counts is not None:
+            wanted.append(("counts", counts, (batch,)))
+        for name, t, shape in wanted:
+            if t.dtype != torch.int32 or t.shape != shape or t.device != x.device:
+                raise ValueError(f"{name} must be int32 {shape} on {x.device}, got {t.dtype} {tuple(t.shape)} on "
+                                 f"{t.device}")
+        # depths only enter sums here; the others' memory goes to the kernels
+        if not all(t.is_contiguous() for name, t, _ in wanted if name != "depths"):
+            raise ValueError("page_table, lens, mask and counts must be contiguous")
+        if max_len is not None and not 0 <= max_len <= page_table.shape[1] * cache.page:
+            raise ValueError(f"max_len must be 0 to {page_table.shape[1] * cache.page}, what the page table "
+                             f"holds, got {max_len}")
+
     def forward(self, x: torch.Tensor, cache: A.PagedCache, page_table: torch.Tensor,
                 lens: torch.Tensor, mask: Optional[torch.Tensor] = None,
                 depths: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
@@ -91,6 +118,7 @@ class OPQAttention(nn.Module):
         last cached one, less one, which gives its position; without a mask a chain."""
         if mask is not None and depths is None:
             raise ValueError("a mask needs depths: a tree's tokens are not at the positions of their places")
+        self._check(x, cache, page_table, lens, mask, depths, counts, max_len)
         batch, draft, _ = x.shape
         rope = self.rope(x.device)
         steps = torch.arange(draft, dtype=torch.int32, device=x.device)
