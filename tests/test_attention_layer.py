@@ -95,3 +95,23 @@ def test_refused_before_anything_is_enqueued(name, bad):
     with pytest.raises(ValueError, match=name) as e:
         _call(**bad)
     assert "CUDA" not in str(e.value)
+
+
+def test_lost_gradients_are_refused():
+    """x or the weights of qkv would get no gradient: an error instead, unless none is asked for."""
+    x = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+
+    def call(layer, x):
+        layer(x, layer.new_cache(1, 16, "fp8", device="cpu"), _i32([[0]]), _i32([0]))
+
+    layer = OPQAttention(128, 2, 1, 64, max_positions=64).to(torch.bfloat16)
+    with pytest.raises(RuntimeError, match="gradients"):
+        call(layer, x)
+    for quiet in (torch.no_grad, torch.inference_mode):
+        with quiet(), pytest.raises(ValueError, match="CUDA"):
+            call(layer, x)
+    layer.qkv.requires_grad_(False)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(layer, x)
+    with pytest.raises(RuntimeError, match="gradients"):
+        call(layer, x.requires_grad_())

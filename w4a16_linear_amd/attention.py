@@ -9,6 +9,10 @@ would take longer than the GPU, this is done in C++ (csrc/attention_torch.cpp, b
 as _attention.so).  Workspaces come from torch's allocator per call, so calls on
 different streams do not share one.
 
+Only apply_rotary is followed by autograd.  Every other call refuses (RuntimeError) a
+tensor that requires grad unless gradients are off (torch.no_grad()), rather than
+return a result cut off from it.
+
     table = rotary_table(rotary_frequencies(128, 1e6), 32768, "cuda")
     cache = new_cache(pages=1024, heads=8, page=64, dim=128, fmt="opq4", device="cuda")
     qk = rotary(qkv.view(tokens, 48, 128)[:, :40], positions, table)
@@ -172,7 +176,10 @@ class _Rotary(torch.autograd.Function):
 
 def apply_rotary(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: str = "half",
                  sections: Optional[Sequence[int]] = None) -> torch.Tensor:
-    """rotary() that autograd differentiates with respect to x, as often as asked."""
+    """rotary() that autograd differentiates with respect to x, as often as asked (not with
+    respect to the table)."""
+    if table.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("table requires grad, which apply_rotary does not follow: detach it")
     return _Rotary.apply(x, positions, table, layout, None if sections is None else tuple(sections), False)
 
 

@@ -10,7 +10,8 @@ sequence, a chain, or a tree of drafted ones) over it, OPQ-quantized output proj
     layer.accept(cache, page_table, lens, kept)  # of a verified tree
 
 Every step but the projections' reshapes runs in libopq; like OPQLinear, a layer whose
-tensors are not on the GPU raises.
+tensors are not on the GPU raises.  No gradient passes through the cache: where one would
+be lost (x or qkv's weights require it and gradients are on) a forward raises.
 """
 from __future__ import annotations
 
@@ -85,6 +86,9 @@ class OPQAttention(nn.Module):
         """All that the calls of a forward would refuse, before the first of them writes."""
         if x.dim() != 3 or x.shape[2] != self.hidden or x.dtype != torch.bfloat16:
             raise ValueError(f"x must be bfloat16 [batch, draft, {self.hidden}], got {x.dtype} {tuple(x.shape)}")
+        if torch.is_grad_enabled() and (x.requires_grad or any(w.requires_grad for w in self.qkv.parameters())):
+            raise RuntimeError("this layer serves and passes no gradients back: call it under torch.no_grad(), "
+                               "or with x and the weights of qkv not requiring them")
         batch, draft, _ = x.shape
         if (cache.heads, cache.dim) != (self.kv_heads, self.dim):
             raise ValueError(f"the cache has {cache.heads} heads of {cache.dim}, the layer {self.kv_heads} of "

@@ -7,6 +7,7 @@
 //
 // Nothing here computes; every call ends in libopq (include/opq_attention.h).
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -43,6 +44,14 @@ const Tensor& tensor_of(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// These calls compute outside autograd: a result that ought to carry a gradient would
+// come back without one, and nothing would say so.
+const Tensor& plain(const Tensor& t, const char* name) {
+  TORCH_CHECK(!(t.requires_grad() && at::GradMode::is_enabled()), name,
+              " requires grad, which this call does not follow (apply_rotary turns positions "
+              "under autograd): detach it, or call under torch.no_grad()");
+  return t;
+}
 // A dense tensor of a known type and shape.
 void* dense(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape,
             c10::Device dev) {
@@ -62,7 +71,7 @@ const Tensor& rows(PyObject* o, const char* name, int64_t ndim) {
   const Tensor& t = tensor_of(o, name);
   TORCH_CHECK_VALUE(t.dim() == ndim && (t.size(-1) <= 1 || t.stride(-1) == 1), name, " must be ",
                     ndim, "-d with a dense last dimension");
-  return t;
+  return plain(t, name);
 }
 
 int dtype_of(at::ScalarType t, const char* what) {
@@ -108,7 +117,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& table = tensor_of(a[2], "table");
   TORCH_CHECK_VALUE(table.dim() == 3, "table must be [length, pairs, 2]");
   const int64_t pairs = table.size(1), length = table.size(0);
-  const void* pt = dense(table, "table", at::kFloat, {length, pairs, 2}, x.device());
+  const void* pt = dense(plain(table, "table"), "table", at::kFloat, {length, pairs, 2}, x.device());
   std::vector<int32_t> sections;
   if (a[4] == Py_None) {
     sections.push_back((int32_t)pairs);
@@ -238,7 +247,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* p[2];
   for (int i = 0; i < 2; ++i) {
     if (a[3 + i] == Py_None) out[i] = at::empty(shape, slots.options().dtype(type));
-    else out[i] = tensor_of(a[3 + i], "out");
+    else out[i] = plain(tensor_of(a[3 + i], "out"), "out");
     p[i] = dense(out[i], "out", type, shape, r.dev);
   }
   check("opq_cache_read", opq_cache_read(&r.c, tokens, static_cast<const int32_t*>(ps), p[0], p[1],
@@ -308,7 +317,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t max_len = a[7] == Py_None ? (room > 0 ? room : 0) : int_of(a[7]);
   const OnDevice on(q);
   const int64_t shape[4] = {batch, draft, heads, dim};
-  Tensor out = a[8] == Py_None ? at::empty(shape, q.options()) : tensor_of(a[8], "out");
+  Tensor out =
+      a[8] == Py_None ? at::empty(shape, q.options()) : plain(tensor_of(a[8], "out"), "out");
   void* po = dense(out, "out", at::kBFloat16, shape, r.dev);
   Tensor lse;
   if (int_of(a[9])) lse = at::empty({batch, draft, heads}, q.options().dtype(at::kFloat));
