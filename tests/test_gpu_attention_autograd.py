@@ -1,5 +1,5 @@
 """The attention side's calls and autograd: only apply_rotary is followed; the others refuse
-tensors that require grad."""
+tensors that require grad, and tell autograd of memory that they write."""
 import pytest
 import torch
 
@@ -52,3 +52,34 @@ def test_lost_gradients_are_refused(gpu_lib, name):
     with torch.inference_mode():
         call(t)
     call(t.detach())
+
+
+def test_written_memory_is_known_to_autograd(gpu_lib):
+    """A tensor that a product saved for its backward, then written in place: the backward
+    says so, and does not use the new values."""
+    x, index, table, cache = _parts()
+    q = x[:1].view(1, 1, 2, 64)
+    lens, pages = index[:1], index[None, :2]
+    writes = [(x.clone(), lambda t: A.rotary(t, index, table, out=t)),
+              (x.clone(), lambda t: A.cache_read(cache, index, out=(t, torch.empty_like(x)))),
+              (q.clone(), lambda t: A.tree_attention(q, cache, pages, lens, out=t)),
+              (cache.k_scale, lambda t: A.cache_write(cache, x, x, index)),
+              (cache.v_scale, lambda t: A.cache_move(cache, index[None], index[None]))]
+    for t, write in writes:
+        w = torch.ones_like(t, requires_grad=True)
+        y = w * t
+        write(t)
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            y.sum().backward()
+
+
+def test_inference_tensors_are_written_as_before(gpu_lib):
+    with torch.inference_mode():
+        x, index, table, cache = _parts()
+        out = torch.empty_like(x)
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            A.rotary(x, index, table, out=out)
+            A.cache_write(cache, x, x, index)
+            A.cache_read(cache, index, out=(out, torch.empty_like(x)))
+    assert torch.isfinite(out).all()

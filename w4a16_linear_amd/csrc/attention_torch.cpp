@@ -52,6 +52,12 @@ const Tensor& plain(const Tensor& t, const char* name) {
               "under autograd): detach it, or call under torch.no_grad()");
   return t;
 }
+// A tensor whose memory this call writes: autograd learns of it, as of every in-place
+// operation, should it have saved the old values.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A dense tensor of a known type and shape.
 void* dense(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape,
             c10::Device dev) {
@@ -156,6 +162,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    static_cast<const float*>(pt), length, 2 * pairs, (int)int_of(a[3]),
                    (int)int_of(a[6]), out.data_ptr(), out.stride(0), out.stride(1), on.stream()));
   if (a[5] != Py_None) {
+    written(out);
     Py_INCREF(a[5]);
     return a[5];
   }
@@ -205,6 +212,11 @@ Cache cache_of(PyObject* o) {
   return r;
 }
 
+void cache_written(PyObject* o) {
+  for (int i = 2; i < 8; ++i)
+    if (THPVariable_Check(PyTuple_GET_ITEM(o, i))) written(THPVariable_Unpack(PyTuple_GET_ITEM(o, i)));
+}
+
 // cache, k, v, slots
 PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -226,6 +238,7 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
         opq_cache_write(&r.c, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
                         v.stride(1), dtype, tokens, static_cast<const int32_t*>(slots),
                         on.stream()));
+  cache_written(a[0]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -252,6 +265,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   check("opq_cache_read", opq_cache_read(&r.c, tokens, static_cast<const int32_t*>(ps), p[0], p[1],
                                          bf16 ? OPQ_BF16 : OPQ_F32, on.stream()));
+  for (const Tensor& t : out) written(t);
   PyObject* k = THPVariable_Wrap(std::move(out[0]));
   PyObject* v = THPVariable_Wrap(std::move(out[1]));
   PyObject* both = k && v ? PyTuple_Pack(2, k, v) : nullptr;
@@ -274,6 +288,7 @@ PyObject* cache_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const OnDevice on(src);
   check("opq_cache_move", opq_cache_move(&r.c, batch, count, static_cast<const int32_t*>(ps),
                                          static_cast<const int32_t*>(pd), on.stream()));
+  cache_written(a[0]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -345,6 +360,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[8] == Py_None) {
     first = THPVariable_Wrap(std::move(out));
   } else {
+    written(out);
     first = a[8];
     Py_INCREF(first);
   }
