@@ -214,3 +214,22 @@ def test_second_differentiation_twice(gpu_lib):
     for _ in range(2):
         gg, = torch.autograd.grad(g, v, w, retain_graph=True)     # R w
         assert torch.equal(gg, A.rotary(w, p, t))
+
+
+@pytest.mark.parametrize("pairs,length", [(512, 2 ** 23 + 77), (3, 1431655766 + 5)])
+def test_table_of_several_launches(gpu_lib, pairs, length):
+    """More entries than 2^32 work-items (34 GB), and rows that a launch's limit is no multiple
+    of: positions on both sides of every launch's end, and the last ones."""
+    f = A.rotary_frequencies(2 * pairs)
+    table = A.rotary_table(f, length, DEV)
+    assert table.numel() // 2 > 2 ** 32
+    step = 2 ** 31 // pairs
+    for at in [p for e in range(step, length + step, step) for p in (e - 1, e, e + 1)] + [0, 1, length - 1]:
+        if at >= length:
+            continue
+        row, angle = table[at].double().cpu().numpy(), at * f.freq
+        # as in test_table: one rounding to float32, the double angle off by 2^-53 p f radians
+        bound = U32 + 2.0 ** -52 * angle + 1e-15
+        assert (np.abs(row[:, 0] - np.cos(angle)) <= bound).all() and (np.abs(row[:, 1] - np.sin(angle)) <= bound).all()
+    del table
+    torch.cuda.empty_cache()

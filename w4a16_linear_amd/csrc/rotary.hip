@@ -130,16 +130,18 @@ __global__ __launch_bounds__(kThreads) void rotary_rows(RotaryArgs a) {
     }
 }
 
+// Positions `first` .. first + len - 1, into `table` from its start.
 __global__ __launch_bounds__(kThreads) void rotary_table(const double* __restrict__ freq,
-                                                         int pairs, int64_t len, double amplitude,
+                                                         int pairs, int64_t first, int64_t len,
+                                                         double amplitude,
                                                          float* __restrict__ table) {
   const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t pos = idx / pairs;
-  if (pos >= len) return;
-  const int i = (int)(idx - pos * pairs);
+  const int64_t at = idx / pairs;
+  if (at >= len) return;
+  const int i = (int)(idx - at * pairs);
   // turns of the angle pos * f, the whole ones dropped.  r is within 2^-53 of
   // itself relative, so a context of 10^6 keeps 1e-10 of a turn.
-  const double turns = (double)pos * (freq[i] * 0.15915494309189533577);
+  const double turns = (double)(first + at) * (freq[i] * 0.15915494309189533577);
   const double r = turns - rint(turns);
   double s, c;
   sincospi(2.0 * r, &s, &c);
@@ -213,10 +215,17 @@ hipError_t launch_rotary(const RotaryArgs& a, bool bf16, bool interleaved, hipSt
 
 hipError_t launch_rotary_table(const double* freq, int64_t pairs, int64_t len, double amplitude,
                                float* table, hipStream_t stream) {
-  const int64_t n = pairs * len, blocks = (n + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL(rotary_table, dim3((unsigned)blocks), dim3(kThreads), 0, stream, freq,
-                     (int)pairs, len, amplitude, table);
-  return hipGetLastError();
+  // whole positions per launch, within the 32-bit count of work-items
+  const int64_t step = kMaxLaunchThreads / pairs;
+  for (int64_t p0 = 0; p0 < len; p0 += step) {
+    const int64_t n = len - p0 < step ? len - p0 : step;
+    const dim3 grid((unsigned)((n * pairs + kThreads - 1) / kThreads));
+    hipLaunchKernelGGL(rotary_table, grid, dim3(kThreads), 0, stream, freq, (int)pairs, p0, n,
+                       amplitude, table + 2 * p0 * pairs);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace opq
