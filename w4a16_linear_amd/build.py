@@ -90,6 +90,24 @@ def _link(objs, lib: str, libs, verbose: bool) -> None:
     os.replace(tmp, lib)
 
 
+def extension_lacks() -> str:
+    """What the extension's build would miss here ("" if nothing): it is the only part that
+    needs torch's and Python's C++ headers."""
+    import sysconfig
+
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    include = os.path.join(os.path.dirname(torch.__file__), "include")
+    for what, path in (("torch's C++ headers", os.path.join(include, "ATen", "core", "Tensor.h")),
+                       ("torch's HIP headers", os.path.join(include, "c10", "hip", "HIPStream.h")),
+                       ("Python's headers", os.path.join(sysconfig.get_paths()["include"], "Python.h"))):
+        if not os.path.exists(path):
+            return f"{what} ({path})"
+    return ""
+
+
 def _compile_extension(verbose: bool) -> str:
     import sysconfig
 
@@ -133,16 +151,24 @@ def _link_extension(obj: str, verbose: bool) -> None:
 
 def build(verbose: bool = False) -> str:
     """Compile every source, link libopq.so, libopq_ceiling.so and the torch
-    extension; returns the path of libopq.so."""
+    extension; returns the path of libopq.so.  Where torch's or Python's headers are
+    missing the libraries are built without the extension, with a note of it (and none
+    of an earlier build is left beside them); attention.load() then raises.  An extension
+    that fails to build raises after the libraries are in place."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = SOURCES + CEILING_SOURCES
+    lacks = extension_lacks()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        ext = ex.submit(_compile_extension, verbose)
+        ext = None if lacks else ex.submit(_compile_extension, verbose)
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
-        ext_obj = ext.result()
     _link([objs[s] for s in SOURCES], LIB, ["-lquadmath"], verbose)
     _link([objs[s] for s in CEILING_SOURCES], CEILING_LIB, [], verbose)
-    _link_extension(ext_obj, verbose)
+    if ext is None:
+        if os.path.exists(EXT_LIB):
+            os.remove(EXT_LIB)
+        print(f"not built: {os.path.basename(EXT_LIB)}, which needs {lacks}", file=sys.stderr)
+    else:
+        _link_extension(ext.result(), verbose)
     return LIB
 
 
