@@ -233,3 +233,13 @@ def test_table_of_several_launches(gpu_lib, pairs, length):
         assert (np.abs(row[:, 0] - np.cos(angle)) <= bound).all() and (np.abs(row[:, 1] - np.sin(angle)) <= bound).all()
     del table
     torch.cuda.empty_cache()
+
+
+def test_out_that_overlaps_itself_is_refused(gpu_lib):
+    t = torch.zeros(4, 16, 2, device=DEV)
+    p = torch.zeros(3, dtype=torch.int32, device=DEV)
+    x = torch.zeros(3, 2, 64, device=DEV)
+    for out in (torch.empty(3, 1, 64, device=DEV).expand(3, 2, 64), torch.empty(1, 2, 64, device=DEV).expand(3, 2, 64)):
+        with pytest.raises(ValueError, match="expanded"):
+            A.rotary(x, p, t, out=out)
+    A.rotary(x[:1].expand(3, 2, 64), p, t, out=torch.empty_like(x))      # of x any stride will do

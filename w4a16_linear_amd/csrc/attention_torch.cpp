@@ -6,6 +6,7 @@
 // host time a call, of which the launches are 3, 3 and 6.
 //
 // Nothing here computes; every call ends in libopq (include/opq_attention.h).
+#include <ATen/MemoryOverlap.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
@@ -152,6 +153,9 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     out = at::empty({tokens, heads, dim}, x.options());
   } else {
     out = rows(a[5], "out", 3);
+    // several threads would write an element, in any order
+    TORCH_CHECK_VALUE(at::has_internal_overlap(out) != at::MemOverlap::Yes,
+                      "out must not be expanded: its rows would be the same memory");
     TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type() &&
                           out.device() == x.device(),
                       "out must be ", x.scalar_type(), " of shape ", x.sizes(), " on ", x.device());
