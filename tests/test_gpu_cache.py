@@ -234,3 +234,16 @@ def test_refusals_and_empty(gpu_lib):
                 cache._replace(v_scale=cache.v_scale[:1]), cache._replace(fmt="opq4")):
         with pytest.raises(ValueError):
             A.cache_write(bad, k, k, slots)
+
+
+def test_read_into_shared_memory_is_refused(gpu_lib):
+    cache = A.new_cache(2, 2, 16, 64, "fp8", device=DEV)
+    slots = torch.arange(5, dtype=torch.int32, device=DEV)
+    flat = torch.empty(2 * 5 * 2 * 64 + 64, device=DEV, dtype=torch.bfloat16)
+    a, b, c = (flat[i:i + 640].view(5, 2, 64) for i in (0, 640, 576))
+    for pair in ((a, a), (a, c), (c, b)):
+        with pytest.raises(ValueError, match="share"):
+            A.cache_read(cache, slots, out=pair)
+    A.cache_read(cache, slots, out=(a, b))
+    A.cache_read(cache, slots, out=(b, a))
+    A.cache_read(cache, slots[:0], out=(a[:0], a[:0]))

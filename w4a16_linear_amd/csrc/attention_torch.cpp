@@ -267,6 +267,10 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else out[i] = plain(tensor_of(a[3 + i], "out"), "out");
     p[i] = dense(out[i], "out", type, shape, r.dev);
   }
+  const size_t bytes = out[0].nbytes();
+  TORCH_CHECK_VALUE(bytes == 0 || static_cast<char*>(p[0]) + bytes <= p[1] ||
+                        static_cast<char*>(p[1]) + bytes <= p[0],
+                    "the two of out must not share memory");
   check("opq_cache_read", opq_cache_read(&r.c, tokens, static_cast<const int32_t*>(ps), p[0], p[1],
                                          bf16 ? OPQ_BF16 : OPQ_F32, on.stream()));
   for (const Tensor& t : out) written(t);
