@@ -258,3 +258,18 @@ def test_a_refused_forward_writes_nothing(gpu_lib):
     assert not any(t.view(torch.uint8).any() for t in cache[2:] if t is not None)
     layer(**args)
     assert cache.k_scale.any()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
+@pytest.mark.parametrize("dim,page", [(128, 64), (256, 256)])
+def test_prompt_at_once_equals_in_chunks(gpu_lib, fmt, dim, page):
+    """A prompt of 400 tokens at once, in three chunks of odd lengths, and its last token alone."""
+    layer = _layer(23, hidden=512, heads=4, kv=2, dim=dim)
+    x = torch.randn(2, 400, 512, device=DEV).bfloat16()
+    per = -(-400 // page)
+    table = _pages(2, per)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    at_once, chunks = (layer.new_cache(2 * per, page, fmt, device=DEV) for _ in range(2))
+    y = layer(x, at_once, table, zero)
+    parts = [layer(x[:, a:b].contiguous(), chunks, table, zero + a, max_len=a) for a, b in ((0, 129), (129, 399), (399, 400))]
+    _close(torch.cat(parts, 1), y)

@@ -247,3 +247,38 @@ def test_read_into_shared_memory_is_refused(gpu_lib):
     A.cache_read(cache, slots, out=(a, b))
     A.cache_read(cache, slots, out=(b, a))
     A.cache_read(cache, slots[:0], out=(a[:0], a[:0]))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
+def test_write_of_several_launches(gpu_lib, fmt):
+    """More work-items than one launch's grid counts: of 2^26 tokens all but a few are skipped,
+    and those, on both sides of the boundary and at the end, are written as in a small call."""
+    dim, tokens, page = 256, 2 ** 26 + 1000, 16
+    x = torch.randn(1, 1, dim, device=DEV)
+    at = torch.tensor([0, 5, 2 ** 26 - 2, 2 ** 26 - 1, 2 ** 26, 2 ** 26 + 1, tokens - 1], device=DEV)
+    slots = torch.full((tokens,), -1, dtype=torch.int32, device=DEV)
+    slots[at] = torch.arange(7, dtype=torch.int32, device=DEV) * 3 + 1
+    big, small = (A.new_cache(2, 1, page, dim, fmt, device=DEV) for _ in range(2))
+    A.cache_write(big, x.expand(tokens, 1, dim), -x.expand(tokens, 1, dim)[:1].expand(tokens, 1, dim), slots)
+    A.cache_write(small, x.expand(7, 1, dim).contiguous(), -x.expand(7, 1, dim), slots[at])
+    for a, b in zip(big[2:], small[2:]):
+        assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert small.k_scale.any()
+
+
+def test_read_of_several_launches(gpu_lib):
+    """2^28 and some rows of 64 read in one call (34 GB a side): the tokens around the boundary
+    and the last ones as in a small call, the skipped ones zero."""
+    dim, tokens, page = 64, 2 ** 28 + 1000, 16
+    cache = A.new_cache(2, 1, page, dim, "fp8", device=DEV)
+    A.cache_write(cache, torch.randn(32, 1, dim, device=DEV), torch.randn(32, 1, dim, device=DEV),
+                  torch.arange(32, dtype=torch.int32, device=DEV))
+    slots = (torch.arange(tokens, dtype=torch.int32, device=DEV) * 7) % 37 - 3
+    k, v = A.cache_read(cache, slots)
+    for a, b in ((0, 100), (2 ** 28 - 132, 2 ** 28 + 68), (tokens - 100, tokens)):
+        for big, small in zip((k, v), A.cache_read(cache, slots[a:b].contiguous())):
+            assert torch.equal(big[a:b], small)
+    none = slots[-1000:] < 0
+    assert not k[-1000:][none].any() and k[-1000:][(slots[-1000:] >= 0) & (slots[-1000:] < 32)].any()
+    del k, v
+    torch.cuda.empty_cache()

@@ -243,3 +243,24 @@ def test_out_that_overlaps_itself_is_refused(gpu_lib):
         with pytest.raises(ValueError, match="expanded"):
             A.rotary(x, p, t, out=out)
     A.rotary(x[:1].expand(3, 2, 64), p, t, out=torch.empty_like(x))      # of x any stride will do
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_call_of_several_launches(gpu_lib, dtype):
+    """More work-items than one launch's grid counts (2^31): on both sides of the boundary, and
+    at the end, the result is that of the same tokens in a call of their own (large enough for
+    the same number of heads a thread).  One token's values, seen by all (stride 0), at
+    changing positions."""
+    dim, tokens = 65, 2 ** 25 + 1000              # a turned pair and 63 copied elements: 64 work-items a token
+    t = torch.from_numpy(_table(np.random.default_rng(1), 101, 1)).to(DEV)
+    x = torch.randn(1, 1, dim, device=DEV).to(dtype).expand(tokens, 1, dim)
+    p = (torch.arange(tokens, device=DEV) % 101).to(torch.int32)
+    y = A.rotary(x, p, t)
+    edge = 2 ** 31 // 64
+    for a, b in ((0, 8192), (edge - 8192, edge + 900), (tokens - 8192, tokens)):
+        assert torch.equal(y[a:b], A.rotary(x[a:b], p[a:b], t))
+    for a in range(0, tokens, 1 << 22):
+        assert (y[a:a + (1 << 22), 0, 2:] == x[0, 0, 2:]).all()
+        assert (y[a:a + (1 << 22), 0, :2] == y[:101, 0, :2][p[a:a + (1 << 22)].long()]).all()
+    del y
+    torch.cuda.empty_cache()

@@ -408,3 +408,65 @@ def test_large_scores(gpu_lib, fmt, draft, power, sign):
                 assert (np.abs(out[b, t, h] - v) <= 2.02 * UBF * np.abs(v)).all(), (b, t, h)
                 # dim products summed in float32, two scalings, the factor ln 2
                 assert abs(lse[b, t, h] - s[best]) <= (dim + 16) * 2 * U32 * abs(s[best]), (b, t, h)
+
+
+def _bf16(x):
+    return torch.from_numpy(np.asarray(x)).to(torch.bfloat16).double().numpy()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("dim,draft", [(64, 1), (64, 16), (128, 1), (128, 5), (256, 1), (256, 40)])
+@pytest.mark.parametrize("gain", [1.0, 0.05])
+def test_weights_at_twice_their_bits(gpu_lib, fmt, dim, draft, gain):
+    """With one tile of rows, and for wide heads, on bf16 and fp8 caches the weights go in with
+    twice bfloat16's bits.  Each sequence has two tokens with values that nearly cancel, so
+    that a result is small beside its parts and its own rounding hides nothing; the drafted
+    tokens see only those two.  With small queries, whose scores' worst case is small too,
+    weights rounded to bfloat16 would break the bound nearly everywhere."""
+    batch, heads = 16, 2
+    p = Problem(dim + draft, fmt, dim, heads, heads, [2] * batch, draft, q_gain=gain)
+    q = p.q.double().cpu().numpy()
+    scale = dim ** -0.5
+    for b in range(batch):
+        k = p.keys[b]
+        s = scale * np.einsum("hd,thd->th", q[b, 0], k[:2])
+        v = p.values[b].copy()
+        v[1] = -np.exp(s[0] - s[1])[:, None] * v[0]              # cancels for the first drafted token
+        slots = torch.tensor([p.slots_of(b, a) for a in range(2 + draft)], dtype=torch.int32, device=DEV)
+        # the keys as they were: codes of their own values (each row's largest is a code's value)
+        A.cache_write(p.cache, torch.from_numpy(k).float().to(DEV), torch.from_numpy(v).float().to(DEV), slots)
+        k, v = A.cache_read(p.cache, slots, torch.float32)
+        p.keys[b], p.values[b] = k.double().cpu().numpy(), v.double().cpu().numpy()
+    seen = np.zeros((batch, draft, draft), bool)
+    out = A.tree_attention(p.q, p.cache, p.table, p.lens_t, _words(seen)).double().cpu().numpy()
+    broken = 0
+    for b in range(batch):
+        for h in range(heads):
+            ref, _, spread, reach = AO.attention(q[b][:, h:h + 1], p.keys[b][:, h], p.values[b][:, h], 2, seen[b], scale)
+            # a score's errors as in Problem.check, in every weight and in their sum of two;
+            # each weight in two parts of 8 bits (2^-17), float32 products and sums; the result
+            e_s = (dim + 8) * 2 * U32 * reach
+            rel = 2.0 ** -17 * 1.01 + 4 * e_s + 16 * U32
+            bound = rel[..., None] * spread + UBF * 1.01 * np.abs(ref) + 1e-38
+            assert (np.abs(out[b][:, h:h + 1] - ref) <= bound).all(), (b, h)
+            # the planted mistake, on the CPU: the weights rounded to bfloat16 once
+            s = scale * q[b][0, h] @ p.keys[b][:2, h].T
+            w = np.exp(s - s.max())
+            once = _bf16(w) @ p.values[b][:2, h] / w.sum()
+            broken += int((np.abs(once - ref[0, 0]) > bound[0, 0]).any())
+    assert gain == 1.0 or broken >= batch * heads // 2
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "opq4"])
+@pytest.mark.parametrize("dim,heads,kv,page", [(64, 8, 2, 32), (128, 8, 1, 64), (256, 4, 2, 16)])
+def test_prompt(gpu_lib, fmt, dim, heads, kv, page):
+    """A prompt as one chain of 333 tokens: many groups of rows, each with its own end of the
+    keys, alone and after tokens that are cached already."""
+    lens, draft = [0, 77], 333
+    p = Problem(dim + page, fmt, dim, heads, kv, lens, draft, page=page)
+    out, lse = A.tree_attention(p.q, p.cache, p.table, p.lens_t, return_lse=True)
+    p.check(out, lse, _chain(2, draft))
+    counts = [333, 200]
+    ct = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    out, lse = A.tree_attention(p.q, p.cache, p.table, p.lens_t, counts=ct, return_lse=True)
+    p.check(out, lse, _chain(2, draft), counts)
