@@ -122,7 +122,9 @@ typedef enum {
  * quantized formats a row whose max is below 2^-100 gets scale 0 and codes 0.
  * A row with a NaN or an infinity (for OPQ_CACHE_BF16: after rounding to
  * bfloat16) gets scale NaN and codes 0, so every value of it reads as NaN: no
- * code is ever a NaN, and a token that a mask hides cannot leak one.
+ * code is ever a NaN, and a token that a mask hides cannot leak one.  (Rows that were
+ * never written hold what the memory held: start a cache as zeros, or write every token
+ * that a sequence's length and draft cover, hidden ones too.)
  */
 typedef struct {
   void* k;
@@ -213,9 +215,9 @@ size_t opq_cache_attention_workspace_bytes(int64_t batch, int64_t draft, int64_t
  *   lse   device out, dense [batch][draft][heads] float32, or NULL
  *   workspace  at least opq_cache_attention_workspace_bytes(...) bytes, no
  *         initialisation; calls that may overlap need their own
- * Scores, the softmax's maximum and sum, and the accumulators are float32; scores may
- * be as large as float32 holds (past 2^26 they are rounded to it before they are
- * compared, so what differs by less counts as equal or as whole steps apart).  The
+ * Scores, the softmax's maximum and sum, and the accumulators are float32.  Scores may
+ * be as large as float32 holds; two that differ by less than its spacing there may come
+ * out equal, or that spacing apart.  The
  * accumulators are divided by the weights' sum at the end, and weights are at
  * most 1: values of up to 2^127 divided by the number of keys cannot overflow.
  * For the matrix product with the codes the weights p v_scale are rounded to

@@ -31,11 +31,12 @@
 //
 // Bounds.  Few rows: memory, at the rate of a large copy.  32 sequences of up to
 // 8191 tokens, 32 query and 8 kv heads of 128, fp8: 61 us, 4.7 TB/s; 2 of 200000
-// tokens, 64 query heads, opq4: 110 us, 4.9 TB/s.  Many rows: the instructions and
+// tokens, 64 query heads, opq4: 116 us (108 at best), 4.6 TB/s.  Many rows: the instructions and
 // waits of a step, as every 32 rows walk over the keys again from the L2 (81 % hits).
 // Trees of 48 tokens on 8 sequences of up to 6001 tokens, bf16: 88 us, 12 % of the
 // matrix cores' and 28 % of the VALU's time; 3 of up to 4093 tokens, 16 heads of 256,
-// 21 tokens each, fp8: 23 us.  One sequence of 1000 tokens: 6 us, two launches.
+// 21 tokens each, fp8: 22 us.  One sequence of 1000 tokens: 6.5 us, and 3.3 for the join.
+// A prompt of 8192 tokens, 32 query and 8 kv heads of 128, bf16: 1330 us, 413 TFLOP/s.
 //
 // Measured and not taken: waves that share decoded keys in LDS and split the rows
 // (4 or 8 waves, 91 to 146 us where this takes 70 to 98); four tiles of rows to a
@@ -612,8 +613,8 @@ __device__ __forceinline__ bf16x8_t query_at(const AttentionArgs& a, const Task&
 
 // Workgroups a CU's registers have to hold.  Two, so that one computes while the
 // other waits, is what everything but a wide bfloat16 tile fits in; one tile of narrow
-// heads has registers for three (32 sequences of 8191 tokens, 8 kv heads of 64, opq4:
-// 45.5 us, 49.2 with two; at 128 dimensions there is no difference).
+// heads has registers for three (32 sequences of 8191 tokens, 8 kv heads of 64, opq4, with
+// the join: 57 us, 60 with two; fp8 57 both ways; at 128 dimensions there is no difference).
 template <int FMT, int D, int NT>
 constexpr int kOccupancy = FMT == OPQ_CACHE_BF16 && D == 256 ? 1 : NT * D == 64 ? 3 : 2;
 

@@ -13,9 +13,9 @@
 // the maximum is a few lane exchanges and nothing is read twice.  With few tokens
 // the launch bounds both ways (48 tokens of 8 heads of 128, fp8: 2.8 us to write, 2.5
 // to read).  Reading long histories is bound by memory: 131072 tokens of 8 heads of 128
-// from opq4, 133 us, 5.3 TB/s.  Writing 32768 such tokens takes 47 us for opq4 (3.8
+// from opq4, 133 us, 5.3 TB/s.  Writing 32768 such tokens takes 48 us for opq4 (3.7
 // TB/s), bound by the VALU (a logarithm and an exponential, each four issue slots, of
-// some twenty a value); fp8 and bf16 by memory: 37 and 41 us, 5.5 and 6.6 TB/s.
+// some twenty a value); fp8 and bf16 by memory: 37 and 44 us, 5.5 and 6.1 TB/s.
 #include "attention_internal.hpp"
 #include "decode.hpp"
 

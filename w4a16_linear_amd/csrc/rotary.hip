@@ -22,8 +22,9 @@ struct alignas(sizeof(T) * A < 16 ? sizeof(T) * A : 16) Pack {
 };
 
 // The stores of a large call carry the nontemporal hint: 4096 tokens of 60 heads of
-// 128, bfloat16, 28.9 us without and 23.7 with it (5.3 TB/s read and written); with
-// a reader behind them 47.5 and 44.4 together, in place 29.4 and 25.6.
+// 128 from rows of 90, three axes, bfloat16, 25.1 us a call without and 21.9 with it
+// (5.7 TB/s read and written); with a cache write of the result behind it 46.2 and 44.5
+// together, in place 23.8 and 21.6.
 template <bool kStream, typename P>
 __device__ __forceinline__ void put(void* p, const P& v) {
   if constexpr (kStream && sizeof(P) == 16) {
