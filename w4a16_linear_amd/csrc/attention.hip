@@ -34,7 +34,7 @@
 // tokens, 64 query heads, opq4: 116 us (108 at best), 4.6 TB/s.  Many rows: the instructions and
 // waits of a step, as every 32 rows walk over the keys again from the L2 (81 % hits).
 // Trees of 48 tokens on 8 sequences of up to 6001 tokens, bf16: 88 us, 12 % of the
-// matrix cores' and 28 % of the VALU's time; 3 of up to 4093 tokens, 16 heads of 256,
+// matrix cores' and 29 % of the VALU's time; 3 of up to 4093 tokens, 16 heads of 256,
 // 21 tokens each, fp8: 22 us.  One sequence of 1000 tokens: 6.5 us, and 3.3 for the join.
 // A prompt of 8192 tokens, 32 query and 8 kv heads of 128, bf16: 1330 us, 413 TFLOP/s.
 //
