@@ -273,3 +273,25 @@ def test_prompt_at_once_equals_in_chunks(gpu_lib, fmt, dim, page):
     y = layer(x, at_once, table, zero)
     parts = [layer(x[:, a:b].contiguous(), chunks, table, zero + a, max_len=a) for a, b in ((0, 129), (129, 399), (399, 400))]
     _close(torch.cat(parts, 1), y)
+
+
+def test_rope_by_any_name(gpu_lib):
+    """One table a device, whether it is named by a tensor's device, an index or without one."""
+    layer = _layer(29, quantize=False)
+    table = layer.rope("cuda")
+    here = torch.cuda.current_device()
+    assert all(layer.rope(d) is table for d in ("cuda", f"cuda:{here}", torch.device("cuda"), torch.device("cuda", here),
+                                                table.device))
+
+
+def test_no_tokens(gpu_lib):
+    """A step without tokens, and one without sequences: nothing written, empty results."""
+    layer = _layer(31)
+    cache = layer.new_cache(2, 16, "fp8", device=DEV)
+    x = torch.randn(1, 3, 256, device=DEV).bfloat16()
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert layer(x[:, :0], cache, _pages(1, 2), zero).shape == (1, 0, 256)
+    assert layer(x[:0], cache, _pages(1, 2)[:0], zero[:0]).shape == (0, 3, 256)
+    counts = zero.clone()
+    assert layer(x[:, :1], cache, _pages(1, 2), zero, counts=counts).shape == (1, 1, 256)
+    assert not any(t.view(torch.uint8).any() for t in cache[2:] if t is not None)

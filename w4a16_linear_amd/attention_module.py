@@ -39,6 +39,12 @@ def token_slots(page_table: torch.Tensor, positions: torch.Tensor, page: int,
     return torch.where(inside, ids * page + positions % page, -1).to(torch.int32)
 
 
+def _int32(name: str, t: torch.Tensor, shape, device: torch.device, dense: bool = True) -> None:
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or (dense and not t.is_contiguous()):
+        raise ValueError(f"{name} must be{' contiguous' if dense else ''} int32 {shape} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
 class OPQAttention(nn.Module):
     """`qkv` [hidden -> (heads + 2 kv_heads) dim] and `o` [heads dim -> hidden] start as
     nn.Linear (replace_with_opq makes them OPQLinear); the rotary table, `rope`, covers
@@ -65,10 +71,12 @@ class OPQAttention(nn.Module):
         """The rotary table on `device`, made at the first call there and kept.  That call
         waits for it, so that every stream and thread may use what is kept without asking
         who made it; it cannot be part of a graph's capture."""
-        device = torch.device(device)
-        if device.type == "cuda" and device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
         table = self._ropes.get(device)
+        if table is None:   # a name, or the first call
+            device = torch.device(device)
+            if device.type == "cuda" and device.index is None:
+                device = torch.device("cuda", torch.cuda.current_device())
+            table = self._ropes.get(device)
         if table is None:
             if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the layer's rotary table is not made yet: call rope(device), or run the "
@@ -83,34 +91,31 @@ class OPQAttention(nn.Module):
         return A.new_cache(pages, self.kv_heads, page, self.dim, fmt, alpha, device)
 
     def _check(self, x, cache, page_table, lens, mask, depths, counts, max_len) -> None:
-        """All that the calls of a forward would refuse, before the first of them writes."""
+        """All that the calls of a forward would refuse, before the first of them writes (a
+        few microseconds: a step of one token is not much more on the host)."""
         if x.dim() != 3 or x.shape[2] != self.hidden or x.dtype != torch.bfloat16:
             raise ValueError(f"x must be bfloat16 [batch, draft, {self.hidden}], got {x.dtype} {tuple(x.shape)}")
-        if torch.is_grad_enabled() and (x.requires_grad or any(w.requires_grad for w in self.qkv.parameters())):
+        # qkv's own weights; those of modules inside it are met at rotary, before anything is written
+        if torch.is_grad_enabled() and (x.requires_grad or any(
+                w is not None and w.requires_grad for w in self.qkv._parameters.values())):
             raise RuntimeError("this layer serves and passes no gradients back: call it under torch.no_grad(), "
                                "or with x and the weights of qkv not requiring them")
         batch, draft, _ = x.shape
-        if (cache.heads, cache.dim) != (self.kv_heads, self.dim):
-            raise ValueError(f"the cache has {cache.heads} heads of {cache.dim}, the layer {self.kv_heads} of "
-                             f"{self.dim}")
-        wanted = [("page_table", page_table, (batch, page_table.shape[-1])), ("lens", lens, (batch,))]
+        _, heads, page = cache.k_scale.shape
+        if heads != self.kv_heads or cache.dim != self.dim:
+            raise ValueError(f"the cache has {heads} heads of {cache.dim}, the layer {self.kv_heads} of {self.dim}")
+        device, columns = x.device, page_table.shape[-1]
+        _int32("page_table", page_table, (batch, columns), device)
+        _int32("lens", lens, (batch,), device)
         if mask is not None:
             words = (draft, (draft + 31) // 32)
-            wanted.append(("mask", mask, words if mask.dim() == 2 else (batch,) + words))
-        if depths is not None:
-            wanted.append(("depths", depths, (batch, draft)))
+            _int32("mask", mask, words if mask.dim() == 2 else (batch,) + words, device)
+        if depths is not None:   # only enters a sum here; the others' memory goes to the kernels
+            _int32("depths", depths, (batch, draft), device, dense=False)
         if counts is not None:
-            wanted.append(("counts", counts, (batch,)))
-        for name, t, shape in wanted:
-            if t.dtype != torch.int32 or t.shape != shape or t.device != x.device:
-                raise ValueError(f"{name} must be int32 {shape} on {x.device}, got {t.dtype} {tuple(t.shape)} on "
-                                 f"{t.device}")
-        # depths only enter sums here; the others' memory goes to the kernels
-        if not all(t.is_contiguous() for name, t, _ in wanted if name != "depths"):
-            raise ValueError("page_table, lens, mask and counts must be contiguous")
-        if max_len is not None and not 0 <= max_len <= page_table.shape[1] * cache.page:
-            raise ValueError(f"max_len must be 0 to {page_table.shape[1] * cache.page}, what the page table "
-                             f"holds, got {max_len}")
+            _int32("counts", counts, (batch,), device)
+        if max_len is not None and not 0 <= max_len <= columns * page:
+            raise ValueError(f"max_len must be 0 to {columns * page}, what the page table holds, got {max_len}")
 
     def forward(self, x: torch.Tensor, cache: A.PagedCache, page_table: torch.Tensor,
                 lens: torch.Tensor, mask: Optional[torch.Tensor] = None,
@@ -124,13 +129,16 @@ class OPQAttention(nn.Module):
             raise ValueError("a mask needs depths: a tree's tokens are not at the positions of their places")
         self._check(x, cache, page_table, lens, mask, depths, counts, max_len)
         batch, draft, _ = x.shape
+        pages, _, page = cache.k_scale.shape
         rope = self.rope(x.device)
-        steps = torch.arange(draft, dtype=torch.int32, device=x.device)
-        places = lens[:, None] + steps                       # where tokens are stored
+        places = lens[:, None]                               # where tokens are stored
+        if draft != 1 or counts is not None:
+            steps = torch.arange(draft, dtype=torch.int32, device=x.device)
+            places = places + steps
         positions = places if depths is None else lens[:, None] + depths
         if counts is not None:
             places = torch.where(steps < counts[:, None], places, -1)
-        slots = token_slots(page_table, places, cache.page, cache.pages)
+        slots = token_slots(page_table, places, page, pages)
         h, k = self.heads, self.kv_heads
         fused = self.qkv(x).view(batch * draft, h + 2 * k, self.dim)
         qk = fused[:, :h + k]
