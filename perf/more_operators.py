@@ -48,37 +48,37 @@ CODES = {"bf16": (torch.bfloat16, 2.0), "fp8": (torch.uint8, 1.0), "opq4": (torc
 def listed():
     return [
         # one user with an adapter of their own on the output projection, one new token
-        dict(name="adapters, one token", op="adapters", tokens=1, k=HIDDEN, n=HIDDEN, rank=8,
+        dict(name="adapters: one token", op="adapters", tokens=1, k=HIDDEN, n=HIDDEN, rank=8,
              adapters=4, requests=1, dtype="bf16", out="bf16"),
         # 48 users, one new token each, adapters out of 64, on the fused QKV projection
-        dict(name="adapters, one token each", op="adapters", tokens=48, k=HIDDEN, n=QKV, rank=16,
+        dict(name="adapters: one token each", op="adapters", tokens=48, k=HIDDEN, n=QKV, rank=16,
              adapters=64, requests=48, dtype="bf16", out="bf16"),
         # the prompts of several requests, ranks padded to the largest, on the FFN's up and gate projection
-        dict(name="adapters, prompts", op="adapters", tokens=4096, k=HIDDEN, n=FFN_UPGATE, rank=64,
+        dict(name="adapters: prompts", op="adapters", tokens=4096, k=HIDDEN, n=FFN_UPGATE, rank=64,
              adapters=16, requests=7, dtype="bf16", out="bf16"),
         # a training step of one adapter on the fused QKV projection
-        dict(name="adapters' gradients, one", op="gradients", tokens=4096, k=HIDDEN, n=QKV, rank=16,
+        dict(name="adapters' gradients: one", op="gradients", tokens=4096, k=HIDDEN, n=QKV, rank=16,
              adapters=1, requests=1, dtype="bf16", out="bf16"),
         # several adapters trained at once on the FFN's down projection, sums kept in 32 bits, odd length
-        dict(name="adapters' gradients, several", op="gradients", tokens=2047, k=FFN, n=HIDDEN, rank=32,
+        dict(name="adapters' gradients: several", op="gradients", tokens=2047, k=FFN, n=HIDDEN, rank=32,
              adapters=5, requests=9, dtype="bf16", out="f32"),
         # the gradient through the quantized output projection, a short odd batch, one max a group of 128
-        dict(name="projection's gradient, short", op="linear", tokens=333, k=HIDDEN, n=HIDDEN, group=128,
+        dict(name="projection's gradient: short", op="linear", tokens=333, k=HIDDEN, n=HIDDEN, group=128,
              out="bf16"),
         # the gradient through the quantized QKV projection
         dict(name="projection's gradient", op="linear", tokens=4096, k=HIDDEN, n=QKV, group=0, out="bf16"),
         # one user, a tree of candidates
-        dict(name="verify, one tree", op="verify", batch=1, draft=24, vocab=32000, tree=True, dtype="f32"),
+        dict(name="verify: one tree", op="verify", batch=1, draft=24, vocab=32000, tree=True, dtype="f32"),
         # a serving batch, chains from a draft model
-        dict(name="verify, chains", op="verify", batch=48, draft=6, vocab=131072, tree=False, dtype="f32"),
+        dict(name="verify: chains", op="verify", batch=48, draft=6, vocab=131072, tree=False, dtype="f32"),
         # four users' beams of eight, forked after a step, with the copies of their last pages
-        dict(name="pages, beams forked", op="fork", rows=32, columns=24, beams=8, page=64, pages=512,
+        dict(name="pages: beams forked", op="fork", rows=32, columns=24, beams=8, page=64, pages=512,
              heads=8, dim=128, fmt="fp8"),
         # a large pool: many samples of some prompts; new tables, few copies
-        dict(name="pages, many rows forked", op="fork", rows=1024, columns=300, beams=16, page=16,
+        dict(name="pages: many rows forked", op="fork", rows=1024, columns=300, beams=16, page=16,
              pages=65536, heads=1, dim=64, fmt="fp8"),
         # a cache drawn together before memory is handed back
-        dict(name="pages, compacted", op="compact", rows=128, columns=40, page=64, pages=4096, used=2100,
+        dict(name="pages: compacted", op="compact", rows=128, columns=40, page=64, pages=4096, used=2100,
              moved=900, heads=8, dim=128, fmt="opq4"),
     ]
 
