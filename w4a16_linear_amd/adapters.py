@@ -1,0 +1,172 @@
+"""Python binding of libopq's adapters (include/opq_adapters.h): low-rank adapters of many
+requests beside one shared projection, their gradients, and the gradient through a quantized
+projection.
+
+As in ``attention``, tensors are checked, outputs are allocated with torch on the caller's
+device, and raw pointers go to the library with the current torch stream; workspaces come
+from torch's allocator per call, so calls on different streams do not share one.
+
+    stack = Adapters(down, up, scale)             # of one projection, every customer's
+    y = opq.linear(x, weight, alpha, out_dtype=torch.bfloat16)
+    lowrank_add(y, x, stack, index, out=y)        # index: which adapter each token uses, or -1
+
+Under autograd use apply_linear and apply_lowrank (module.AdaptedLinear does); the other
+calls refuse tensors that require grad, as attention's do.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional, Tuple
+
+import torch
+
+from . import attention, opq
+from .opq import OPQ_BF16, OPQ_F32, _check
+
+_P, _I, _L, _F, _Z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t)
+
+# signatures in header order
+_SIGNATURES = {
+    "opq_lowrank_workspace_bytes": (_Z, [_L, _L, _L, _L]),
+    "opq_lowrank_add": (_I, [_P, _P, _L, _P, _L, _P, _L, _I, _P, _L, _I, _P, _Z, _P]),
+    "opq_lowrank_backward_workspace_bytes": (_Z, [_L, _L, _L, _L, _L]),
+    "opq_lowrank_backward": (_I, [_P, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _L, _P, _P, _I, _P, _Z, _P]),
+    "opq_linear_backward_workspace_bytes": (_Z, [_L, _L, _L]),
+    "opq_linear_backward": (_I, [_P, _P, _P, _P, _L, _L, _L, _F, _P, _I, _P, _Z, _P]),
+    "opq_linear_backward_bits": (_I, [_P, _P, _P, _P, _L, _L, _L, _I, _F, _P, _I, _P, _Z, _P]),
+    "opq_linear_backward_grouped": (_I, [_P, _P, _P, _P, _L, _L, _L, _L, _F, _P, _I, _P, _Z, _P]),
+}
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_ready: Optional[ctypes.CDLL] = None
+
+
+def load() -> ctypes.CDLL:
+    """libopq.so with the adapters' signatures set; raises if it or the extension is missing."""
+    global _ready
+    if _ready is None:
+        lib = attention.load()
+        for name, (res, args) in _SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _ready = lib
+    return _ready
+
+
+def _calls():
+    return attention._ext or attention._calls()
+
+
+class Adapters(NamedTuple):
+    """A stack of low-rank adapters of one projection [in -> out]: token t with adapter i gets
+    scale[i] * up[i]^T (down[i] x_t) added.  The rank is a multiple of 8, up to 128 (smaller ranks:
+    rows of zeros); in and out are multiples of 8."""
+    down: torch.Tensor    # bfloat16 [adapters, rank, in]
+    up: torch.Tensor      # bfloat16 [adapters, rank, out]: the transpose of a layer's [out, rank]
+    scale: torch.Tensor   # float32 [adapters]
+
+
+def _float(what: str, dtype: torch.dtype) -> bool:
+    if dtype not in _FLOATS:
+        raise ValueError(f"{what} must be float32 or bfloat16, got {dtype}")
+    return dtype == torch.bfloat16
+
+
+def lowrank_add(y: Optional[torch.Tensor], x: torch.Tensor, adapters: Adapters, index: torch.Tensor,
+                out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [tokens, out] (float32 or bfloat16; None: zeros) plus, for every token, its adapter's
+    output.  x: bfloat16 [tokens, in]; index: int32 [tokens], the adapter of each token (outside
+    0..adapters-1, such as -1: none, the token keeps its y).  Rows are dense, their strides free
+    (multiples of 8).  Returns `out` (which may be y), or a new tensor of out_dtype (y's type
+    by default, bfloat16 without y)."""
+    if out_dtype is None:
+        out_dtype = y.dtype if isinstance(y, torch.Tensor) else torch.bfloat16
+    bf16 = _float("out_dtype", out_dtype) if out is None else False
+    return _calls().lowrank_add(y, x, adapters, index, out, bf16, workspace)
+
+
+def lowrank_backward(dy: torch.Tensor, x: torch.Tensor, adapters: Adapters, index: torch.Tensor,
+                     dx: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     dx_dtype: torch.dtype = torch.bfloat16, grad_dtype: torch.dtype = torch.float32,
+                     input_grad: bool = True, adapter_grads: bool = True,
+                     workspace: Optional[torch.Tensor] = None
+                     ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(dx, d_down, d_up) from dy, bfloat16 [tokens, out].  dx: what the adapters give is added
+    to `dx` [tokens, in] (None: zeros) in its type (dx_dtype without one), into `out` (which may be
+    `dx`) or a new tensor.  d_down and d_up have the stack's shapes, in grad_dtype; adapters without
+    tokens get zeros.  input_grad, adapter_grads: which are wanted (None in the place of others)."""
+    return _calls().lowrank_backward(dy, x, adapters, index, dx, out, _float("dx_dtype", dx_dtype),
+                                     _float("grad_dtype", grad_dtype), input_grad, adapter_grads, workspace)
+
+
+# ------------------------------------------------------- through the projection
+
+def linear_backward_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(load().opq_linear_backward_workspace_bytes(m, n, k))
+
+
+def _check_rows(qw, n: int, k: int) -> None:
+    for name, t in (("packed", qw.packed), ("sign", qw.sign)):
+        opq._need_cuda(name, t, torch.int32, 2)
+    opq._need_cuda("scale", qw.scale, torch.float32, 1)
+    if tuple(qw.packed.shape) != (n, k // 8) or tuple(qw.sign.shape) != (n, k // 32) or tuple(qw.scale.shape) != (n,):
+        raise ValueError(f"weight buffers do not match n={n}, k={k}")
+
+
+def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.Tensor] = None,
+                    out_dtype: torch.dtype = torch.bfloat16,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx [m, k] = dy [m, n] W', the gradient of opq.linear's x: dy bfloat16, weight any of
+    opq's stored forms.  `workspace`: a device tensor of linear_backward_workspace_bytes(m, n, k)
+    bytes (by default one of torch's allocator)."""
+    lib = load()
+    opq._need_cuda("dy", dy, torch.bfloat16, 2)
+    if torch.is_grad_enabled() and dy.requires_grad:
+        raise RuntimeError("dy requires grad, which this call does not follow: detach it, or call under "
+                           "torch.no_grad()")
+    m = dy.shape[0]
+    n, k = weight.shape
+    if dy.shape[1] != n:
+        raise ValueError(f"dy has n={dy.shape[1]}, weight has n={n}")
+    if out is None:
+        _float("out_dtype", out_dtype)
+        out = torch.empty((m, k), dtype=out_dtype, device=dy.device)
+    else:
+        opq._need_cuda("out", out, out.dtype, 2)
+        bf16 = _float("out", out.dtype)
+        if tuple(out.shape) != (m, k):
+            raise ValueError(f"out must have shape {(m, k)}, got {tuple(out.shape)}")
+        if torch.is_grad_enabled() and out.requires_grad:
+            raise RuntimeError("out requires grad, which this call does not follow")
+        if not out.is_inference():
+            torch.autograd.graph.increment_version(out)
+    for name, t in (("out", out), ("packed", weight.packed), ("sign", weight.sign), ("scale", weight[2])):
+        if t.device != dy.device:
+            raise ValueError(f"{name} must be on {dy.device}, got {t.device}")
+    need = linear_backward_workspace_bytes(m, n, k)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
+    elif workspace.device != dy.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dy.device}")
+    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    tail = (out.data_ptr(), OPQ_BF16 if out.dtype == torch.bfloat16 else OPQ_F32, opq._ptr(workspace), room)
+    with torch.cuda.device(dy.device):
+        tail = tail + (opq._stream(dy.device),)
+        if isinstance(weight, opq.BitsWeight):
+            opq._check_bits(weight, n, k)
+            _check("opq_linear_backward_bits",
+                   lib.opq_linear_backward_bits(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
+                                                weight.scale.data_ptr(), m, n, k, weight.bits, alpha, *tail))
+        elif isinstance(weight, opq.GroupedWeight):
+            opq._check_grouped(weight, n, k)
+            _check("opq_linear_backward_grouped",
+                   lib.opq_linear_backward_grouped(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
+                                                   weight.scale16.data_ptr(), m, n, k, weight.group, alpha, *tail))
+        else:
+            _check_rows(weight, n, k)
+            _check("opq_linear_backward",
+                   lib.opq_linear_backward(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
+                                           weight.scale.data_ptr(), m, n, k, alpha, *tail))
+    return out

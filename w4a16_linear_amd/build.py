@@ -26,10 +26,11 @@ LIB = os.path.join(HERE, "libopq.so")
 CEILING_LIB = os.path.join(HERE, "libopq_ceiling.so")
 
 SOURCES = ["opq_api.cpp", "tables.cpp", "quantize.hip", "dequantize.hip", "linear.hip",
-           "attention_api.cpp", "rotary.hip", "cache.hip", "attention.hip"]
+           "attention_api.cpp", "rotary.hip", "cache.hip", "attention.hip",
+           "adapters_api.cpp", "lowrank.hip", "linear_backward.hip"]
 CEILING_SOURCES = ["stream_ceiling.hip"]
-# the attention side's calls on torch tensors, a CPython extension over libopq.so
-EXT_SOURCE = "attention_torch.cpp"
+# the attention side's and the adapters' calls on torch tensors, a CPython extension over libopq.so
+EXT_SOURCES = ["attention_torch.cpp", "adapters_torch.cpp"]
 EXT_LIB = os.path.join(HERE, "_attention.so")
 ARCH = "gfx950"
 
@@ -108,13 +109,18 @@ def extension_lacks() -> str:
     return ""
 
 
-def _compile_extension(verbose: bool) -> str:
+def _compile_extension(verbose: bool) -> list:
+    with cf.ThreadPoolExecutor(max_workers=len(EXT_SOURCES)) as ex:
+        return list(ex.map(lambda src: _compile_extension_source(src, verbose), EXT_SOURCES))
+
+
+def _compile_extension_source(src: str, verbose: bool) -> str:
     import sysconfig
 
     import torch
 
     here = os.path.dirname(torch.__file__)
-    obj = os.path.join(OBJDIR, EXT_SOURCE + ".o")
+    obj = os.path.join(OBJDIR, src + ".o")
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
@@ -123,23 +129,23 @@ def _compile_extension(verbose: bool) -> str:
            "-isystem", os.path.join(here, "include"),
            "-isystem", os.path.join(here, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
-           "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+           "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"compile failed: {EXT_SOURCE}\n{r.stdout}{r.stderr}")
+        raise RuntimeError(f"compile failed: {src}\n{r.stdout}{r.stderr}")
     return obj
 
 
-def _link_extension(obj: str, verbose: bool) -> None:
+def _link_extension(objs: list, verbose: bool) -> None:
     import torch
 
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = EXT_LIB + ".tmp"
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     # torch's libraries are loaded by `import torch`; libopq.so lies beside the extension
-    cmd = [cxx, "-shared", "-fPIC", "-o", tmp, obj, "-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu",
+    cmd = [cxx, "-shared", "-fPIC", "-o", tmp] + objs + ["-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu",
            "-ltorch_python", "-L", HERE, "-l:libopq.so", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -1,0 +1,221 @@
+// The C ABI of the adapters (include/opq_adapters.h): argument checks in the
+// documented order, host tables, then the launches on the caller's stream.
+#include "opq_adapters.h"
+
+#include <hip/hip_runtime_api.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "adapters_internal.hpp"
+#include "opq_internal.hpp"
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 22;
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+constexpr int64_t kMaxElements = int64_t(1) << 39;
+constexpr int64_t kMaxLinear = 65536;
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool aligned4(const void* p) { return aligned(p, 4); }
+bool aligned16(const void* p) { return aligned(p, 16); }
+bool dtype_ok(int d) { return d == OPQ_F32 || d == OPQ_BF16; }
+int hip_status(hipError_t e) { return e == hipSuccess ? OPQ_OK : OPQ_ERR_HIP; }
+
+bool sizes_ok(int64_t m, int64_t k, int64_t n, int64_t rank) {
+  return m >= 0 && k >= 8 && k % 8 == 0 && n >= 8 && n % 8 == 0 && rank >= 8 && rank <= 128 &&
+         rank % 8 == 0;
+}
+// Rows of an output must not overlap; an input's may be the same.
+bool in_stride_ok(int64_t s, int64_t width) { return s == 0 || s >= width; }
+bool sizes_supported(int64_t m, int64_t k, int64_t n) {
+  return m <= kMaxTokens && k <= kMaxWidth && n <= kMaxWidth;
+}
+bool within(int64_t m, int64_t stride) { return m == 0 || stride <= kMaxElements / m; }
+
+}  // namespace
+
+extern "C" {
+
+size_t opq_lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank) {
+  if (!sizes_ok(m, k, n, rank) || !sizes_supported(m, k, n) || m == 0) return 0;
+  return opq::lowrank_workspace_bytes(m, k, n, rank);
+}
+
+int opq_lowrank_add(const opq_lowrank* adapters, const uint16_t* x, int64_t x_stride,
+                    const int32_t* index, int64_t m, const void* y, int64_t y_stride, int y_dtype,
+                    void* out, int64_t out_stride, int out_dtype, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!adapters) return OPQ_ERR_NULL;
+  const opq_lowrank& a = *adapters;
+  if ((a.count > 0 && (!a.down || !a.up || !a.scale)) || (m > 0 && (!x || !index || !out)))
+    return OPQ_ERR_NULL;
+  if (!sizes_ok(m, a.k, a.n, a.rank) || a.count < 0 || !in_stride_ok(x_stride, a.k) ||
+      (y && !in_stride_ok(y_stride, a.n)) || out_stride < a.n)
+    return OPQ_ERR_SHAPE;
+  if (!aligned16(a.down) || !aligned16(a.up) || !aligned4(a.scale) || !aligned16(x) ||
+      !aligned4(index) || !aligned16(y) || !aligned16(out) || !aligned16(workspace) ||
+      x_stride % 8 || (y && y_stride % 8) || out_stride % 8)
+    return OPQ_ERR_ALIGN;
+  if ((y && !dtype_ok(y_dtype)) || !dtype_ok(out_dtype)) return OPQ_ERR_DTYPE;
+  const size_t need = opq_lowrank_workspace_bytes(m, a.k, a.n, a.rank);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return OPQ_ERR_WORKSPACE;
+  if (!sizes_supported(m, a.k, a.n) || a.count > (int64_t(1) << 30) || !within(m, x_stride) ||
+      (y && !within(m, y_stride)) || !within(m, out_stride))
+    return OPQ_ERR_UNSUPPORTED;
+  if (m == 0) return OPQ_OK;
+  opq::LowrankAdd c{};
+  c.a = a;
+  c.x = x;
+  c.x_stride = x_stride;
+  c.index = index;
+  c.m = m;
+  c.y = y;
+  c.y_stride = y_stride;
+  c.y_bf16 = y && y_dtype == OPQ_BF16;
+  c.out = out;
+  c.out_stride = out_stride;
+  c.out_bf16 = out_dtype == OPQ_BF16;
+  c.workspace = workspace;
+  return hip_status(opq::launch_lowrank_add(c, static_cast<hipStream_t>(stream)));
+}
+
+size_t opq_lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank,
+                                            int64_t count) {
+  if (!sizes_ok(m, k, n, rank) || !sizes_supported(m, k, n) || count < 0 || count > opq::kMaxTrained)
+    return 0;
+  return opq::lowrank_backward_workspace_bytes(m, k, n, rank, count);
+}
+
+int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_t dy_stride,
+                         const uint16_t* x, int64_t x_stride, const int32_t* index, int64_t m,
+                         const void* dx, int64_t dx_stride, int dx_dtype, void* dx_out,
+                         int64_t dx_out_stride, void* d_down, void* d_up, int grad_dtype,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (!adapters) return OPQ_ERR_NULL;
+  const opq_lowrank& a = *adapters;
+  if ((a.count > 0 && (!a.down || !a.up || !a.scale || !d_down != !d_up)) ||
+      (m > 0 && (!dy || !x || !index)))
+    return OPQ_ERR_NULL;
+  if (!sizes_ok(m, a.k, a.n, a.rank) || a.count < 0 || !in_stride_ok(dy_stride, a.n) ||
+      !in_stride_ok(x_stride, a.k) || (dx && !in_stride_ok(dx_stride, a.k)) ||
+      (dx_out && dx_out_stride < a.k))
+    return OPQ_ERR_SHAPE;
+  if (!aligned16(a.down) || !aligned16(a.up) || !aligned4(a.scale) || !aligned16(dy) ||
+      !aligned16(x) || !aligned4(index) || !aligned16(dx) || !aligned16(dx_out) ||
+      !aligned16(d_down) || !aligned16(d_up) || !aligned16(workspace) || dy_stride % 8 ||
+      x_stride % 8 || (dx && dx_stride % 8) || (dx_out && dx_out_stride % 8))
+    return OPQ_ERR_ALIGN;
+  if ((dx_out && !dtype_ok(dx_dtype)) || (d_down && !dtype_ok(grad_dtype))) return OPQ_ERR_DTYPE;
+  const size_t need = opq_lowrank_backward_workspace_bytes(m, a.k, a.n, a.rank, a.count);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return OPQ_ERR_WORKSPACE;
+  if (!sizes_supported(m, a.k, a.n) || a.count > opq::kMaxTrained || !within(m, dy_stride) ||
+      !within(m, x_stride) || (dx && !within(m, dx_stride)) || (dx_out && !within(m, dx_out_stride)))
+    return OPQ_ERR_UNSUPPORTED;
+  if ((m == 0 || !dx_out) && (a.count == 0 || !d_down)) return OPQ_OK;
+  opq::LowrankBackward c{};
+  c.a = a;
+  c.dy = dy;
+  c.dy_stride = dy_stride;
+  c.x = x;
+  c.x_stride = x_stride;
+  c.index = index;
+  c.m = m;
+  c.dx = dx;
+  c.dx_stride = dx_stride;
+  c.dx_bf16 = dx_dtype == OPQ_BF16;
+  c.dx_out = m > 0 ? dx_out : nullptr;
+  c.dx_out_stride = dx_out_stride;
+  c.d_down = a.count > 0 ? d_down : nullptr;
+  c.d_up = a.count > 0 ? d_up : nullptr;
+  c.grad_bf16 = grad_dtype == OPQ_BF16;
+  c.workspace = workspace;
+  return hip_status(opq::launch_lowrank_backward(c, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------- projection's gradient
+
+size_t opq_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || k % 32 || m > kMaxTokens || n > kMaxLinear || k > kMaxLinear)
+    return 0;
+  const size_t ld = (size_t)(n + 31) / 32 * 32;
+  // W', W' transposed (rows of ld), and dy with such rows where its own are shorter
+  return (size_t)n * k * 2 + (size_t)k * ld * 2 + ((size_t)n < ld ? (size_t)m * ld * 2 : 0);
+}
+
+// The checks of one storage form; `more` its own about shapes and types.
+static int backward_checks(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
+                           const void* scale, int64_t m, int64_t n, int64_t k, float alpha,
+                           bool more_shape_ok, const void* dx, int dx_dtype, const void* workspace,
+                           size_t workspace_bytes) {
+  if ((m > 0 && n > 0 && !dy) || (n > 0 && k > 0 && (!packed || !sign || !scale)) ||
+      (m > 0 && k > 0 && !dx))
+    return OPQ_ERR_NULL;
+  if (m < 0 || n < 0 || k < 0 || k % 32 || !more_shape_ok) return OPQ_ERR_SHAPE;
+  if (!(std::isfinite(alpha) && alpha > 0.0f)) return OPQ_ERR_ALPHA;
+  if (!aligned16(dy) || !aligned16(packed) || !aligned16(sign) || !aligned16(scale) ||
+      !aligned16(dx) || !aligned16(workspace))
+    return OPQ_ERR_ALIGN;
+  if (!dtype_ok(dx_dtype)) return OPQ_ERR_DTYPE;
+  const size_t need = opq_linear_backward_workspace_bytes(m, n, k);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return OPQ_ERR_WORKSPACE;
+  if (m > kMaxTokens || n > kMaxLinear || k > kMaxLinear) return OPQ_ERR_UNSUPPORTED;
+  return OPQ_OK;
+}
+
+// W' is in the workspace's first n k elements.
+static int backward_product(const uint16_t* dy, int64_t m, int64_t n, int64_t k, void* dx,
+                            int dx_dtype, void* workspace, hipStream_t st) {
+  const int64_t ld = (n + 31) / 32 * 32;
+  const uint16_t* w = static_cast<const uint16_t*>(workspace);
+  uint16_t* wt = static_cast<uint16_t*>(workspace) + n * k;
+  int e = n > 0 ? hip_status(opq::launch_transpose(w, n, k, wt, ld, st)) : OPQ_OK;
+  if (e == OPQ_OK && n < ld) {
+    uint16_t* padded = wt + k * ld;
+    e = hip_status(opq::launch_pad_rows(dy, m, n, padded, ld, st));
+    dy = padded;
+  }
+  if (e != OPQ_OK) return e;
+  return hip_status(opq::launch_linear_dense(dy, wt, nullptr, m, k, ld, dx, dx_dtype == OPQ_BF16, st));
+}
+
+int opq_linear_backward(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
+                        const float* scale, int64_t m, int64_t n, int64_t k, float alpha, void* dx,
+                        int dx_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, true, dx, dx_dtype, workspace,
+                          workspace_bytes);
+  if (e != OPQ_OK || m == 0 || k == 0) return e;
+  e = opq_dequantize(packed, sign, scale, n, k, alpha, static_cast<uint16_t*>(workspace), stream);
+  if (e != OPQ_OK) return e;
+  return backward_product(dy, m, n, k, dx, dx_dtype, workspace, static_cast<hipStream_t>(stream));
+}
+
+int opq_linear_backward_bits(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
+                             const float* scale, int64_t m, int64_t n, int64_t k, int bits,
+                             float alpha, void* dx, int dx_dtype, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, bits >= 3 && bits <= 6, dx,
+                          dx_dtype, workspace, workspace_bytes);
+  if (e != OPQ_OK || m == 0 || k == 0) return e;
+  e = opq_dequantize_bits(packed, sign, scale, n, k, bits, alpha, static_cast<uint16_t*>(workspace),
+                          stream);
+  if (e != OPQ_OK) return e;
+  return backward_product(dy, m, n, k, dx, dx_dtype, workspace, static_cast<hipStream_t>(stream));
+}
+
+int opq_linear_backward_grouped(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
+                                const uint16_t* scale16, int64_t m, int64_t n, int64_t k,
+                                int64_t group, float alpha, void* dx, int dx_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const bool group_ok = (group == 32 || group == 64 || group == 128 || group == 256) && k % group == 0;
+  int e = backward_checks(dy, packed, sign, scale16, m, n, k, alpha, group_ok, dx, dx_dtype,
+                          workspace, workspace_bytes);
+  if (e != OPQ_OK || m == 0 || k == 0) return e;
+  e = opq_dequantize_grouped(packed, sign, scale16, n, k, group, alpha,
+                             static_cast<uint16_t*>(workspace), stream);
+  if (e != OPQ_OK) return e;
+  return backward_product(dy, m, n, k, dx, dx_dtype, workspace, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

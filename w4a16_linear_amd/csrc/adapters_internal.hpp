@@ -1,0 +1,59 @@
+// Internal interface between the C ABI of the adapters (adapters_api.cpp) and
+// their kernel launchers.  Not installed.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "opq_adapters.h"
+
+namespace opq {
+
+// lowrank.hip
+struct LowrankAdd {
+  opq_lowrank a;
+  const uint16_t* x;
+  int64_t x_stride;
+  const int32_t* index;
+  int64_t m;
+  const void* y;  // or nullptr
+  int64_t y_stride;
+  bool y_bf16;
+  void* out;
+  int64_t out_stride;
+  bool out_bf16;
+  void* workspace;
+};
+size_t lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank);
+hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream);
+
+constexpr int64_t kMaxTrained = 1024;  // adapters of a backward pass: its counts are held in LDS
+struct LowrankBackward {
+  opq_lowrank a;
+  const uint16_t* dy;
+  int64_t dy_stride;
+  const uint16_t* x;
+  int64_t x_stride;
+  const int32_t* index;
+  int64_t m;
+  const void* dx;  // or nullptr
+  int64_t dx_stride;
+  bool dx_bf16;
+  void* dx_out;  // or nullptr
+  int64_t dx_out_stride;
+  void* d_down;  // both or neither
+  void* d_up;
+  bool grad_bf16;
+  void* workspace;
+};
+size_t lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank, int64_t count);
+hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream);
+
+// linear_backward.hip: dst [k][ld] = the transpose of w [n][k] (bfloat16), columns n..ld-1 zero
+hipError_t launch_transpose(const uint16_t* w, int64_t n, int64_t k, uint16_t* dst, int64_t ld,
+                            hipStream_t stream);
+// dst [m][ld] = src [m][n], columns n..ld-1 zero
+hipError_t launch_pad_rows(const uint16_t* src, int64_t m, int64_t n, uint16_t* dst, int64_t ld,
+                           hipStream_t stream);
+
+}  // namespace opq

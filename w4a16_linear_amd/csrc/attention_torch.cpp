@@ -6,111 +6,22 @@
 // host time a call, of which the launches are 3, 3 and 6.
 //
 // Nothing here computes; every call ends in libopq (include/opq_attention.h).
-#include <ATen/MemoryOverlap.h>
-#include <ATen/core/Tensor.h>
-#include <ATen/core/grad_mode.h>
-#include <ATen/ops/empty.h>
-#include <c10/hip/HIPFunctions.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
 #include <cmath>
 #include <cstring>
 #include <vector>
 
 #include "opq_attention.h"
+#include "torch_common.hpp"
+
+namespace opq_torch {
+
+PyObject* g_error = nullptr;
+
+}  // namespace opq_torch
 
 namespace {
 
-using at::Tensor;
-
-PyObject* g_error = nullptr;  // opq.OpqError
-
-// The library launches on the current device: make it the tensors' one.
-struct OnDevice {
-  c10::DeviceIndex old, dev;
-  explicit OnDevice(const Tensor& t) : old(c10::hip::current_device()), dev(t.device().index()) {
-    if (old != dev) c10::hip::set_device(dev);
-  }
-  ~OnDevice() {
-    if (old != dev) c10::hip::set_device(old);
-  }
-  void* stream() const { return c10::hip::getCurrentHIPStream(dev).stream(); }
-};
-
-const Tensor& tensor_of(PyObject* o, const char* name) {
-  TORCH_CHECK_VALUE(THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda(), name,
-                    " must be a CUDA (HIP) tensor");
-  return THPVariable_Unpack(o);
-}
-
-// These calls compute outside autograd: a result that ought to carry a gradient would
-// come back without one, and nothing would say so.
-const Tensor& plain(const Tensor& t, const char* name) {
-  TORCH_CHECK(!(t.requires_grad() && at::GradMode::is_enabled()), name,
-              " requires grad, which this call does not follow (apply_rotary turns positions "
-              "under autograd): detach it, or call under torch.no_grad()");
-  return t;
-}
-// A tensor whose memory this call writes: autograd learns of it, as of every in-place
-// operation, should it have saved the old values.
-void written(const Tensor& t) {
-  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-}
-
-// A dense tensor of a known type and shape.
-void* dense(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape,
-            c10::Device dev) {
-  TORCH_CHECK_VALUE(t.scalar_type() == type, name, " must be ", type, ", got ", t.scalar_type());
-  TORCH_CHECK_VALUE(t.sizes() == shape && t.is_contiguous(), name,
-                    " must be contiguous with shape ", shape, ", got ", t.sizes());
-  TORCH_CHECK_VALUE(t.device() == dev, name, " must be on ", dev, ", got ", t.device());
-  return t.data_ptr();
-}
-void* dense(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape,
-            c10::Device dev) {
-  return dense(tensor_of(o, name), name, type, shape, dev);
-}
-
-// A tensor whose last dimension is dense; its other strides are free.
-const Tensor& rows(PyObject* o, const char* name, int64_t ndim) {
-  const Tensor& t = tensor_of(o, name);
-  TORCH_CHECK_VALUE(t.dim() == ndim && (t.size(-1) <= 1 || t.stride(-1) == 1), name, " must be ",
-                    ndim, "-d with a dense last dimension");
-  return plain(t, name);
-}
-
-int dtype_of(at::ScalarType t, const char* what) {
-  TORCH_CHECK_VALUE(t == at::kFloat || t == at::kBFloat16, what,
-                    " must be float32 or bfloat16, got ", t);
-  return t == at::kFloat ? OPQ_F32 : OPQ_BF16;
-}
-
-void check(const char* fn, int status) {
-  if (status == OPQ_OK) return;
-  PyObject* e = PyObject_CallFunction(g_error, "sis", fn, status, opq_status_str(status));
-  if (e) {
-    PyErr_SetObject(g_error, e);
-    Py_DECREF(e);
-  }
-  throw python_error();
-}
-
-int64_t int_of(PyObject* o) {
-  const int64_t v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw python_error();
-  return v;
-}
-double double_of(PyObject* o) {
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) throw python_error();
-  return v;
-}
-
-void arguments(Py_ssize_t n, Py_ssize_t want) {
-  TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n);
-}
+using namespace opq_torch;
 
 // ------------------------------------------------------------------ rotary
 
@@ -394,6 +305,8 @@ PyMethodDef kMethods[] = {{"rotary", FAST(rotary), METH_FASTCALL, nullptr},
                           {"cache_read", FAST(cache_read), METH_FASTCALL, nullptr},
                           {"cache_move", FAST(cache_move), METH_FASTCALL, nullptr},
                           {"attention", FAST(attention), METH_FASTCALL, nullptr},
+                          {"lowrank_add", FAST(lowrank_add), METH_FASTCALL, nullptr},
+                          {"lowrank_backward", FAST(lowrank_backward), METH_FASTCALL, nullptr},
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_attention", nullptr, -1, kMethods,
