@@ -4,7 +4,9 @@
  *   opq_rotary            rotary positions on queries and keys (and its backward pass);
  *   opq_cache_write/read  a paged key/value cache, quantized as it is written;
  *   opq_cache_attention   attention of one token, or of a tree of drafted
- *                         tokens, per sequence, straight from the cache's codes.
+ *                         tokens, per sequence, straight from the cache's codes;
+ *   opq_pages_*           the cache's pages forked, taken, freed, drawn together;
+ *   opq_verify_drafts     drafted tokens verified against the target's probabilities.
  *
  * The conventions of opq.h hold (status codes, order of the argument checks,
  * streams, nothing allocated or synchronised, nothing enqueued on an error),
@@ -236,6 +238,129 @@ int opq_cache_attention(const opq_cache* cache, const uint16_t* q, int64_t batch
                         const uint32_t* mask, int64_t mask_batch_stride, float scale,
                         uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                         void* stream);
+
+/* ------------------------------------------------------------------- pages */
+
+/*
+ * Pages of a cache, forked, taken, freed and drawn together.  A page table,
+ * int32 [rows][columns], names the pages that hold each row's tokens, in order; an
+ * entry outside 0..pages-1 (such as -1) names none.  A page that no entry of the
+ * table names is free: the table is all the state there is, and what is freed is freed by
+ * no longer naming it.  One table names the same pages in the caches of every layer.
+ *   table, lens, parents  device;  every output: device out, int32, dense
+ *   pages  1..2^20;  page  tokens of a page, a power of two, 16 or more;
+ *   rows * columns up to 2^28, rows up to 2^20
+ *   workspace  at least opq_pages_workspace_bytes(rows of the new table, pages)
+ *          bytes, no initialisation; calls that may overlap need their own
+ * Lengths are clamped to 0..columns * page.  Free pages are taken lowest first, so
+ * results are the same from call to call.  Errors of the three: OPQ_ERR_NULL,
+ * OPQ_ERR_SHAPE, OPQ_ERR_ALIGN, OPQ_ERR_WORKSPACE, OPQ_ERR_UNSUPPORTED, OPQ_ERR_HIP.
+ */
+size_t opq_pages_workspace_bytes(int64_t rows, int64_t pages);
+
+/*
+ * Rows resized: row i keeps the entries of its first lens[i] tokens (those of the rest
+ * become -1: their pages are freed unless other rows name them) and takes free
+ * pages, row by row, for the entries it lacks.
+ *   lens     [rows] int32, the tokens each row shall have room for
+ *   out      [rows][columns]; may be table
+ *   missing  [1]: entries left -1 because no page was free (all of them come after
+ *            those that got one)
+ */
+int opq_pages_resize(const int32_t* table, const int32_t* lens, int64_t rows, int64_t columns,
+                     int64_t pages, int64_t page, int32_t* out, int32_t* missing, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Rows forked, reordered, dropped: row i of the new table is a copy of row
+ * parents[i] as far as its lens[parents[i]] tokens go (beams after a step, samples of one
+ * prompt; a parent outside 0..rows-1: an empty row).  Rows share full pages.  A
+ * last page that is partly filled, so will be written on, stays with the
+ * first new row that ends in it, unless a row names it as a full page; every other row that
+ * ends in it gets a free page instead, and a pair for opq_cache_copy_pages (of each cache).
+ *   parents  [new_rows] int32
+ *   out      [new_rows][columns]; must not overlap table
+ *   out_lens [new_rows]: the rows' tokens
+ *   src, dst [new_rows]: page dst[i] is to become a copy of page src[i]; -1: none
+ *   missing  [1]: rows that lack their last page (-1) because none was free
+ */
+int opq_pages_fork(const int32_t* table, const int32_t* lens, int64_t rows, int64_t columns,
+                   const int32_t* parents, int64_t new_rows, int64_t pages, int64_t page,
+                   int32_t* out, int32_t* out_lens, int32_t* src, int32_t* dst, int32_t* missing,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Pages drawn together: with U pages in use, the k-th used page (by id) past the first U
+ * ids moves to the k-th free page of them.
+ *   out       [rows][columns], the table after the move; may be table
+ *   src, dst  [moves], moves = min(pages / 2, rows * columns): the pairs for
+ *             opq_cache_copy_pages, -1 behind the last
+ *   used      [1]: U
+ */
+int opq_pages_compact(const int32_t* table, int64_t rows, int64_t columns, int64_t pages,
+                      int32_t* out, int32_t* src, int32_t* dst, int32_t* used, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Whole pages copied, keys and values of every head, codes and scales as they are: page
+ * src[i] to page dst[i].  A pair with a page outside 0..pages-1 (such as -1) copies
+ * nothing.  No page may be a destination twice, or a source and a destination: what such
+ * a page holds afterwards is unspecified.
+ *   src, dst  device, [count] int32;  count up to 2^20
+ * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALPHA, OPQ_ERR_ALIGN, OPQ_ERR_DTYPE,
+ * OPQ_ERR_UNSUPPORTED, OPQ_ERR_HIP.
+ */
+int opq_cache_copy_pages(const opq_cache* cache, int64_t count, const int32_t* src,
+                         const int32_t* dst, void* stream);
+
+/* ------------------------------------------------------------------ drafts */
+
+/* Bytes of device workspace opq_verify_drafts needs. */
+size_t opq_verify_drafts_workspace_bytes(int64_t batch, int64_t vocab);
+
+/*
+ * Drafted tokens verified against the target model's probabilities, with given random
+ * numbers: the tokens that come out are distributed as the target's own.  Of a
+ * sequence's `draft` tokens the first is certain (the last one decided, whose
+ * row gives what follows it); the others hang under their parents.  From node 0 on, the
+ * node's children are tested in the order of their indexes; the first kept one is
+ * the next node.  With p the probabilities of the node, x the child's token, u its random
+ * number:
+ *   - with draft_probs (a chain drawn from a draft model, q the probabilities x was
+ *     drawn from): kept if u q(x) < p(x);
+ *   - without (a tree or chain of candidates): kept if u Z < p(x), Z = 1 less the
+ *     p of the node's children tested before; a sibling's token again counts p = 0.
+ * Nothing with p(x) = 0 is kept.  At the last node `next` is drawn with the
+ * first token's number u0 from weights w: p; max(p - q, 0) if a token drawn from q was
+ * refused; p without the tested children's tokens for candidates.  It is the
+ * lowest token i with w_i > 0 whose w_0 + ... + w_i exceeds u0 times the sum of all, the
+ * last with w_i > 0 if rounding leaves none, -1 if every weight is 0.
+ *   probs    device, [batch][draft][vocab] of dtype (OPQ_F32 or OPQ_BF16): row t
+ *            after token t
+ *   tokens   device, [batch][draft] int32; one outside 0..vocab-1 has p = 0
+ *   uniforms device, [batch][draft] float32 in [0, 1)
+ *   draft_probs  device, [batch][draft-1][vocab] of dtype, row t - 1 of token t; or NULL
+ *   parents  device, [batch][draft] int32 or NULL (a chain: t - 1), not both this
+ *            and draft_probs.  A token whose parent is not an earlier one is never kept
+ *   counts   device, [batch] int32 or NULL: how many of the draft count (0: the
+ *            sequence gets kept -1, count 0 and next -1)
+ *   kept     device out, [batch][draft] int32: indexes of the kept tokens in order, 0
+ *            first, then -1;  count, next  device out, [batch] int32
+ * Rows of probabilities have free strides (in elements, not negative; vocab is dense) and need
+ * only their element's alignment; the int32 and float32 arrays are dense and 4-byte
+ * aligned, the workspace 16-byte.  A probability that is negative, infinite or NaN counts
+ * as 0.  Products, Z and sums are in float64; sums in a fixed order.
+ * draft 1..1024, vocab 1..2^22, batch up to 65535 (OPQ_ERR_UNSUPPORTED past them, and for
+ * draft_probs with parents).
+ * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALIGN, OPQ_ERR_DTYPE,
+ * OPQ_ERR_WORKSPACE, OPQ_ERR_UNSUPPORTED, OPQ_ERR_HIP.
+ */
+int opq_verify_drafts(const void* probs, int dtype, int64_t batch, int64_t draft, int64_t vocab,
+                      int64_t batch_stride, int64_t token_stride, const int32_t* tokens,
+                      const float* uniforms, const void* draft_probs, int64_t q_batch_stride,
+                      int64_t q_token_stride, const int32_t* parents, const int32_t* counts,
+                      int32_t* kept, int32_t* count, int32_t* next, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -41,6 +41,14 @@ _SIGNATURES = {
     "opq_cache_write": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _L, _P, _P]),
     "opq_cache_read": (_I, [_P, _L, _P, _P, _P, _I, _P]),
     "opq_cache_move": (_I, [_P, _L, _L, _P, _P, _P]),
+    "opq_pages_workspace_bytes": (ctypes.c_size_t, [_L, _L]),
+    "opq_pages_resize": (_I, [_P, _P, _L, _L, _L, _L, _P, _P, _P, ctypes.c_size_t, _P]),
+    "opq_pages_fork": (_I, [_P, _P, _L, _L, _P, _L, _L, _L, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "opq_pages_compact": (_I, [_P, _L, _L, _L, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "opq_cache_copy_pages": (_I, [_P, _L, _P, _P, _P]),
+    "opq_verify_drafts_workspace_bytes": (ctypes.c_size_t, [_L, _L]),
+    "opq_verify_drafts": (_I, [_P, _I, _L, _L, _L, _L, _L, _P, _P, _P, _L, _L, _P, _P, _P, _P, _P, _P,
+                               ctypes.c_size_t, _P]),
     "opq_cache_attention_workspace_bytes": (ctypes.c_size_t, [_L, _L, _L, _L, _L, _L]),
     "opq_cache_attention": (_I, [_P, _P, _L, _L, _L, _L, _L, _L, _P, _L, _P, _P, _L, _P, _L, _F,
                                  _P, _P, _P, ctypes.c_size_t, _P]),
@@ -265,6 +273,65 @@ def cache_move(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor) -> None:
     to the slots right after the cached ones.  A sequence's rows are all read before
     any is written; sequences of one call must not share slots."""
     (_ext or _calls()).cache_move(cache, src, dst)
+
+
+# ------------------------------------------------------------------- pages
+
+def pages_fork(page_table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor, pages: int, page: int,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A new page table whose row i continues row parents[i] of page_table (int32 [rows,
+    columns]; lens: int32 [rows], its tokens; a parent that is no row: an empty row): beams
+    after a step, samples of one prompt, requests dropped (a page is free when no entry names it).
+    Full pages are shared; of the rows that end in one partly filled page the first keeps it and each
+    other gets a free page.  Returns (page_table, lens, src, dst, missing): src and dst, int32 [new
+    rows], are the pairs for cache_copy_pages (-1: none), missing, int32 [1], the rows whose last
+    entry is -1 because no page was free.  `out`: a table to write, not the one that is read."""
+    return (_ext or _calls()).pages_fork(page_table, lens, parents, pages, page, out, workspace)
+
+
+def pages_resize(page_table: torch.Tensor, lens: torch.Tensor, pages: int, page: int,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(page_table, missing): rows with entries for lens (int32 [rows]) tokens.  Entries past them
+    become -1, those that are lacking take the lowest free pages, row by row; missing, int32 [1],
+    counts the ones left -1 because no page was free.  `out` may be page_table."""
+    return (_ext or _calls()).pages_resize(page_table, lens, pages, page, out, workspace)
+
+
+def pages_compact(page_table: torch.Tensor, pages: int, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(page_table, src, dst, used): the table with its used pages (their number: `used`, int32 [1])
+    at the lowest ids, and the pairs for cache_copy_pages that take them there, in ascending order,
+    -1 behind the last (int32 [min(pages // 2, rows * columns)]).  `out` may be page_table."""
+    return (_ext or _calls()).pages_compact(page_table, pages, out, workspace)
+
+
+def cache_copy_pages(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copy whole pages src to dst (int32 [count]; a pair with -1 copies nothing), as they are
+    stored.  No page may be a destination twice, or a source and a destination."""
+    (_ext or _calls()).cache_copy_pages(cache, src, dst)
+
+
+# ------------------------------------------------------------------ drafts
+
+def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor,
+                  draft_probs: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                  counts: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Which drafted tokens the target model keeps, and the token after them: (kept, count,
+    next), int32 [batch, draft], [batch], [batch].  What comes out is distributed as the target's
+    own samples; `kept` is what OPQAttention.accept takes.
+
+    probs: the target's probabilities (float32 or bfloat16 [batch, draft, vocab]), row t after
+    drafted token t.  tokens: int32 [batch, draft]; the first is certain, the others hang under
+    `parents` (int32 [batch, draft]; without them a chain).  uniforms: float32 [batch, draft] in
+    [0, 1), number t tests token t, number 0 draws `next`.  draft_probs [batch, draft - 1, vocab]:
+    what a chain's tokens were drawn from (row t - 1 for token t); without them the drafted
+    tokens are candidates, chosen without chance.  counts: int32 [batch], drafted tokens that
+    count (0: kept -1, count 0, next -1).  The rules stand in include/opq_attention.h."""
+    return (_ext or _calls()).verify_drafts(probs, tokens, uniforms, draft_probs, parents, counts, workspace)
 
 
 # --------------------------------------------------------------- attention

@@ -27,6 +27,7 @@ CEILING_LIB = os.path.join(HERE, "libopq_ceiling.so")
 
 SOURCES = ["opq_api.cpp", "tables.cpp", "quantize.hip", "dequantize.hip", "linear.hip",
            "attention_api.cpp", "rotary.hip", "cache.hip", "attention.hip",
+           "pages.hip", "verify.hip",
            "adapters_api.cpp", "lowrank.hip", "linear_backward.hip"]
 CEILING_SOURCES = ["stream_ceiling.hip"]
 # the attention side's and the adapters' calls on torch tensors, a CPython extension over libopq.so

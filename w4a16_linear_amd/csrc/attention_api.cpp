@@ -241,6 +241,185 @@ int opq_cache_move(const opq_cache* cache, int64_t batch, int64_t count, const i
                                            static_cast<hipStream_t>(stream)));
 }
 
+int opq_cache_copy_pages(const opq_cache* cache, int64_t count, const int32_t* src,
+                         const int32_t* dst, void* stream) {
+  if (cache_null(cache) || (count > 0 && (!src || !dst))) return OPQ_ERR_NULL;
+  const opq_cache& c = *cache;
+  if (!cache_shape_ok(c) || count < 0) return OPQ_ERR_SHAPE;
+  if (!cache_alpha_ok(c)) return OPQ_ERR_ALPHA;
+  if (!cache_aligned(c) || !aligned4(src) || !aligned4(dst)) return OPQ_ERR_ALIGN;
+  if (!format_ok(c.format)) return OPQ_ERR_DTYPE;
+  if (!cache_supported(c) || count > opq::kMaxPages) return OPQ_ERR_UNSUPPORTED;
+  if (count == 0 || c.pages == 0) return OPQ_OK;
+  const bool signs = c.format == OPQ_CACHE_OPQ4;
+  const opq::CacheRows side[2] = {{nullptr, 0, 0, c.k, signs ? c.k_sign : nullptr, c.k_scale},
+                                  {nullptr, 0, 0, c.v, signs ? c.v_sign : nullptr, c.v_scale}};
+  return hip_status(opq::launch_cache_copy_pages(side, c, count, src, dst,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------------ pages
+
+constexpr int64_t kMaxPageRows = int64_t(1) << 20;
+constexpr int64_t kMaxEntries = int64_t(1) << 28;
+
+size_t opq_pages_workspace_bytes(int64_t rows, int64_t pages) {
+  if (rows < 0 || rows > kMaxPageRows || pages < 1 || pages > opq::kMaxPages) return 0;
+  return opq::pages_workspace_bytes(rows, pages);
+}
+
+// What the three calls check alike, once their pointers are known not to be NULL.
+static int pages_checks(int64_t rows, int64_t new_rows, int64_t columns, int64_t pages,
+                        const void* workspace, size_t workspace_bytes) {
+  const size_t need = opq_pages_workspace_bytes(new_rows, pages);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return OPQ_ERR_WORKSPACE;
+  if (rows > kMaxPageRows || new_rows > kMaxPageRows || pages > opq::kMaxPages ||
+      !product_within(rows, columns, 1, kMaxEntries) ||
+      !product_within(new_rows, columns, 1, kMaxEntries))
+    return OPQ_ERR_UNSUPPORTED;
+  return OPQ_OK;
+}
+
+int opq_pages_resize(const int32_t* table, const int32_t* lens, int64_t rows, int64_t columns,
+                     int64_t pages, int64_t page, int32_t* out, int32_t* missing, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!missing || (rows > 0 && !lens) || (rows > 0 && columns > 0 && (!table || !out)))
+    return OPQ_ERR_NULL;
+  if (rows < 0 || columns < 0 || pages < 1 || !page_ok(page)) return OPQ_ERR_SHAPE;
+  if (!aligned4(table) || !aligned4(lens) || !aligned4(out) || !aligned4(missing) ||
+      !aligned16(workspace))
+    return OPQ_ERR_ALIGN;
+  const int e = pages_checks(rows, rows, columns, pages, workspace, workspace_bytes);
+  if (e != OPQ_OK) return e;
+  if (page > kMaxInt) return OPQ_ERR_UNSUPPORTED;
+  opq::PagesArgs a{};
+  a.table = table;
+  a.lens = lens;
+  a.out = out;
+  a.result = missing;
+  a.rows = a.new_rows = (int)rows;
+  a.columns = (int)columns;
+  a.pages = (int)pages;
+  a.page = (int)page;
+  a.workspace = static_cast<char*>(workspace);
+  return hip_status(opq::launch_pages(opq::PagesCall::kResize, a, static_cast<hipStream_t>(stream)));
+}
+
+int opq_pages_fork(const int32_t* table, const int32_t* lens, int64_t rows, int64_t columns,
+                   const int32_t* parents, int64_t new_rows, int64_t pages, int64_t page,
+                   int32_t* out, int32_t* out_lens, int32_t* src, int32_t* dst, int32_t* missing,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!missing || (rows > 0 && !lens) || (rows > 0 && columns > 0 && !table) ||
+      (new_rows > 0 && (!parents || !out_lens || !src || !dst)) ||
+      (new_rows > 0 && columns > 0 && !out))
+    return OPQ_ERR_NULL;
+  if (rows < 0 || new_rows < 0 || columns < 0 || pages < 1 || !page_ok(page)) return OPQ_ERR_SHAPE;
+  if (!aligned4(table) || !aligned4(lens) || !aligned4(parents) || !aligned4(out) ||
+      !aligned4(out_lens) || !aligned4(src) || !aligned4(dst) || !aligned4(missing) ||
+      !aligned16(workspace))
+    return OPQ_ERR_ALIGN;
+  const int e = pages_checks(rows, new_rows, columns, pages, workspace, workspace_bytes);
+  if (e != OPQ_OK) return e;
+  if (page > kMaxInt) return OPQ_ERR_UNSUPPORTED;
+  opq::PagesArgs a{};
+  a.table = table;
+  a.lens = lens;
+  a.parents = parents;
+  a.out = out;
+  a.out_lens = out_lens;
+  a.src = src;
+  a.dst = dst;
+  a.result = missing;
+  a.rows = (int)rows;
+  a.new_rows = (int)new_rows;
+  a.columns = (int)columns;
+  a.pages = (int)pages;
+  a.page = (int)page;
+  a.workspace = static_cast<char*>(workspace);
+  return hip_status(opq::launch_pages(opq::PagesCall::kFork, a, static_cast<hipStream_t>(stream)));
+}
+
+int opq_pages_compact(const int32_t* table, int64_t rows, int64_t columns, int64_t pages,
+                      int32_t* out, int32_t* src, int32_t* dst, int32_t* used, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const bool some = rows > 0 && columns > 0;
+  if (!used || (some && (!table || !out)) || (some && pages > 1 && (!src || !dst)))
+    return OPQ_ERR_NULL;
+  if (rows < 0 || columns < 0 || pages < 1) return OPQ_ERR_SHAPE;
+  if (!aligned4(table) || !aligned4(out) || !aligned4(src) || !aligned4(dst) || !aligned4(used) ||
+      !aligned16(workspace))
+    return OPQ_ERR_ALIGN;
+  const int e = pages_checks(rows, rows, columns, pages, workspace, workspace_bytes);
+  if (e != OPQ_OK) return e;
+  opq::PagesArgs a{};
+  a.table = table;
+  a.out = out;
+  a.src = src;
+  a.dst = dst;
+  a.result = used;
+  a.rows = a.new_rows = (int)rows;
+  a.columns = (int)columns;
+  a.pages = (int)pages;
+  a.page = 16;  // lengths do not matter here
+  const int64_t entries = rows * columns;
+  a.moves = (int)(entries < pages / 2 ? entries : pages / 2);
+  a.workspace = static_cast<char*>(workspace);
+  return hip_status(opq::launch_pages(opq::PagesCall::kCompact, a, static_cast<hipStream_t>(stream)));
+}
+
+// ----------------------------------------------------------------------- drafts
+
+size_t opq_verify_drafts_workspace_bytes(int64_t batch, int64_t vocab) {
+  if (batch < 1 || batch > 65535 || vocab < 1 || vocab > (int64_t(1) << 22)) return 0;
+  return opq::verify_workspace_bytes(batch, vocab);
+}
+
+int opq_verify_drafts(const void* probs, int dtype, int64_t batch, int64_t draft, int64_t vocab,
+                      int64_t batch_stride, int64_t token_stride, const int32_t* tokens,
+                      const float* uniforms, const void* draft_probs, int64_t q_batch_stride,
+                      int64_t q_token_stride, const int32_t* parents, const int32_t* counts,
+                      int32_t* kept, int32_t* count, int32_t* next, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (batch > 0 && (!probs || !tokens || !uniforms || !kept || !count || !next)) return OPQ_ERR_NULL;
+  if (batch < 0 || draft < 1 || vocab < 1 || batch_stride < 0 || token_stride < 0 ||
+      (draft_probs && (q_batch_stride < 0 || q_token_stride < 0)))
+    return OPQ_ERR_SHAPE;
+  const uintptr_t element = dtype == OPQ_F32 ? 4 : 2;
+  if (!aligned(probs, element) || !aligned(draft_probs, element) || !aligned4(tokens) ||
+      !aligned4(uniforms) || !aligned4(parents) || !aligned4(counts) || !aligned4(kept) ||
+      !aligned4(count) || !aligned4(next) || !aligned16(workspace))
+    return OPQ_ERR_ALIGN;
+  if (!dtype_ok(dtype)) return OPQ_ERR_DTYPE;
+  const size_t need = opq_verify_drafts_workspace_bytes(batch, vocab);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return OPQ_ERR_WORKSPACE;
+  if (batch > 65535 || draft > 1024 || vocab > (int64_t(1) << 22) || (draft_probs && parents) ||
+      !product_within(batch, batch_stride, 1, kMaxElements) ||
+      !product_within(draft, token_stride, 1, kMaxElements) ||
+      (draft_probs && (!product_within(batch, q_batch_stride, 1, kMaxElements) ||
+                       !product_within(draft, q_token_stride, 1, kMaxElements))))
+    return OPQ_ERR_UNSUPPORTED;
+  if (batch == 0) return OPQ_OK;
+  opq::VerifyArgs a{};
+  a.p = probs;
+  a.q = draft_probs;
+  a.tokens = tokens;
+  a.uniforms = uniforms;
+  a.parents = parents;
+  a.counts = counts;
+  a.kept = kept;
+  a.count = count;
+  a.next = next;
+  a.p_batch = batch_stride;
+  a.p_token = token_stride;
+  a.q_batch = q_batch_stride;
+  a.q_token = q_token_stride;
+  a.batch = (int)batch;
+  a.draft = (int)draft;
+  a.vocab = (int)vocab;
+  a.workspace = workspace;
+  return hip_status(opq::launch_verify(a, dtype == OPQ_BF16, static_cast<hipStream_t>(stream)));
+}
+
 static bool attention_shape_ok(int64_t batch, int64_t draft, int64_t heads, int64_t kv_heads,
                                int64_t dim, int64_t max_len) {
   return batch >= 0 && draft >= 0 && heads > 0 && kv_heads > 0 && heads % kv_heads == 0 &&

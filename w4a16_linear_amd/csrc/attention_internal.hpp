@@ -64,6 +64,44 @@ constexpr int64_t kMaxMoves = 128;  // rows that opq_cache_move holds of a seque
 hipError_t launch_cache_move(const CacheRows (&side)[2], const opq_cache& c, int64_t batch,
                              int64_t count, const int32_t* src, const int32_t* dst,
                              hipStream_t stream);
+hipError_t launch_cache_copy_pages(const CacheRows (&side)[2], const opq_cache& c, int64_t count,
+                                   const int32_t* src, const int32_t* dst, hipStream_t stream);
+
+// pages.hip
+constexpr int64_t kMaxPages = int64_t(1) << 20;
+enum class PagesCall { kResize, kFork, kCompact };
+struct PagesArgs {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* parents;
+  int32_t* out;
+  int32_t* out_lens;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* result;  // missing, or used
+  int rows, new_rows, columns, pages, page, moves;
+  char* workspace;
+};
+size_t pages_workspace_bytes(int64_t rows, int64_t pages);
+hipError_t launch_pages(PagesCall call, const PagesArgs& a, hipStream_t stream);
+
+// verify.hip
+struct VerifyArgs {
+  const void* p;
+  const void* q;  // or nullptr
+  const int32_t* tokens;
+  const float* uniforms;
+  const int32_t* parents;  // or nullptr
+  const int32_t* counts;   // or nullptr
+  int32_t* kept;
+  int32_t* count;
+  int32_t* next;
+  int64_t p_batch, p_token, q_batch, q_token;
+  int batch, draft, vocab;
+  void* workspace;
+};
+size_t verify_workspace_bytes(int64_t batch, int64_t vocab);
+hipError_t launch_verify(const VerifyArgs& a, bool bf16, hipStream_t stream);
 
 // attention.hip
 struct AttentionPlan {

@@ -6,6 +6,7 @@
 // host time a call, of which the launches are 3, 3 and 6.
 //
 // Nothing here computes; every call ends in libopq (include/opq_attention.h).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <vector>
@@ -212,6 +213,205 @@ PyObject* cache_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// cache, src, dst
+PyObject* cache_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 3);
+  const Cache r = cache_of(a[0]);
+  const Tensor& src = tensor_of(a[1], "src");
+  TORCH_CHECK_VALUE(src.dim() == 1, "src must be [count]");
+  const int64_t count = src.size(0);
+  const void* ps = dense(src, "src", at::kInt, {count}, r.dev);
+  const void* pd = dense(a[2], "dst", at::kInt, {count}, r.dev);
+  const OnDevice on(src);
+  check("opq_cache_copy_pages",
+        opq_cache_copy_pages(&r.c, count, static_cast<const int32_t*>(ps),
+                             static_cast<const int32_t*>(pd), on.stream()));
+  cache_written(a[0]);
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------------- pages
+
+// The tuple of results: tensors made here, or (where given) objects passed in.
+template <size_t N>
+PyObject* tuple_of(Tensor (&t)[N], PyObject* const (&given)[N]) {
+  PyObject* all = PyTuple_New(N);
+  for (size_t i = 0; all && i < N; ++i) {
+    PyObject* o = given[i];
+    if (o) {
+      Py_INCREF(o);
+      written(t[i]);
+    } else {
+      o = THPVariable_Wrap(std::move(t[i]));
+    }
+    if (!o) Py_CLEAR(all);
+    else PyTuple_SET_ITEM(all, i, o);
+  }
+  return all;
+}
+
+const Tensor& page_table_of(PyObject* o) {
+  const Tensor& t = tensor_of(o, "page_table");
+  TORCH_CHECK_VALUE(t.dim() == 2, "page_table must be [rows, columns]");
+  dense(t, "page_table", at::kInt, t.sizes(), t.device());
+  return t;
+}
+
+int32_t* ints(const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+
+// Two dense tensors that share bytes.
+bool share(const Tensor& a, const Tensor& b) {
+  const char* pa = static_cast<const char*>(a.data_ptr());
+  const char* pb = static_cast<const char*>(b.data_ptr());
+  return a.nbytes() && b.nbytes() && pa < pb + b.nbytes() && pb < pa + a.nbytes();
+}
+
+// page_table, lens, pages, page, out or None, workspace or None -> (table, missing)
+PyObject* pages_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 6);
+  const Tensor& table = page_table_of(a[0]);
+  const int64_t rows = table.size(0), columns = table.size(1), pages = int_of(a[2]);
+  const Tensor& lens = tensor_of(a[1], "lens");
+  const void* pl = dense(lens, "lens", at::kInt, {rows}, table.device());
+  const OnDevice on(table);
+  Tensor t[2];
+  PyObject* given[2] = {nullptr, nullptr};
+  if (a[4] == Py_None) {
+    t[0] = at::empty(table.sizes(), table.options());
+  } else {
+    t[0] = tensor_of(given[0] = a[4], "out");
+    dense(t[0], "out", at::kInt, table.sizes(), table.device());
+    TORCH_CHECK_VALUE(t[0].data_ptr() == table.data_ptr() || !share(t[0], table),
+                      "out must be page_table itself or share no memory with it");
+    TORCH_CHECK_VALUE(!share(t[0], lens), "out must not share memory with lens");
+  }
+  t[1] = at::empty({1}, table.options());
+  size_t bytes = opq_pages_workspace_bytes(rows, pages);
+  const Tensor ws = workspace_of(a[5], &bytes, table);
+  check("opq_pages_resize",
+        opq_pages_resize(ints(table), static_cast<const int32_t*>(pl), rows, columns, pages,
+                         int_of(a[3]), ints(t[0]), ints(t[1]), ws.defined() ? ws.data_ptr() : nullptr,
+                         ws.defined() ? bytes : 0, on.stream()));
+  return tuple_of(t, given);
+  END_HANDLE_TH_ERRORS
+}
+
+// page_table, lens, parents, pages, page, out or None, workspace or None
+// -> (table, lens, src, dst, missing)
+PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 7);
+  const Tensor& table = page_table_of(a[0]);
+  const int64_t rows = table.size(0), columns = table.size(1), pages = int_of(a[3]);
+  const Tensor& lens = tensor_of(a[1], "lens");
+  const void* pl = dense(lens, "lens", at::kInt, {rows}, table.device());
+  const Tensor& parents = tensor_of(a[2], "parents");
+  TORCH_CHECK_VALUE(parents.dim() == 1, "parents must be [new rows]");
+  const int64_t made = parents.size(0);
+  const void* pp = dense(parents, "parents", at::kInt, {made}, table.device());
+  const OnDevice on(table);
+  Tensor t[5];
+  PyObject* given[5] = {};
+  if (a[5] == Py_None) {
+    t[0] = at::empty({made, columns}, table.options());
+  } else {
+    t[0] = tensor_of(given[0] = a[5], "out");
+    dense(t[0], "out", at::kInt, {made, columns}, table.device());
+    TORCH_CHECK_VALUE(!share(t[0], table) && !share(t[0], lens) && !share(t[0], parents),
+                      "out must not share memory with page_table, lens or parents: rows are copied from rows");
+  }
+  for (int i = 1; i < 4; ++i) t[i] = at::empty({made}, table.options());
+  t[4] = at::empty({1}, table.options());
+  size_t bytes = opq_pages_workspace_bytes(made, pages);
+  const Tensor ws = workspace_of(a[6], &bytes, table);
+  check("opq_pages_fork",
+        opq_pages_fork(ints(table), static_cast<const int32_t*>(pl), rows, columns,
+                       static_cast<const int32_t*>(pp), made, pages, int_of(a[4]), ints(t[0]),
+                       ints(t[1]), ints(t[2]), ints(t[3]), ints(t[4]),
+                       ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? bytes : 0, on.stream()));
+  return tuple_of(t, given);
+  END_HANDLE_TH_ERRORS
+}
+
+// page_table, pages, out or None, workspace or None -> (table, src, dst, used)
+PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 4);
+  const Tensor& table = page_table_of(a[0]);
+  const int64_t rows = table.size(0), columns = table.size(1), pages = int_of(a[1]);
+  const OnDevice on(table);
+  Tensor t[4];
+  PyObject* given[4] = {};
+  if (a[2] == Py_None) {
+    t[0] = at::empty(table.sizes(), table.options());
+  } else {
+    t[0] = tensor_of(given[0] = a[2], "out");
+    dense(t[0], "out", at::kInt, table.sizes(), table.device());
+    TORCH_CHECK_VALUE(t[0].data_ptr() == table.data_ptr() || !share(t[0], table),
+                      "out must be page_table itself or share no memory with it");
+  }
+  const int64_t moves = std::max<int64_t>(0, std::min(pages / 2, rows * columns));
+  t[1] = at::empty({moves}, table.options());
+  t[2] = at::empty({moves}, table.options());
+  t[3] = at::empty({1}, table.options());
+  size_t bytes = opq_pages_workspace_bytes(rows, pages);
+  const Tensor ws = workspace_of(a[3], &bytes, table);
+  check("opq_pages_compact",
+        opq_pages_compact(ints(table), rows, columns, pages, ints(t[0]), ints(t[1]), ints(t[2]),
+                          ints(t[3]), ws.defined() ? ws.data_ptr() : nullptr,
+                          ws.defined() ? bytes : 0, on.stream()));
+  return tuple_of(t, given);
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------------ drafts
+
+// probs, tokens, uniforms, draft_probs or None, parents or None, counts or None, workspace or None
+// -> (kept, count, next)
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 7);
+  const Tensor& p = rows(a[0], "probs", 3);
+  const int dtype = dtype_of(p.scalar_type(), "probs");
+  const int64_t batch = p.size(0), draft = p.size(1), vocab = p.size(2);
+  const c10::Device dev = p.device();
+  const void* tokens = dense(a[1], "tokens", at::kInt, {batch, draft}, dev);
+  const Tensor& u = plain(tensor_of(a[2], "uniforms"), "uniforms");
+  const void* uniforms = dense(u, "uniforms", at::kFloat, {batch, draft}, dev);
+  Tensor q;
+  if (a[3] != Py_None) {
+    q = rows(a[3], "draft_probs", 3);
+    TORCH_CHECK_VALUE(q.size(0) == batch && q.size(1) == draft - 1 && q.size(2) == vocab,
+                      "draft_probs must be [", batch, ", ", draft - 1, ", ", vocab, "], got ", q.sizes());
+    TORCH_CHECK_VALUE(q.scalar_type() == p.scalar_type(), "draft_probs must be ", p.scalar_type(), " as probs, got ",
+                      q.scalar_type());
+    TORCH_CHECK_VALUE(q.device() == dev, "draft_probs must be on ", dev, ", got ", q.device());
+    TORCH_CHECK_VALUE(a[4] == Py_None, "draft_probs go with a chain, not with parents");
+  }
+  const void* parents = a[4] == Py_None ? nullptr : dense(a[4], "parents", at::kInt, {batch, draft}, dev);
+  const void* counts = a[5] == Py_None ? nullptr : dense(a[5], "counts", at::kInt, {batch}, dev);
+  const OnDevice on(p);
+  const auto options = p.options().dtype(at::kInt);
+  Tensor t[3] = {at::empty({batch, draft}, options), at::empty({batch}, options), at::empty({batch}, options)};
+  size_t bytes = opq_verify_drafts_workspace_bytes(batch, vocab);
+  const Tensor ws = workspace_of(a[6], &bytes, p);
+  // a draft of one token has no draft probabilities to point to
+  const bool drawn = q.defined() && q.numel() > 0;
+  check("opq_verify_drafts",
+        opq_verify_drafts(p.data_ptr(), dtype, batch, draft, vocab, p.stride(0), p.stride(1),
+                          static_cast<const int32_t*>(tokens), static_cast<const float*>(uniforms),
+                          drawn ? q.data_ptr() : nullptr, drawn ? q.stride(0) : 0, drawn ? q.stride(1) : 0,
+                          static_cast<const int32_t*>(parents), static_cast<const int32_t*>(counts), ints(t[0]),
+                          ints(t[1]), ints(t[2]), ws.defined() ? ws.data_ptr() : nullptr,
+                          ws.defined() ? bytes : 0, on.stream()));
+  PyObject* none[3] = {};
+  return tuple_of(t, none);
+  END_HANDLE_TH_ERRORS
+}
+
 // --------------------------------------------------------------- attention
 
 // q, cache, page_table, lens, mask|None, counts|None, scale|None, max_len|None, out|None,
@@ -304,6 +504,11 @@ PyMethodDef kMethods[] = {{"rotary", FAST(rotary), METH_FASTCALL, nullptr},
                           {"cache_write", FAST(cache_write), METH_FASTCALL, nullptr},
                           {"cache_read", FAST(cache_read), METH_FASTCALL, nullptr},
                           {"cache_move", FAST(cache_move), METH_FASTCALL, nullptr},
+                          {"cache_copy_pages", FAST(cache_copy_pages), METH_FASTCALL, nullptr},
+                          {"pages_resize", FAST(pages_resize), METH_FASTCALL, nullptr},
+                          {"pages_fork", FAST(pages_fork), METH_FASTCALL, nullptr},
+                          {"pages_compact", FAST(pages_compact), METH_FASTCALL, nullptr},
+                          {"verify_drafts", FAST(verify_drafts), METH_FASTCALL, nullptr},
                           {"attention", FAST(attention), METH_FASTCALL, nullptr},
                           {"lowrank_add", FAST(lowrank_add), METH_FASTCALL, nullptr},
                           {"lowrank_backward", FAST(lowrank_backward), METH_FASTCALL, nullptr},

@@ -541,6 +541,76 @@ hipError_t launch_cache_move(const CacheRows (&side)[2], const opq_cache& c, int
   return hipGetLastError();
 }
 
+namespace {
+
+// One of the cache's arrays: what a page holds of it, in 16-byte units and in chunks.
+struct PageArray {
+  uint4* base;
+  int64_t units, chunks;
+};
+struct CopyArgs {
+  PageArray array[6];
+  const int32_t* src;
+  const int32_t* dst;
+  int64_t items, chunks;  // chunks of a page over all arrays; items: count times them
+  uint32_t pages;
+};
+constexpr int kCopyUnits = 4;  // 16-byte units of a thread: 16 KB a chunk
+
+// Pages copied: workgroups take chunks of 16 KB of the pairs in turn.  All units of a chunk
+// are requested before the first is stored.
+__global__ __launch_bounds__(kThreads) void copy_pages(CopyArgs a) {
+  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+    const int64_t pair = item / a.chunks;
+    const int32_t src = a.src[pair], dst = a.dst[pair];
+    if ((uint32_t)src >= a.pages || (uint32_t)dst >= a.pages || src == dst) continue;
+    int64_t chunk = item % a.chunks;
+    PageArray p = a.array[0];
+#pragma unroll
+    for (int i = 1; i < 6; ++i)
+      if (chunk >= p.chunks) {
+        chunk -= p.chunks;
+        p = a.array[i];
+      }
+    const uint4* from = p.base + src * p.units;
+    uint4* to = p.base + dst * p.units;
+    const int64_t at = chunk * (kThreads * kCopyUnits) + threadIdx.x;
+    uint4 v[kCopyUnits];
+#pragma unroll
+    for (int i = 0; i < kCopyUnits; ++i)
+      if (at + i * kThreads < p.units) v[i] = from[at + i * kThreads];
+#pragma unroll
+    for (int i = 0; i < kCopyUnits; ++i)
+      if (at + i * kThreads < p.units) to[at + i * kThreads] = v[i];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_cache_copy_pages(const CacheRows (&side)[2], const opq_cache& c, int64_t count,
+                                   const int32_t* src, const int32_t* dst, hipStream_t stream) {
+  const int64_t rows = c.heads * c.page;
+  const int64_t bytes = c.format == OPQ_CACHE_BF16 ? 2 * c.dim
+                        : c.format == OPQ_CACHE_FP8 ? c.dim : c.dim / 2;
+  CopyArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    void* const base[3] = {side[i].codes, side[i].sign, side[i].scale};
+    const int64_t units[3] = {rows * bytes / 16, side[i].sign ? rows * (c.dim / 32) / 4 : 0, rows / 4};
+    for (int j = 0; j < 3; ++j) {
+      const int64_t chunks = (units[j] + kThreads * kCopyUnits - 1) / (kThreads * kCopyUnits);
+      a.array[3 * i + j] = {static_cast<uint4*>(base[j]), units[j], chunks};
+      a.chunks += chunks;
+    }
+  }
+  a.src = src;
+  a.dst = dst;
+  a.items = count * a.chunks;
+  a.pages = (uint32_t)c.pages;
+  const int64_t blocks = a.items < 4096 ? a.items : 4096;
+  hipLaunchKernelGGL(copy_pages, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_cache_read(const CacheRows (&side)[2], const opq_cache& c, bool bf16,
                              int64_t tokens, const int32_t* slots, const LevelPlanes& lp,
                              hipStream_t stream) {

@@ -1,0 +1,338 @@
+// Pages of a cache forked, taken, freed and drawn together (include/opq_attention.h).
+//
+// The table is all the state: a page is free if no entry names it.  Each call goes
+// through four phases,
+//   clear  the bitmaps,
+//   mark   the pages that the new table keeps (a wave a row),
+//   plan   the rows' needs added up, the free pages listed (one workgroup),
+//   write  the new table,
+// as four kernels, or for small tables as one workgroup with barriers between.  What is
+// counted are places in a fixed order (rows, columns, page ids), so nothing depends on
+// the order of the atomics: they only set bits and take minima.
+#include <algorithm>
+
+#include "attention_internal.hpp"
+#include "device_common.hpp"
+
+namespace opq {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kRowThreads = 256;
+constexpr int kNoRow = 0x7FFFFFFF;
+// One workgroup: its bitmaps lie in LDS.
+constexpr int kOnePages = 16384;
+constexpr int64_t kOneEntries = 32768;
+
+struct Space {
+  uint32_t* named;  // [pages / 32] pages named in full (fork), or named at all
+  uint32_t* part;   // [pages / 32] fork: pages that rows end in, partly filled
+  int32_t* first;   // [pages] fork: the first row that ends in the page; compact: where it moves
+  int32_t* free;    // [pages] free pages in order, as many as are needed
+  int32_t* row;     // [rows] resize: entries lacking, then the row's first place in `free`;
+                    // fork: the page the row ends in, then its place in `free`; -1: none
+  int32_t* total;   // [2] pages needed, pages free
+};
+
+// Work spread over threads: this one's index and their number.
+struct Me {
+  int64_t thread, threads;
+  __device__ int lane() const { return threadIdx.x & (kWave - 1); }
+  __device__ int64_t wave() const { return thread / kWave; }
+  __device__ int64_t waves() const { return threads / kWave; }
+};
+
+__device__ __forceinline__ bool named(const PagesArgs& a, int id) { return id >= 0 && id < a.pages; }
+__device__ __forceinline__ void set_bit(uint32_t* bits, int id) {
+  const uint32_t bit = 1u << (id & 31);
+  // most rows name pages that others have set already; a stale word costs an atomic
+  if (!(__hip_atomic_load(bits + (id >> 5), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit))
+    atomicOr(bits + (id >> 5), bit);
+}
+__device__ __forceinline__ bool bit_of(const uint32_t* bits, int id) {
+  return __hip_atomic_load(bits + (id >> 5), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >> (id & 31) & 1u;
+}
+
+// Tokens of an old row (0 for none), and the entries they need.
+__device__ __forceinline__ int64_t tokens_of(const PagesArgs& a, int row) {
+  if (row < 0 || row >= a.rows) return 0;
+  return min((int64_t)max(a.lens[row], 0), (int64_t)a.columns * a.page);
+}
+__device__ __forceinline__ int entries_of(const PagesArgs& a, int64_t tokens) {
+  return (int)((tokens + a.page - 1) / a.page);
+}
+
+template <PagesCall CALL>
+__device__ void clear(const PagesArgs& a, const Space& s, Me me) {
+  const int words = (a.pages + 31) / 32;
+  for (int64_t i = me.thread; i < words; i += me.threads) {
+    s.named[i] = 0;
+    if (CALL == PagesCall::kFork) s.part[i] = 0;
+  }
+  if (CALL == PagesCall::kFork)
+    for (int64_t i = me.thread; i < a.pages; i += me.threads) s.first[i] = kNoRow;
+}
+
+template <PagesCall CALL>
+__device__ void mark(const PagesArgs& a, const Space& s, Me me) {
+  if constexpr (CALL == PagesCall::kCompact) {
+    const int64_t entries = (int64_t)a.rows * a.columns;
+    for (int64_t i = me.thread; i < entries; i += me.threads)
+      if (named(a, a.table[i])) set_bit(s.named, a.table[i]);
+    return;
+  }
+  for (int64_t row = me.wave(); row < a.new_rows; row += me.waves()) {
+    if constexpr (CALL == PagesCall::kResize) {
+      const int32_t* in = a.table + row * a.columns;
+      const int need = entries_of(a, tokens_of(a, (int)row));
+      int lack = 0;
+      for (int c0 = 0; c0 < need; c0 += kWave) {
+        const int c = c0 + me.lane();
+        const int id = c < need ? in[c] : 0;
+        if (c < need && named(a, id)) set_bit(s.named, id);
+        lack += __popcll(__ballot(c < need && !named(a, id)));
+      }
+      if (me.lane() == 0) s.row[row] = lack;
+    } else {
+      const int from = a.parents[row];
+      const int64_t tokens = tokens_of(a, from);
+      const int full = (int)(tokens / a.page);
+      const int32_t* in = a.table + (int64_t)(tokens ? from : 0) * a.columns;
+      for (int c = me.lane(); c < full; c += kWave)
+        if (named(a, in[c])) set_bit(s.named, in[c]);
+      if (me.lane() == 0) {
+        const int id = tokens % a.page ? in[full] : -1;
+        s.row[row] = named(a, id) ? id : -1;
+        if (named(a, id)) {
+          atomicMin(s.first + id, (int)row);
+          set_bit(s.part, id);
+        }
+      }
+    }
+  }
+}
+
+// This thread's value added over the threads before it (exclusive), and over all.
+__device__ __forceinline__ int scan(int v, int* s_sum, int* all) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  int up = v;
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int o = __shfl_up(up, off, kWave);
+    if (lane >= off) up += o;
+  }
+  __syncthreads();  // the sums of the last scan are read
+  if (lane == kWave - 1) s_sum[wave] = up;
+  __syncthreads();
+  int before = up - v, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / kWave; ++w) {
+    if (w < wave) before += s_sum[w];
+    total += s_sum[w];
+  }
+  *all = total;
+  return before;
+}
+
+// Pages of a word that the new table names, and those that exist.
+template <PagesCall CALL>
+__device__ __forceinline__ uint32_t named_word(const Space& s, int w) {
+  return s.named[w] | (CALL == PagesCall::kFork ? s.part[w] : 0u);
+}
+__device__ __forceinline__ uint32_t word_mask(int pages, int w) {
+  const int left = pages - w * 32;
+  return left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+}
+
+template <PagesCall CALL>
+__device__ void plan(const PagesArgs& a, const Space& s, int* s_sum) {
+  const int tid = threadIdx.x;
+  const int words = (a.pages + 31) / 32;
+  const int per = (words + kPlanThreads - 1) / kPlanThreads;
+  const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+  int all;
+  if constexpr (CALL == PagesCall::kCompact) {
+    int mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(s.named[w]);
+    scan(mine, s_sum, &all);
+    const int used = all;
+    int beyond = 0, holes = 0;
+    for (int w = w0; w < w1; ++w) {
+      const uint32_t low = word_mask(used, w), bits = s.named[w];  // ids below `used`
+      beyond += __popc(bits & ~low);
+      holes += __popc(~bits & low);
+    }
+    int moves;
+    int at = scan(beyond, s_sum, &moves);
+    for (int w = w0; w < w1; ++w)
+      for (uint32_t b = s.named[w] & ~word_mask(used, w); b; b &= b - 1) a.src[at++] = w * 32 + __ffs(b) - 1;
+    at = scan(holes, s_sum, &all);  // as many
+    for (int w = w0; w < w1; ++w)
+      for (uint32_t b = ~s.named[w] & word_mask(used, w); b; b &= b - 1) a.dst[at++] = w * 32 + __ffs(b) - 1;
+    __syncthreads();
+    for (int i = tid; i < a.moves; i += kPlanThreads) {
+      if (i < moves) s.first[a.src[i]] = a.dst[i];
+      else a.src[i] = a.dst[i] = -1;
+    }
+    if (tid == 0) s.total[0] = *a.result = used;
+    return;
+  }
+  int needed = 0;
+  for (int64_t r0 = 0; r0 < a.new_rows; r0 += kPlanThreads) {
+    const int64_t row = r0 + tid;
+    int v = row < a.new_rows ? s.row[row] : 0;
+    if constexpr (CALL == PagesCall::kFork) {
+      const int id = row < a.new_rows ? v : -1;
+      v = id >= 0 && (bit_of(s.named, id) ||
+                      __hip_atomic_load(s.first + id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != (int)row);
+    }
+    const int before = scan(v, s_sum, &all);
+    if (row < a.new_rows) s.row[row] = CALL == PagesCall::kFork && !v ? -1 : needed + before;
+    needed += all;
+  }
+  int mine = 0;
+  for (int w = w0; w < w1; ++w) mine += __popc(~named_word<CALL>(s, w) & word_mask(a.pages, w));
+  int at = scan(mine, s_sum, &all);
+  for (int w = w0; w < w1 && at < needed; ++w)
+    for (uint32_t b = ~named_word<CALL>(s, w) & word_mask(a.pages, w); b && at < needed; b &= b - 1)
+      s.free[at++] = w * 32 + __ffs(b) - 1;
+  if (tid == 0) {
+    s.total[0] = needed;
+    s.total[1] = all;
+    *a.result = max(0, needed - all);
+  }
+}
+
+template <PagesCall CALL>
+__device__ void write(const PagesArgs& a, const Space& s, Me me) {
+  if constexpr (CALL == PagesCall::kCompact) {
+    const int used = s.total[0];
+    const int64_t entries = (int64_t)a.rows * a.columns;
+    for (int64_t i = me.thread; i < entries; i += me.threads) {
+      const int id = a.table[i];
+      a.out[i] = !named(a, id) ? -1 : id < used ? id : s.first[id];
+    }
+    return;
+  }
+  const int free = s.total[1];
+  for (int64_t row = me.wave(); row < a.new_rows; row += me.waves()) {
+    int32_t* out = a.out + row * a.columns;
+    int at = s.row[row];
+    if constexpr (CALL == PagesCall::kResize) {
+      const int32_t* in = a.table + row * a.columns;
+      const int need = entries_of(a, tokens_of(a, (int)row));
+      for (int c0 = 0; c0 < a.columns; c0 += kWave) {
+        const int c = c0 + me.lane();
+        int id = c < need ? in[c] : -1;
+        const bool lacks = c < need && !named(a, id);
+        const uint64_t mask = __ballot(lacks);
+        const int k = at + __popcll(mask & ((uint64_t(1) << me.lane()) - 1));
+        if (lacks) id = k < free ? s.free[k] : -1;
+        if (c < a.columns) out[c] = id;
+        at += __popcll(mask);
+      }
+    } else {
+      const int from = a.parents[row];
+      const int64_t tokens = tokens_of(a, from);
+      const int need = entries_of(a, tokens);
+      const int32_t* in = a.table + (int64_t)(tokens ? from : 0) * a.columns;
+      const int fresh = at >= 0 && at < free ? s.free[at] : -1;
+      for (int c = me.lane(); c < a.columns; c += kWave) {
+        int id = c < need ? in[c] : -1;
+        if (!named(a, id)) id = -1;
+        if (c == need - 1 && at >= 0) id = fresh;
+        out[c] = id;
+      }
+      if (me.lane() == 0) {
+        a.src[row] = fresh >= 0 ? in[need - 1] : -1;
+        a.dst[row] = fresh;
+        a.out_lens[row] = (int)tokens;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ Me in_grid() {
+  return {(int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x};
+}
+
+template <PagesCall CALL>
+__global__ __launch_bounds__(kRowThreads) void pages_clear(PagesArgs a, Space s) {
+  clear<CALL>(a, s, in_grid());
+}
+template <PagesCall CALL>
+__global__ __launch_bounds__(kRowThreads) void pages_mark(PagesArgs a, Space s) {
+  mark<CALL>(a, s, in_grid());
+}
+template <PagesCall CALL>
+__global__ __launch_bounds__(kPlanThreads) void pages_plan(PagesArgs a, Space s) {
+  __shared__ int s_sum[kPlanThreads / kWave];
+  plan<CALL>(a, s, s_sum);
+}
+template <PagesCall CALL>
+__global__ __launch_bounds__(kRowThreads) void pages_write(PagesArgs a, Space s) {
+  write<CALL>(a, s, in_grid());
+}
+
+template <PagesCall CALL>
+__global__ __launch_bounds__(kPlanThreads) void pages_one(PagesArgs a, Space s) {
+  __shared__ uint32_t s_named[kOnePages / 32];
+  __shared__ uint32_t s_part[kOnePages / 32];
+  __shared__ int s_sum[kPlanThreads / kWave];
+  const Me me{(int64_t)threadIdx.x, kPlanThreads};
+  s.named = s_named;
+  s.part = s_part;
+  clear<CALL>(a, s, me);
+  __syncthreads();
+  mark<CALL>(a, s, me);
+  __syncthreads();
+  plan<CALL>(a, s, s_sum);
+  __syncthreads();
+  write<CALL>(a, s, me);
+}
+
+size_t up256(size_t b) { return (b + 255u) & ~size_t(255); }
+
+template <PagesCall CALL>
+hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
+  const int64_t entries = (int64_t)a.new_rows * a.columns;
+  if (a.pages <= kOnePages && entries <= kOneEntries) {
+    hipLaunchKernelGGL(pages_one<CALL>, dim3(1), dim3(kPlanThreads), 0, stream, a, s);
+    return hipGetLastError();
+  }
+  const auto blocks = [](int64_t threads) {
+    return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((threads + kRowThreads - 1) / kRowThreads, 2048)));
+  };
+  const dim3 rows = blocks(CALL == PagesCall::kCompact ? entries : (int64_t)a.new_rows * kWave);
+  hipLaunchKernelGGL(pages_clear<CALL>, blocks(CALL == PagesCall::kFork ? a.pages : (a.pages + 31) / 32),
+                     dim3(kRowThreads), 0, stream, a, s);
+  hipLaunchKernelGGL(pages_mark<CALL>, rows, dim3(kRowThreads), 0, stream, a, s);
+  hipLaunchKernelGGL(pages_plan<CALL>, dim3(1), dim3(kPlanThreads), 0, stream, a, s);
+  hipLaunchKernelGGL(pages_write<CALL>, rows, dim3(kRowThreads), 0, stream, a, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t pages_workspace_bytes(int64_t rows, int64_t pages) {
+  const size_t words = (size_t)(pages + 31) / 32 * 4, ids = (size_t)pages * 4;
+  return 2 * up256(words) + 2 * up256(ids) + up256((size_t)rows * 4) + 256;
+}
+
+hipError_t launch_pages(PagesCall call, const PagesArgs& a, hipStream_t stream) {
+  const size_t words = up256((size_t)(a.pages + 31) / 32 * 4), ids = up256((size_t)a.pages * 4);
+  char* w = a.workspace;
+  Space s;
+  s.total = reinterpret_cast<int32_t*>(w);
+  s.named = reinterpret_cast<uint32_t*>(w + 256);
+  s.part = reinterpret_cast<uint32_t*>(w + 256 + words);
+  s.first = reinterpret_cast<int32_t*>(w + 256 + 2 * words);
+  s.free = reinterpret_cast<int32_t*>(w + 256 + 2 * words + ids);
+  s.row = reinterpret_cast<int32_t*>(w + 256 + 2 * words + 2 * ids);
+  switch (call) {
+    case PagesCall::kResize: return launch<PagesCall::kResize>(a, s, stream);
+    case PagesCall::kFork: return launch<PagesCall::kFork>(a, s, stream);
+    default: return launch<PagesCall::kCompact>(a, s, stream);
+  }
+}
+
+}  // namespace opq
