@@ -546,42 +546,49 @@ namespace {
 // One of the cache's arrays: what a page holds of it, in 16-byte units and in chunks.
 struct PageArray {
   uint4* base;
-  int64_t units, chunks;
+  int64_t units;
+  int chunks;
 };
 struct CopyArgs {
   PageArray array[6];
   const int32_t* src;
   const int32_t* dst;
-  int64_t items, chunks;  // chunks of a page over all arrays; items: count times them
+  int count, chunks;  // pairs; chunks of a page over all arrays
   uint32_t pages;
 };
-constexpr int kCopyUnits = 4;  // 16-byte units of a thread: 16 KB a chunk
+constexpr int kCopyUnits = 4;  // 16-byte units of a lane: 4 KB a chunk
 
-// Pages copied: workgroups take chunks of 16 KB of the pairs in turn.  All units of a chunk
-// are requested before the first is stored.
+// Pages copied: a wave a chunk of a pair (4 KB, so that small pages fill waves too), all its
+// loads out before the first store.  (The units are held in variables of their own: an
+// array of them filled under conditions became LDS, and finding its place in it a read of the
+// dispatch packet in host memory: 12 us a launch.)
 __global__ __launch_bounds__(kThreads) void copy_pages(CopyArgs a) {
-  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int64_t pair = item / a.chunks;
+  int chunk = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave);
+  if (chunk >= a.chunks) return;
+  uint4* base = a.array[0].base;
+  int64_t units = a.array[0].units;
+  int held = a.array[0].chunks;
+#pragma unroll
+  for (int i = 1; i < 6; ++i)
+    if (chunk >= held) {
+      chunk -= held;
+      base = a.array[i].base;
+      units = a.array[i].units;
+      held = a.array[i].chunks;
+    }
+  const int64_t last = units - 1;
+  const int64_t at = (int64_t)chunk * (kWave * kCopyUnits) + (threadIdx.x & (kWave - 1));
+  for (int pair = blockIdx.y; pair < a.count; pair += gridDim.y) {
     const int32_t src = a.src[pair], dst = a.dst[pair];
     if ((uint32_t)src >= a.pages || (uint32_t)dst >= a.pages || src == dst) continue;
-    int64_t chunk = item % a.chunks;
-    PageArray p = a.array[0];
-#pragma unroll
-    for (int i = 1; i < 6; ++i)
-      if (chunk >= p.chunks) {
-        chunk -= p.chunks;
-        p = a.array[i];
-      }
-    const uint4* from = p.base + src * p.units;
-    uint4* to = p.base + dst * p.units;
-    const int64_t at = chunk * (kThreads * kCopyUnits) + threadIdx.x;
-    uint4 v[kCopyUnits];
-#pragma unroll
-    for (int i = 0; i < kCopyUnits; ++i)
-      if (at + i * kThreads < p.units) v[i] = from[at + i * kThreads];
-#pragma unroll
-    for (int i = 0; i < kCopyUnits; ++i)
-      if (at + i * kThreads < p.units) to[at + i * kThreads] = v[i];
+    const uint4* from = base + src * units;
+    uint4* to = base + dst * units;
+    const uint4 v0 = from[min(at, last)], v1 = from[min(at + kWave, last)];
+    const uint4 v2 = from[min(at + 2 * kWave, last)], v3 = from[min(at + 3 * kWave, last)];
+    if (at <= last) to[at] = v0;
+    if (at + kWave <= last) to[at + kWave] = v1;
+    if (at + 2 * kWave <= last) to[at + 2 * kWave] = v2;
+    if (at + 3 * kWave <= last) to[at + 3 * kWave] = v3;
   }
 }
 
@@ -597,17 +604,17 @@ hipError_t launch_cache_copy_pages(const CacheRows (&side)[2], const opq_cache& 
     void* const base[3] = {side[i].codes, side[i].sign, side[i].scale};
     const int64_t units[3] = {rows * bytes / 16, side[i].sign ? rows * (c.dim / 32) / 4 : 0, rows / 4};
     for (int j = 0; j < 3; ++j) {
-      const int64_t chunks = (units[j] + kThreads * kCopyUnits - 1) / (kThreads * kCopyUnits);
+      const int chunks = (int)((units[j] + kWave * kCopyUnits - 1) / (kWave * kCopyUnits));
       a.array[3 * i + j] = {static_cast<uint4*>(base[j]), units[j], chunks};
       a.chunks += chunks;
     }
   }
   a.src = src;
   a.dst = dst;
-  a.items = count * a.chunks;
+  a.count = (int)count;
   a.pages = (uint32_t)c.pages;
-  const int64_t blocks = a.items < 4096 ? a.items : 4096;
-  hipLaunchKernelGGL(copy_pages, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+  const unsigned x = (unsigned)((a.chunks + kThreads / kWave - 1) / (kThreads / kWave));
+  hipLaunchKernelGGL(copy_pages, dim3(x, (unsigned)(count < 4096 ? count : 4096)), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

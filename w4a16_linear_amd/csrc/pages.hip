@@ -2,13 +2,15 @@
 //
 // The table is all the state: a page is free if no entry names it.  Each call goes
 // through four phases,
-//   clear  the bitmaps,
+//   clear  a byte a page,
 //   mark   the pages that the new table keeps (a wave a row),
 //   plan   the rows' needs added up, the free pages listed (one workgroup),
 //   write  the new table,
 // as four kernels, or for small tables as one workgroup with barriers between.  What is
 // counted are places in a fixed order (rows, columns, page ids), so nothing depends on
-// the order of the atomics: they only set bits and take minima.
+// who comes first: marks are stores of one value, and the one atomic takes a minimum.
+// (Bits set by atomics took 115 us for the 1024 x 300 entries of rows that share
+// prompts, where bytes take 5: the atomics of different XCDs on one word meet in memory.)
 #include <algorithm>
 
 #include "attention_internal.hpp"
@@ -20,13 +22,14 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 constexpr int kNoRow = 0x7FFFFFFF;
-// One workgroup: its bitmaps lie in LDS.
+// One workgroup: its bytes lie in LDS.
 constexpr int kOnePages = 16384;
 constexpr int64_t kOneEntries = 32768;
 
 struct Space {
-  uint32_t* named;  // [pages / 32] pages named in full (fork), or named at all
-  uint32_t* part;   // [pages / 32] fork: pages that rows end in, partly filled
+  uint8_t* named;   // [words * 32] 1: pages named in full (fork), or named at all
+  uint8_t* part;    // [words * 32] 1: fork: pages that rows end in, partly filled
+  uint32_t* words;  // [words] the pages in use, a bit each
   int32_t* first;   // [pages] fork: the first row that ends in the page; compact: where it moves
   int32_t* free;    // [pages] free pages in order, as many as are needed
   int32_t* row;     // [rows] resize: entries lacking, then the row's first place in `free`;
@@ -43,16 +46,6 @@ struct Me {
 };
 
 __device__ __forceinline__ bool named(const PagesArgs& a, int id) { return id >= 0 && id < a.pages; }
-__device__ __forceinline__ void set_bit(uint32_t* bits, int id) {
-  const uint32_t bit = 1u << (id & 31);
-  // most rows name pages that others have set already; a stale word costs an atomic
-  if (!(__hip_atomic_load(bits + (id >> 5), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit))
-    atomicOr(bits + (id >> 5), bit);
-}
-__device__ __forceinline__ bool bit_of(const uint32_t* bits, int id) {
-  return __hip_atomic_load(bits + (id >> 5), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >> (id & 31) & 1u;
-}
-
 // Tokens of an old row (0 for none), and the entries they need.
 __device__ __forceinline__ int64_t tokens_of(const PagesArgs& a, int row) {
   if (row < 0 || row >= a.rows) return 0;
@@ -65,9 +58,9 @@ __device__ __forceinline__ int entries_of(const PagesArgs& a, int64_t tokens) {
 template <PagesCall CALL>
 __device__ void clear(const PagesArgs& a, const Space& s, Me me) {
   const int words = (a.pages + 31) / 32;
-  for (int64_t i = me.thread; i < words; i += me.threads) {
-    s.named[i] = 0;
-    if (CALL == PagesCall::kFork) s.part[i] = 0;
+  for (int64_t i = me.thread; i < 2 * words; i += me.threads) {
+    reinterpret_cast<uint4*>(s.named)[i] = make_uint4(0, 0, 0, 0);
+    if (CALL == PagesCall::kFork) reinterpret_cast<uint4*>(s.part)[i] = make_uint4(0, 0, 0, 0);
   }
   if (CALL == PagesCall::kFork)
     for (int64_t i = me.thread; i < a.pages; i += me.threads) s.first[i] = kNoRow;
@@ -78,7 +71,7 @@ __device__ void mark(const PagesArgs& a, const Space& s, Me me) {
   if constexpr (CALL == PagesCall::kCompact) {
     const int64_t entries = (int64_t)a.rows * a.columns;
     for (int64_t i = me.thread; i < entries; i += me.threads)
-      if (named(a, a.table[i])) set_bit(s.named, a.table[i]);
+      if (named(a, a.table[i])) s.named[a.table[i]] = 1;
     return;
   }
   for (int64_t row = me.wave(); row < a.new_rows; row += me.waves()) {
@@ -89,7 +82,7 @@ __device__ void mark(const PagesArgs& a, const Space& s, Me me) {
       for (int c0 = 0; c0 < need; c0 += kWave) {
         const int c = c0 + me.lane();
         const int id = c < need ? in[c] : 0;
-        if (c < need && named(a, id)) set_bit(s.named, id);
+        if (c < need && named(a, id)) s.named[id] = 1;
         lack += __popcll(__ballot(c < need && !named(a, id)));
       }
       if (me.lane() == 0) s.row[row] = lack;
@@ -99,13 +92,13 @@ __device__ void mark(const PagesArgs& a, const Space& s, Me me) {
       const int full = (int)(tokens / a.page);
       const int32_t* in = a.table + (int64_t)(tokens ? from : 0) * a.columns;
       for (int c = me.lane(); c < full; c += kWave)
-        if (named(a, in[c])) set_bit(s.named, in[c]);
+        if (named(a, in[c])) s.named[in[c]] = 1;
       if (me.lane() == 0) {
         const int id = tokens % a.page ? in[full] : -1;
         s.row[row] = named(a, id) ? id : -1;
         if (named(a, id)) {
           atomicMin(s.first + id, (int)row);
-          set_bit(s.part, id);
+          s.part[id] = 1;
         }
       }
     }
@@ -133,11 +126,18 @@ __device__ __forceinline__ int scan(int v, int* s_sum, int* all) {
   return before;
 }
 
-// Pages of a word that the new table names, and those that exist.
-template <PagesCall CALL>
-__device__ __forceinline__ uint32_t named_word(const Space& s, int w) {
-  return s.named[w] | (CALL == PagesCall::kFork ? s.part[w] : 0u);
+// The bits of 32 bytes that are 0 or 1.
+__device__ __forceinline__ uint32_t bits_of(const uint8_t* bytes) {
+  const uint4* v = reinterpret_cast<const uint4*>(bytes);
+  const uint4 a = v[0], b = v[1];
+  const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    bits |= ((x[i] & 1u) | (x[i] >> 7 & 2u) | (x[i] >> 14 & 4u) | (x[i] >> 21 & 8u)) << (4 * i);
+  return bits;
 }
+// Of the ids of word w those below `pages`.
 __device__ __forceinline__ uint32_t word_mask(int pages, int w) {
   const int left = pages - w * 32;
   return left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
@@ -149,25 +149,29 @@ __device__ void plan(const PagesArgs& a, const Space& s, int* s_sum) {
   const int words = (a.pages + 31) / 32;
   const int per = (words + kPlanThreads - 1) / kPlanThreads;
   const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
-  int all;
+  int all, mine = 0;  // words w0 .. w1 - 1 are this thread's alone
+  for (int w = w0; w < w1; ++w) {
+    uint32_t bits = bits_of(s.named + w * 32);
+    if (CALL == PagesCall::kFork) bits |= bits_of(s.part + w * 32);
+    s.words[w] = bits;
+    mine += __popc(bits);
+  }
   if constexpr (CALL == PagesCall::kCompact) {
-    int mine = 0;
-    for (int w = w0; w < w1; ++w) mine += __popc(s.named[w]);
     scan(mine, s_sum, &all);
     const int used = all;
     int beyond = 0, holes = 0;
     for (int w = w0; w < w1; ++w) {
-      const uint32_t low = word_mask(used, w), bits = s.named[w];  // ids below `used`
+      const uint32_t low = word_mask(used, w), bits = s.words[w];  // ids below `used`
       beyond += __popc(bits & ~low);
       holes += __popc(~bits & low);
     }
     int moves;
     int at = scan(beyond, s_sum, &moves);
     for (int w = w0; w < w1; ++w)
-      for (uint32_t b = s.named[w] & ~word_mask(used, w); b; b &= b - 1) a.src[at++] = w * 32 + __ffs(b) - 1;
+      for (uint32_t b = s.words[w] & ~word_mask(used, w); b; b &= b - 1) a.src[at++] = w * 32 + __ffs(b) - 1;
     at = scan(holes, s_sum, &all);  // as many
     for (int w = w0; w < w1; ++w)
-      for (uint32_t b = ~s.named[w] & word_mask(used, w); b; b &= b - 1) a.dst[at++] = w * 32 + __ffs(b) - 1;
+      for (uint32_t b = ~s.words[w] & word_mask(used, w); b; b &= b - 1) a.dst[at++] = w * 32 + __ffs(b) - 1;
     __syncthreads();
     for (int i = tid; i < a.moves; i += kPlanThreads) {
       if (i < moves) s.first[a.src[i]] = a.dst[i];
@@ -182,18 +186,17 @@ __device__ void plan(const PagesArgs& a, const Space& s, int* s_sum) {
     int v = row < a.new_rows ? s.row[row] : 0;
     if constexpr (CALL == PagesCall::kFork) {
       const int id = row < a.new_rows ? v : -1;
-      v = id >= 0 && (bit_of(s.named, id) ||
+      v = id >= 0 && (s.named[id] ||
                       __hip_atomic_load(s.first + id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != (int)row);
     }
     const int before = scan(v, s_sum, &all);
     if (row < a.new_rows) s.row[row] = CALL == PagesCall::kFork && !v ? -1 : needed + before;
     needed += all;
   }
-  int mine = 0;
-  for (int w = w0; w < w1; ++w) mine += __popc(~named_word<CALL>(s, w) & word_mask(a.pages, w));
-  int at = scan(mine, s_sum, &all);
+  const int ids = max(0, min(a.pages, w1 * 32) - w0 * 32);
+  int at = scan(ids - mine, s_sum, &all);
   for (int w = w0; w < w1 && at < needed; ++w)
-    for (uint32_t b = ~named_word<CALL>(s, w) & word_mask(a.pages, w); b && at < needed; b &= b - 1)
+    for (uint32_t b = ~s.words[w] & word_mask(a.pages, w); b && at < needed; b &= b - 1)
       s.free[at++] = w * 32 + __ffs(b) - 1;
   if (tid == 0) {
     s.total[0] = needed;
@@ -275,8 +278,8 @@ __global__ __launch_bounds__(kRowThreads) void pages_write(PagesArgs a, Space s)
 
 template <PagesCall CALL>
 __global__ __launch_bounds__(kPlanThreads) void pages_one(PagesArgs a, Space s) {
-  __shared__ uint32_t s_named[kOnePages / 32];
-  __shared__ uint32_t s_part[kOnePages / 32];
+  __shared__ __attribute__((aligned(16))) uint8_t s_named[kOnePages];
+  __shared__ __attribute__((aligned(16))) uint8_t s_part[CALL == PagesCall::kFork ? kOnePages : 16];
   __shared__ int s_sum[kPlanThreads / kWave];
   const Me me{(int64_t)threadIdx.x, kPlanThreads};
   s.named = s_named;
@@ -303,7 +306,7 @@ hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
     return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((threads + kRowThreads - 1) / kRowThreads, 2048)));
   };
   const dim3 rows = blocks(CALL == PagesCall::kCompact ? entries : (int64_t)a.new_rows * kWave);
-  hipLaunchKernelGGL(pages_clear<CALL>, blocks(CALL == PagesCall::kFork ? a.pages : (a.pages + 31) / 32),
+  hipLaunchKernelGGL(pages_clear<CALL>, blocks(CALL == PagesCall::kFork ? a.pages : (a.pages + 15) / 16),
                      dim3(kRowThreads), 0, stream, a, s);
   hipLaunchKernelGGL(pages_mark<CALL>, rows, dim3(kRowThreads), 0, stream, a, s);
   hipLaunchKernelGGL(pages_plan<CALL>, dim3(1), dim3(kPlanThreads), 0, stream, a, s);
@@ -314,20 +317,26 @@ hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
 }  // namespace
 
 size_t pages_workspace_bytes(int64_t rows, int64_t pages) {
-  const size_t words = (size_t)(pages + 31) / 32 * 4, ids = (size_t)pages * 4;
-  return 2 * up256(words) + 2 * up256(ids) + up256((size_t)rows * 4) + 256;
+  const size_t words = (size_t)(pages + 31) / 32, ids = (size_t)pages * 4;
+  return 2 * up256(words * 32) + up256(words * 4) + 2 * up256(ids) + up256((size_t)rows * 4) + 256;
 }
 
 hipError_t launch_pages(PagesCall call, const PagesArgs& a, hipStream_t stream) {
-  const size_t words = up256((size_t)(a.pages + 31) / 32 * 4), ids = up256((size_t)a.pages * 4);
+  const size_t words = (size_t)(a.pages + 31) / 32;
   char* w = a.workspace;
+  auto take = [&](size_t bytes) {
+    char* here = w;
+    w += up256(bytes);
+    return here;
+  };
   Space s;
-  s.total = reinterpret_cast<int32_t*>(w);
-  s.named = reinterpret_cast<uint32_t*>(w + 256);
-  s.part = reinterpret_cast<uint32_t*>(w + 256 + words);
-  s.first = reinterpret_cast<int32_t*>(w + 256 + 2 * words);
-  s.free = reinterpret_cast<int32_t*>(w + 256 + 2 * words + ids);
-  s.row = reinterpret_cast<int32_t*>(w + 256 + 2 * words + 2 * ids);
+  s.total = reinterpret_cast<int32_t*>(take(8));
+  s.named = reinterpret_cast<uint8_t*>(take(words * 32));
+  s.part = reinterpret_cast<uint8_t*>(take(words * 32));
+  s.words = reinterpret_cast<uint32_t*>(take(words * 4));
+  s.first = reinterpret_cast<int32_t*>(take((size_t)a.pages * 4));
+  s.free = reinterpret_cast<int32_t*>(take((size_t)a.pages * 4));
+  s.row = reinterpret_cast<int32_t*>(take((size_t)a.new_rows * 4));
   switch (call) {
     case PagesCall::kResize: return launch<PagesCall::kResize>(a, s, stream);
     case PagesCall::kFork: return launch<PagesCall::kFork>(a, s, stream);

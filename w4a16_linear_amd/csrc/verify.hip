@@ -226,6 +226,15 @@ __device__ __forceinline__ double scan(double v, double* s_sum, double* all) {
   return before + v;
 }
 
+// The lowest `first` and the highest `last` of the workgroup: a wave's lowest is that of its
+// lowest lane that has one, so one lane a wave goes to LDS.
+__device__ __forceinline__ void note(int first, int last, int* s_first, int* s_last) {
+  const uint64_t some = __ballot(last >= 0), past = __ballot(first != 0x7FFFFFFF);
+  const int lane = threadIdx.x & (kWave - 1);
+  if (past && lane == __ffsll((unsigned long long)past) - 1) atomicMin(s_first, first);
+  if (some && lane == 63 - __clzll((long long)some)) atomicMax(s_last, last);
+}
+
 // Workgroup = sequence: the piece, then the token.
 template <typename T, int PIECE>
 __global__ __launch_bounds__(kThreads) void verify_draw(VerifyArgs a, const double* sums, const Found* founds,
@@ -251,14 +260,16 @@ __global__ __launch_bounds__(kThreads) void verify_draw(VerifyArgs a, const doub
   const double aim = (double)a.uniforms[(int64_t)b * a.draft] * all;
   {
     double at = to - mine;
+    int first = 0x7FFFFFFF, last = -1;
     for (int i = tid * per; i < min(pieces, (tid + 1) * per); ++i) {
       const double s = sums[(int64_t)b * pieces + i];
       if (s > 0.0) {
-        atomicMax(&s_last, i);
-        if (at + s > aim) atomicMin(&s_first, i);
+        last = i;
+        if (at + s > aim) first = min(first, i);
       }
       at += s;
     }
+    note(first, last, &s_first, &s_last);
   }
   __syncthreads();
   if (s_last < 0) {  // nothing to draw from
@@ -295,17 +306,16 @@ __global__ __launch_bounds__(kThreads) void verify_draw(VerifyArgs a, const doub
     for (int e = 0; e < 4; ++e) own += w[i + e] = four[e];
   }
   double at = s_before + (scan(own, s_sum, &all) - own);
+  int first = 0x7FFFFFFF, last = -1;
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     at += w[i];
     if (w[i] > 0.0) {
-      atomicMax(&s_last, v0 + tid * kRun + i);
-      if (at > aim) {
-        atomicMin(&s_first, v0 + tid * kRun + i);
-        break;
-      }
+      last = v0 + tid * kRun + i;
+      if (at > aim) first = min(first, last);
     }
   }
+  note(first, last, &s_first, &s_last);
   __syncthreads();
   if (tid == 0) a.next[b] = min(s_first, s_last);
 }
