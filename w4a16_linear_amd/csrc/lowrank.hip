@@ -19,11 +19,11 @@
 // of 16 bytes) and v_perm pairs rows, 32 of them for the eight operands of the
 // eight columns; nothing goes through LDS.
 //
-// Tokens are grouped by adapter where they are used.  Forward, each workgroup
-// sorts the (up to 256) tokens of its block in LDS, stably, into tiles of equal
-// adapters; a call needs no plan and no launch for it.  A tile's columns are
-// independent in the matrix product, so what is in another token's row never
-// reaches a token.
+// Tokens are grouped by adapter where they are used: each wave looks at the 64
+// tokens of its block, one a lane, and finds tiles of equal adapters with ballots, in
+// registers; a forward call needs no plan, no launch and no barrier for it.  A tile's
+// columns are independent in the matrix product, so what is in another token's row
+// never reaches a token.
 //
 // Rounding: c is float32.  Entering a second product it is cut into bfloat16
 // parts: two (16 bits) where the result is bfloat16 itself, three (24 bits, all
@@ -39,74 +39,61 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kBlockTokens = 256;  // tokens a workgroup sorts: one a thread
-constexpr int kNone = 0x7FFFFFFE;  // sorts behind every adapter
+constexpr int kBlockTokens = kWave;  // tokens a wave groups: one a lane
+constexpr int kNoAdapter = -1, kNoToken = -2;
 
 // -------------------------------------------------------------- token tiles
 
-// The block's tokens in the order of their adapters, cut into tiles of at most
-// TILE tokens of one adapter.
+// The adapter of the block's token `lane`.
+__device__ __forceinline__ int block_id(const int32_t* index, int cnt, int64_t adapters) {
+  const int lane = threadIdx.x & (kWave - 1);
+  if (lane >= cnt) return kNoToken;
+  const int id = index[lane];
+  return id >= 0 && id < adapters ? id : kNoAdapter;
+}
+
+__device__ __forceinline__ uint64_t below(int lane) { return (uint64_t(1) << lane) - 1; }
+__device__ __forceinline__ int first_of(uint64_t mask) { return __ffsll((unsigned long long)mask) - 1; }
+
+// Tokens that lead a tile: every TILE-th of an adapter's.
 template <int TILE>
-struct Tiles {
-  int id[kBlockTokens];
-  uint16_t order[kBlockTokens];  // token (of the block) at each sorted place
-  uint16_t first[kBlockTokens];  // sorted place of each tile's first token
-  int adapter[kBlockTokens];     // adapter of each tile, or kNone
-  uint8_t starts[kBlockTokens];
-  int count;                     // tiles
-  int same;
-  int sums[kWaves];
-  __device__ int size(int tile, int cnt) const {
-    return (tile + 1 < count ? first[tile + 1] : cnt) - first[tile];
+__device__ __forceinline__ uint64_t leaders(int id, int lowest) {
+  const int lane = threadIdx.x & (kWave - 1);
+  uint64_t left = __ballot(id >= lowest), lead = 0;
+  while (left) {  // a turn an adapter
+    const int who = __builtin_amdgcn_readlane(id, first_of(left));
+    const uint64_t same = __ballot(id == who);
+    lead |= __ballot(id == who && __popcll(same & below(lane)) % TILE == 0);
+    left &= ~same;
   }
+  return lead;
+}
+
+struct Tile {
+  int id, size;
+  int token;  // of lane s: the tile's s-th token
 };
 
 template <int TILE>
-__device__ __forceinline__ void make_tiles(Tiles<TILE>& s, const int32_t* index, int cnt, int64_t adapters) {
-  const int t = threadIdx.x;
-  int id = 0x7FFFFFFF;  // past the block: behind everything
-  if (t < cnt) {
-    id = index[t];
-    if (id < 0 || id >= adapters) id = kNone;
-  }
-  s.id[t] = id;
-  if (t == 0) s.same = 1;
-  __syncthreads();
-  if (t < cnt && id != s.id[0]) s.same = 0;
-  __syncthreads();
-  // place: tokens of lower adapters, and earlier ones of the same; rank: among the same
-  int place = t, rank = t;
-  if (!s.same) {
-    place = rank = 0;
-    for (int o = 0; o < cnt; ++o) {
-      const int other = s.id[o];
-      place += other < id;
-      rank += other == id && o < t;
-    }
-    place += rank;
-  }
-  if (t < cnt) {
-    s.order[place] = (uint16_t)t;
-    s.starts[place] = rank % TILE == 0;
-  }
-  __syncthreads();
-  const int lane = t & (kWave - 1), wave = t / kWave;
-  const bool start = t < cnt && s.starts[t];
-  const uint64_t mask = __ballot(start);
-  if (lane == 0) s.sums[wave] = __popcll(mask);
-  __syncthreads();
-  int before = __popcll(mask & ((uint64_t(1) << lane) - 1));
-  int total = 0;
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += s.sums[w];
-    total += s.sums[w];
-  }
-  if (start) {
-    s.first[before] = (uint16_t)t;
-    s.adapter[before] = s.id[s.order[t]];
-  }
-  if (t == 0) s.count = total;
-  __syncthreads();
+__device__ __forceinline__ bool leads(int id, int lane) {
+  const int who = __builtin_amdgcn_readlane(id, lane);
+  return __popcll(__ballot(id == who) & below(lane)) % TILE == 0;
+}
+
+template <int TILE>
+__device__ __forceinline__ Tile tile_of(int id, int leader) {
+  const int lane = threadIdx.x & (kWave - 1);
+  Tile t;
+  t.id = __builtin_amdgcn_readlane(id, leader);
+  const uint64_t same = __ballot(id == t.id);
+  const int before = __popcll(same & below(leader));
+  t.size = min(TILE, __popcll(same) - before);
+  const int place = __popcll(same & below(lane)) - before;
+  const bool in = id == t.id && place >= 0 && place < TILE;
+  // Every lane sends its number to its place, those outside the tile to the last lane, which is
+  // asked only for a tile of all 64: then none is outside.
+  t.token = __builtin_amdgcn_ds_permute((in ? place : kWave - 1) * 4, lane);
+  return t;
 }
 
 // ------------------------------------------------------------------- helpers
@@ -165,15 +152,19 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
   }
 }
 
-// A NaN stays one: bf16_rne is for numbers.
-__device__ __forceinline__ uint32_t bf16_any(float f) { return f == f ? bf16_rne(f) : 0x7FC0u; }
+// Two values rounded to bfloat16 (nearest even; a NaN stays one), by one instruction of this part.
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{a, b}), bf16x2_t));
+}
 
 template <bool BF16>
 __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8]) {
   if constexpr (BF16) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_any(v[2 * i]) | bf16_any(v[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
@@ -182,344 +173,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8])
   }
 }
 
-// -------------------------------------------------------------------- shrink
-
-struct ShrinkSide {
-  const uint16_t* p;  // [count][rank][d]
-  const uint16_t* v;  // [m][stride]
-  int64_t stride;
-  float* part;        // [slices][m][rank]
-  int d, slices;
-};
-struct ShrinkArgs {
-  ShrinkSide side[2];  // workgroups x < side[0].slices take the first, the rest the second
-  const int32_t* index;
-  int64_t m, count;
-  int rank;
-};
-
-// Workgroup (slice of d, share of the block's tiles, block of tokens).  A wave
-// takes every fourth 32-wide step of the slice for a tile of up to 32 tokens and
-// all rank rows; the waves' sums meet in LDS, the slices' in the reader.
-// RT: 16-row tiles of the rank.
-template <int RT>
-__global__ __launch_bounds__(kThreads) void lowrank_shrink(ShrinkArgs a) {
-  constexpr int kTile = 32;
-  constexpr int kDepth = RT >= 8 ? 1 : RT >= 4 ? 2 : 4;  // steps whose loads are out together
-  __shared__ Tiles<kTile> s;
-  __shared__ float s_red[kWaves * RT * 2 * 4 * kWave];
-  const ShrinkSide& g = a.side[blockIdx.x >= (unsigned)a.side[0].slices];
-  const int slice = blockIdx.x - (blockIdx.x >= (unsigned)a.side[0].slices ? a.side[0].slices : 0);
-  const int64_t t0 = (int64_t)blockIdx.z * kBlockTokens;
-  const int cnt = (int)min((int64_t)kBlockTokens, a.m - t0);
-  make_tiles(s, a.index + t0, cnt, a.count);
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int c = lane & 15, q = lane >> 4;
-  const int steps = (g.d + 31) / 32;
-  const int per = (steps + g.slices - 1) / g.slices;
-  const int begin = slice * per, end = min(steps, begin + per);
-
-  for (int tile = blockIdx.y; tile < s.count; tile += gridDim.y) {
-    const int id = s.adapter[tile];
-    if (id == kNone) break;  // they come last
-    const int size = s.size(tile, cnt), first = s.first[tile];
-    const uint16_t* p = g.p + (int64_t)id * a.rank * g.d + q * 8;
-    uint32_t row[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) row[i] = (uint32_t)min(i * 16 + c, a.rank - 1) * (uint32_t)g.d;
-    const uint16_t* v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      v[h] = g.v + (t0 + s.order[first + min(h * 16 + c, size - 1)]) * g.stride + q * 8;
-    floatx4_t acc[2][RT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) acc[h][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-
-    auto walk = [&](auto halves) __attribute__((always_inline)) {
-      constexpr int H = decltype(halves)::value;
-      int at = begin + wave;
-      auto some = [&](auto depth) __attribute__((always_inline)) {
-        constexpr int D = decltype(depth)::value;
-        uint4 vv[D][H], pp[D][RT];
-#pragma unroll
-        for (int u = 0; u < D; ++u) {
-          const int e = (at + u * kWaves) * 32;
-          const bool in = e + q * 8 < g.d;  // d is a multiple of 8
-#pragma unroll
-          for (int h = 0; h < H; ++h) vv[u][h] = in ? load16(v[h] + e) : zero16();
-#pragma unroll
-          for (int i = 0; i < RT; ++i) pp[u][i] = in ? load16(p + row[i] + e) : zero16();
-        }
-#pragma unroll
-        for (int u = 0; u < D; ++u)
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-              acc[h][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(pp[u][i]), operand(vv[u][h]),
-                                                                  acc[h][i], 0, 0, 0);
-        at += D * kWaves;
-      };
-      while (at + (kDepth - 1) * kWaves < end) some(std::integral_constant<int, kDepth>{});
-      while (at < end) some(std::integral_constant<int, 1>{});
-    };
-    if (size > 16) walk(std::integral_constant<int, 2>{});
-    else walk(std::integral_constant<int, 1>{});
-
-    // [wave][half][row tile][lane][4]
-    float4* red = reinterpret_cast<float4*>(s_red);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        red[((wave * 2 + h) * RT + i) * kWave + lane] =
-            make_float4(acc[h][i][0], acc[h][i][1], acc[h][i][2], acc[h][i][3]);
-    __syncthreads();
-    for (int o = threadIdx.x; o < 2 * RT * kWave; o += kThreads) {
-      const int ln = o % kWave, i = o / kWave % RT, h = o / kWave / RT;
-      const int token = h * 16 + (ln & 15), r = i * 16 + (ln >> 4) * 4;  // rank is a multiple of 8
-      if (token < size && r < a.rank) {
-        float4 sum = red[o];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) {
-          const float4 add = red[w * 2 * RT * kWave + o];
-          sum.x += add.x; sum.y += add.y; sum.z += add.z; sum.w += add.w;
-        }
-        const int64_t t = t0 + s.order[first + token];
-        *reinterpret_cast<float4*>(g.part + ((int64_t)slice * a.m + t) * a.rank + r) = sum;
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// -------------------------------------------------------------------- expand
-
-struct ExpandArgs {
-  const uint16_t* p;   // [count][rank][d]
-  const float* scale;
-  const float* part;   // [slices][m][rank]
-  const int32_t* index;
-  const void* base;    // [m][base_stride], or nullptr
-  void* out;           // [m][out_stride]
-  int64_t base_stride, out_stride, m, count;
-  int rank, d, slices, block;  // block: tokens of a workgroup, <= kBlockTokens
-};
-
-// Workgroup (512 columns, share of the block's tiles, block of tokens), a wave
-// 128 columns.  The tiles' operands (s c, in parts) are made once in LDS for the
-// four waves, kMade tiles at a time.  Of lane (c, q) = (l % 16, l / 16) the
-// stack's block is rank rows 32 s + 8 q ..., columns 8 pi(c) ... with pi(4 i + j)
-// = 4 j + i: the accumulators of a lane are then, for i = 0..3, the eight columns
-// 8 (4 i + q) ..., so that in a load or store of 16 bytes a token's four lanes
-// touch 64 bytes in a row.
-template <int RS, bool BASE_BF16, bool OUT_BF16>
-__global__ __launch_bounds__(kThreads) void lowrank_expand(ExpandArgs a) {
-  constexpr int PARTS = OUT_BF16 ? 2 : 3;
-  constexpr int kMade = RS * PARTS <= 4 ? 16 : RS * PARTS <= 8 ? 8 : 4;
-  __shared__ Tiles<16> s;
-  __shared__ uint4 s_c[kMade * RS * PARTS * kWave];
-  const int64_t t0 = (int64_t)blockIdx.z * a.block;
-  const int cnt = (int)min((int64_t)a.block, a.m - t0);
-  make_tiles(s, a.index + t0, cnt, a.count);
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int c = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 512 + wave * 128;
-  const int mine = n0 + ((c & 3) * 4 + (c >> 2)) * 8;  // first column of the lane's block
-  uint4 p[RS][8];
-  int held = -1;  // adapter in p
-
-  // this workgroup's tiles: consecutive ones, so that neighbours share an adapter
-  const int share = (s.count + gridDim.y - 1) / gridDim.y;
-  const int last = min(s.count, ((int)blockIdx.y + 1) * share);
-  for (int from = blockIdx.y * share; from < last; from += kMade) {
-    const int made = min(kMade, last - from);
-    for (int w = wave; w < made * RS; w += kWaves) {
-      const int tile = from + w / RS, rs = w % RS;
-      const int id = s.adapter[tile];
-      uint32_t cut[8][PARTS];
-      float v[8] = {};
-      const int r = rs * 32 + q * 8;
-      if (id != kNone && c < s.size(tile, cnt) && r < a.rank) {
-        const float* f = a.part + (t0 + s.order[s.first[tile] + c]) * a.rank + r;
-        const int64_t plane = a.m * a.rank;
-#pragma unroll 4
-        for (int k = 0; k < a.slices; ++k) {
-          float add[8];
-          load8<false>(f, k * plane, add);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += add[e];
-        }
-        const float by = a.scale[id];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= by;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) split<PARTS>(v[e], cut[e]);
-#pragma unroll
-      for (int k = 0; k < PARTS; ++k)
-        s_c[(w * PARTS + k) * kWave + lane] =
-            make_uint4(cut[0][k] | cut[1][k] << 16, cut[2][k] | cut[3][k] << 16,
-                       cut[4][k] | cut[5][k] << 16, cut[6][k] | cut[7][k] << 16);
-    }
-    __syncthreads();
-    for (int w = 0; w < made && n0 < a.d; ++w) {
-      const int tile = from + w, id = __builtin_amdgcn_readfirstlane(s.adapter[tile]);
-      const int size = s.size(tile, cnt);
-      if (id == kNone && a.base == a.out) break;  // nothing to copy, and they come last
-      if (id != held && id != kNone) {
-        held = id;
-#pragma unroll
-        for (int k = 0; k < RS; ++k) {
-          const int r = k * 32 + q * 8;
-          const bool in = r < a.rank && mine < a.d;
-          const uint16_t* at = a.p + ((int64_t)id * a.rank + r) * a.d + mine;
-          uint4 rows[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) rows[e] = in ? load16(at + (int64_t)e * a.d) : zero16();
-          transpose8(rows, p[k]);
-        }
-      }
-      floatx4_t acc[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-      if (id != kNone) {
-#pragma unroll
-        for (int k = 0; k < RS; ++k)
-#pragma unroll
-          for (int e = 0; e < PARTS; ++e) {
-            const bf16x8_t h = operand(s_c[((w * RS + k) * PARTS + e) * kWave + lane]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(p[k][j]), h, acc[j], 0, 0, 0);
-          }
-      }
-      if (c < size) {
-        const int64_t t = t0 + s.order[s.first[tile] + c];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = n0 + (i * 4 + q) * 8;
-          if (n < a.d) {
-            float v[8] = {};
-            if (a.base) load8<BASE_BF16>(a.base, t * a.base_stride + n, v);
-            if (id != kNone) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
-            }
-            store8<OUT_BF16>(a.out, t * a.out_stride + n, v);
-          }
-        }
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// ------------------------------------------------------------------ launches
-
-// 16-row tiles of the rank, as an instance has them.
-int rank_tiles(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
-
-struct ShrinkPlan {
-  int slices, shares;
-  int64_t blocks;
-};
-
-// About 512 workgroups, as long as a wave has a step of its own; shares: workgroups
-// over a block's tiles.  Both follow from m and d alone: the host does not know how
-// many adapters a call meets.
-ShrinkPlan shrink_plan(int64_t m, int64_t d) {
-  ShrinkPlan p;
-  m = std::max<int64_t>(m, 1);
-  p.blocks = (m + kBlockTokens - 1) / kBlockTokens;
-  p.shares = (int)(m > kBlockTokens ? 8 : std::min<int64_t>(m, 32));
-  const int64_t steps = (d + 31) / 32;
-  const int64_t want = (512 + p.blocks * p.shares - 1) / (p.blocks * p.shares);
-  p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({want, (steps + 3) / 4, 16}));
-  const int64_t per = (steps + p.slices - 1) / p.slices;
-  p.slices = (int)std::max<int64_t>(1, (steps + per - 1) / per);  // none without steps
-  return p;
-}
-
-size_t up256(size_t b) { return (b + 255u) & ~size_t(255); }
-
-hipError_t launch_shrink(const ShrinkArgs& a, const ShrinkPlan& plan, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.side[0].slices + a.side[1].slices), (unsigned)plan.shares, (unsigned)plan.blocks);
-  switch (rank_tiles(a.rank)) {
-    case 1: hipLaunchKernelGGL(lowrank_shrink<1>, grid, dim3(kThreads), 0, stream, a); break;
-    case 2: hipLaunchKernelGGL(lowrank_shrink<2>, grid, dim3(kThreads), 0, stream, a); break;
-    case 4: hipLaunchKernelGGL(lowrank_shrink<4>, grid, dim3(kThreads), 0, stream, a); break;
-    default: hipLaunchKernelGGL(lowrank_shrink<8>, grid, dim3(kThreads), 0, stream, a); break;
-  }
-  return hipGetLastError();
-}
-
-template <int RS>
-void launch_expand_of(const ExpandArgs& a, bool base_bf16, bool out_bf16, dim3 grid, hipStream_t stream) {
-  if (base_bf16 && out_bf16)
-    hipLaunchKernelGGL((lowrank_expand<RS, true, true>), grid, dim3(kThreads), 0, stream, a);
-  else if (base_bf16)
-    hipLaunchKernelGGL((lowrank_expand<RS, true, false>), grid, dim3(kThreads), 0, stream, a);
-  else if (out_bf16)
-    hipLaunchKernelGGL((lowrank_expand<RS, false, true>), grid, dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((lowrank_expand<RS, false, false>), grid, dim3(kThreads), 0, stream, a);
-}
-
-hipError_t launch_expand(ExpandArgs a, bool base_bf16, bool out_bf16, hipStream_t stream) {
-  a.block = a.m <= 256 ? 256 : 128;
-  const int64_t shares = a.m > 256 ? 1 : std::min<int64_t>(a.m, 64);
-  const dim3 grid((unsigned)((a.d + 511) / 512), (unsigned)shares, (unsigned)((a.m + a.block - 1) / a.block));
-  if (a.rank <= 32) launch_expand_of<1>(a, base_bf16, out_bf16, grid, stream);
-  else if (a.rank <= 64) launch_expand_of<2>(a, base_bf16, out_bf16, grid, stream);
-  else launch_expand_of<4>(a, base_bf16, out_bf16, grid, stream);
-  return hipGetLastError();
-}
-
-}  // namespace
-
-size_t lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank) {
-  (void)n;
-  return up256((size_t)shrink_plan(m, k).slices * (size_t)m * (size_t)rank * 4u);
-}
-
-hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream) {
-  const ShrinkPlan plan = shrink_plan(c.m, c.a.k);
-  ShrinkArgs s{};
-  s.side[0] = {c.a.down, c.x, c.x_stride, static_cast<float*>(c.workspace), (int)c.a.k, plan.slices};
-  s.index = c.index;
-  s.m = c.m;
-  s.count = c.a.count;
-  s.rank = (int)c.a.rank;
-  const hipError_t e = launch_shrink(s, plan, stream);
-  if (e != hipSuccess) return e;
-  ExpandArgs x{};
-  x.p = c.a.up;
-  x.scale = c.a.scale;
-  x.part = static_cast<const float*>(c.workspace);
-  x.index = c.index;
-  x.base = c.y;
-  x.out = c.out;
-  x.base_stride = c.y_stride;
-  x.out_stride = c.out_stride;
-  x.m = c.m;
-  x.count = c.a.count;
-  x.rank = (int)c.a.rank;
-  x.d = (int)c.a.n;
-  x.slices = plan.slices;
-  return launch_expand(x, c.y_bf16, c.out_bf16, stream);
-}
-
-// ------------------------------------------------------------------ backward
-
-namespace {
-
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWaves = kPlanThreads / kWave;
+// -------------------------------------------------------------- training's plan
 
 // A backward pass' tokens in the order of their adapters, each adapter's from a multiple
 // of 32 on, and the items of work: up to `seg` tokens of one adapter.  An adapter with one
@@ -543,31 +197,61 @@ struct PlanArgs {
   int count, seg;
 };
 
+constexpr int kPlanBytes = (kWaves * (int)kMaxTrained + 3 * kWaves) * 4;
+constexpr int kPlanAdapters = (int)kMaxTrained / kThreads;  // adapters of a thread
+
 // One workgroup: a stable counting sort, every wave over a run of the tokens of its own.
-__global__ __launch_bounds__(kPlanThreads) void lowrank_plan(PlanArgs a) {
-  __shared__ int s_count[kPlanWaves * kMaxTrained];
-  __shared__ int s_scan[3][kPlanWaves];
+__device__ void plan_tokens(const PlanArgs& a, int* s) {
+  constexpr int kAhead = 8;  // vectors of 64 tokens requested together
+  int* s_scan = s + kWaves * kMaxTrained;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  for (int i = tid; i < kPlanWaves * a.count; i += kPlanThreads) s_count[i] = 0;
+  for (int i = tid; i < kWaves * a.count; i += kThreads) s[i] = 0;
   __syncthreads();
-  const int64_t per = ((a.m + kPlanWaves - 1) / kPlanWaves + kWave - 1) / kWave * kWave;
+  const int64_t per = ((a.m + kWaves - 1) / kWaves + kWave - 1) / kWave * kWave;
   const int64_t begin = min(a.m, wave * per), end = min(a.m, begin + per);
-  int* mine = s_count + wave * a.count;
-  for (int64_t t = begin + lane; t < end; t += kWave) {
-    const int id = a.index[t];
-    if (id >= 0 && id < a.count) atomicAdd(mine + id, 1);
-  }
-  __syncthreads();
-  // thread = adapter: the waves' counts become offsets in the adapter's run
-  int total = 0;
-  if (tid < a.count)
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int n = s_count[w * a.count + tid];
-      s_count[w * a.count + tid] = total;
-      total += n;
+  int* mine = s + wave * a.count;
+  auto each = [&](auto&& what) __attribute__((always_inline)) {
+    for (int64_t t0 = begin; t0 < end; t0 += kAhead * kWave) {
+      int id[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t t = t0 + i * kWave + lane;
+        id[i] = a.index[min(t, end - 1)];
+        if (t >= end || id[i] >= a.count) id[i] = -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        uint64_t left = __ballot(id[i] >= 0);
+        while (left) {  // a turn an adapter met
+          const int who = __builtin_amdgcn_readlane(id[i], first_of(left));
+          const uint64_t same = __ballot(id[i] == who);
+          what(t0 + i * kWave + lane, who, id[i] == who, same);
+          left &= ~same;
+        }
+      }
     }
-  const int items = (total + a.seg - 1) / a.seg;
-  int own[3] = {(total + 31) & ~31, items, items > 1 ? items : 0}, at[3];
+  };
+  each([&](int64_t, int who, bool, uint64_t same) __attribute__((always_inline)) {
+    if (lane == 0) mine[who] += __popcll(same);
+  });
+  __syncthreads();
+  // the thread's adapters: the waves' counts become offsets in an adapter's run
+  int total[kPlanAdapters], own[3] = {0, 0, 0}, at[3];
+#pragma unroll
+  for (int i = 0; i < kPlanAdapters; ++i) {
+    const int id = tid * kPlanAdapters + i;
+    total[i] = 0;
+    if (id < a.count)
+      for (int w = 0; w < kWaves; ++w) {
+        const int n = s[w * a.count + id];
+        s[w * a.count + id] = total[i];
+        total[i] += n;
+      }
+    const int items = (total[i] + a.seg - 1) / a.seg;
+    own[0] += (total[i] + 31) & ~31;
+    own[1] += items;
+    own[2] += items > 1 ? items : 0;
+  }
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     int v = own[i];
@@ -575,47 +259,510 @@ __global__ __launch_bounds__(kPlanThreads) void lowrank_plan(PlanArgs a) {
       const int up = __shfl_up(v, off, kWave);
       if (lane >= off) v += up;
     }
-    if (lane == kWave - 1) s_scan[i][wave] = v;
+    if (lane == kWave - 1) s_scan[i * kWaves + wave] = v;
     at[i] = v - own[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 3; ++i)
-    for (int w = 0; w < wave; ++w) at[i] += s_scan[i][w];
-  if (tid == kPlanThreads - 1) {
+    for (int w = 0; w < wave; ++w) at[i] += s_scan[i * kWaves + w];
+  if (tid == kThreads - 1) {
     *a.g.places = at[0] + own[0];
     *a.g.items = at[1] + own[1];
   }
-  if (tid < a.count) {
-    a.g.slots[2 * tid] = items == 1 ? -1 : at[2];
-    a.g.slots[2 * tid + 1] = own[2];
+#pragma unroll
+  for (int k = 0; k < kPlanAdapters; ++k) {
+    const int id = tid * kPlanAdapters + k;
+    if (id >= a.count) break;
+    const int items = (total[k] + a.seg - 1) / a.seg, padded = (total[k] + 31) & ~31;
+    a.g.slots[2 * id] = items == 1 ? -1 : at[2];
+    a.g.slots[2 * id + 1] = items > 1 ? items : 0;
     for (int i = 0; i < items; ++i) {
-      a.g.adapter[at[1] + i] = tid;
+      a.g.adapter[at[1] + i] = id;
       a.g.from[at[1] + i] = at[0] + i * a.seg;
-      a.g.length[at[1] + i] = min(a.seg, total - i * a.seg);
+      a.g.length[at[1] + i] = min(a.seg, total[k] - i * a.seg);
       a.g.slot[at[1] + i] = items > 1 ? at[2] + i : -1;
     }
-    for (int i = total; i < own[0]; ++i) a.g.order[at[0] + i] = -1;
-    for (int w = 0; w < kPlanWaves; ++w) s_count[w * a.count + tid] += at[0];
+    for (int i = total[k]; i < padded; ++i) a.g.order[at[0] + i] = -1;
+    for (int w = 0; w < kWaves; ++w) s[w * a.count + id] += at[0];
+    at[0] += padded;
+    at[1] += items;
+    at[2] += items > 1 ? items : 0;
   }
   __syncthreads();
-  for (int64_t t0 = begin; t0 < end; t0 += kWave) {
-    const int64_t t = t0 + lane;
-    int id = t < end ? a.index[t] : -1;
-    if (id >= a.count) id = -1;
-    uint64_t left = __ballot(id >= 0);
-    while (left) {  // one turn an adapter met
-      const int who = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
-      const uint64_t same = __ballot(id == who);
-      const int place = mine[who];
-      if (id == who) a.g.order[place + __popcll(same & ((uint64_t(1) << lane) - 1))] = (int32_t)t;
-      wave_lds_sync();
-      if (lane == 0) mine[who] = place + __popcll(same);
-      wave_lds_sync();
-      left &= ~same;
+  each([&](int64_t t, int who, bool in, uint64_t same) __attribute__((always_inline)) {
+    const int place = mine[who];
+    if (in) a.g.order[place + __popcll(same & below(lane))] = (int32_t)t;
+    wave_lds_sync();
+    if (lane == 0) mine[who] = place + __popcll(same);
+    wave_lds_sync();
+  });
+}
+
+// -------------------------------------------------------------------- shrink
+
+struct ShrinkSide {
+  const uint16_t* p;  // [count][rank][d]
+  const uint16_t* v;  // [m][stride]
+  int64_t stride;
+  float* part;        // [slices][m][rank]
+  int d, slices;
+};
+struct ShrinkArgs {
+  ShrinkSide side[2];  // workgroups x < side[0].slices take the first, the rest the second
+  const int32_t* index;
+  int64_t m, count;
+  int rank;
+  bool single;  // workgroup y takes the tile that token y leads, if it leads one
+};
+
+// Workgroup (slice of d, share of the block's tiles, block of tokens).  A wave
+// takes a quarter of the slice's 32-wide steps for a tile, all tokens of the block that use
+// one adapter, and all rank rows; the waves' sums meet in LDS, the slices' in the
+// reader.  (Tiles of 32 tokens read the stack twice as often, from L2: 39 us for the
+// two sides of 4096 tokens, 3840 -> 11520, rank 16, where the tokens alone take 27.)
+// RT: 16-row tiles of the rank.  PLAN: the workgroup past the slices sorts the tokens for
+// the gradients, which wait for this launch anyway (9 us as a launch of its own).
+template <int RT, bool PLAN>
+__global__ __launch_bounds__(kThreads) void lowrank_shrink(ShrinkArgs a, PlanArgs plan) {
+  constexpr int kTile = kBlockTokens, kParts = kTile / 16;
+  constexpr int kDepth = RT >= 8 ? 1 : RT >= 4 ? 2 : 4;  // steps whose loads are out together
+  constexpr int kSums = kWaves * RT * 2 * 4 * kWave;
+  __shared__ float s_red[PLAN && kSums * 4 < kPlanBytes ? kPlanBytes / 4 : kSums];
+  if (PLAN && (int)blockIdx.x == a.side[0].slices + a.side[1].slices) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) plan_tokens(plan, reinterpret_cast<int*>(s_red));
+    return;
+  }
+  const bool second = (int)blockIdx.x >= a.side[0].slices;
+  const ShrinkSide& g = a.side[second];
+  const int slice = blockIdx.x - (second ? a.side[0].slices : 0);
+  const int64_t t0 = (int64_t)blockIdx.z * kBlockTokens;
+  const int id = block_id(a.index + t0, (int)min((int64_t)kBlockTokens, a.m - t0), a.count);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, q = lane >> 4;
+  uint64_t lead;
+  if (a.single) {
+    if (__builtin_amdgcn_readlane(id, blockIdx.y) < 0 || !leads<kTile>(id, blockIdx.y)) return;
+    lead = uint64_t(1) << blockIdx.y;
+  } else {
+    lead = leaders<kTile>(id, 0);
+    for (unsigned i = 0; i < blockIdx.y; ++i) lead &= lead - 1;  // tiles y, y + shares, ...
+  }
+  const int whole = g.d / 32, steps = (g.d + 31) / 32;
+  const int per = (steps + g.slices - 1) / g.slices;
+  const int begin = slice * per, end = min(steps, begin + per);
+  const int run = per >= kWaves * kDepth ? kDepth : 1;
+
+  while (lead) {
+    const Tile tile = tile_of<kTile>(id, first_of(lead));
+    for (unsigned i = 0; i < gridDim.y; ++i) lead &= lead - 1;
+    if (a.single) lead = 0;
+    const uint16_t* p = g.p + (int64_t)tile.id * a.rank * g.d + q * 8;
+    uint32_t row[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) row[i] = (uint32_t)min(i * 16 + c, a.rank - 1) * (uint32_t)g.d;
+    const uint16_t* v[kParts];
+#pragma unroll
+    for (int h = 0; h < kParts; ++h)
+      v[h] = g.v + (t0 + __shfl(tile.token, min(h * 16 + c, tile.size - 1), kWave)) * g.stride + q * 8;
+    floatx4_t acc[kParts][RT];
+#pragma unroll
+    for (int h = 0; h < kParts; ++h)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[h][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    auto walk = [&](auto parts) __attribute__((always_inline)) {
+      constexpr int H = decltype(parts)::value;  // sixteenths of tokens
+      // a wave takes runs of steps, so that it reads up to 256 bytes of a row in a row
+      auto some = [&](int at, auto depth, bool full) __attribute__((always_inline)) {
+        constexpr int D = decltype(depth)::value;
+        uint4 vv[D][H], pp[D][RT];
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+          const int e = (at + u) * 32;
+          const bool in = full || e + q * 8 < g.d;  // d is a multiple of 8
+#pragma unroll
+          for (int h = 0; h < H; ++h) vv[u][h] = in ? load16(v[h] + e) : zero16();
+#pragma unroll
+          for (int i = 0; i < RT; ++i) pp[u][i] = in ? load16(p + row[i] + e) : zero16();
+        }
+#pragma unroll
+        for (int u = 0; u < D; ++u)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+              acc[h][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(pp[u][i]), operand(vv[u][h]),
+                                                                  acc[h][i], 0, 0, 0);
+      };
+      const int stop = min(end, whole);
+      int at = begin + wave * run;
+      for (; at < end; at += kWaves * run) {
+        const int to = min(end, at + run);
+        if (at + kDepth <= stop && run == kDepth) {
+          some(at, std::integral_constant<int, kDepth>{}, true);
+        } else {
+          for (int u = at; u < to; ++u) some(u, std::integral_constant<int, 1>{}, u < whole);
+        }
+      }
+    };
+    if (tile.size > 32) walk(std::integral_constant<int, 4>{});
+    else if (tile.size > 16) walk(std::integral_constant<int, 2>{});
+    else walk(std::integral_constant<int, 1>{});
+
+    // [wave][part of two][row tile][lane][4]
+    float4* red = reinterpret_cast<float4*>(s_red);
+#pragma unroll
+    for (int two = 0; two < kParts; two += 2) {
+      if (two * 16 >= tile.size) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          red[((wave * 2 + h) * RT + i) * kWave + lane] = make_float4(
+              acc[two + h][i][0], acc[two + h][i][1], acc[two + h][i][2], acc[two + h][i][3]);
+      __syncthreads();
+      for (int o = wave; o < 2 * RT; o += kWaves) {
+        const int i = o % RT, h = o / RT;
+        const int token = (two + h) * 16 + c, r = i * 16 + q * 4;  // rank is a multiple of 8
+        const int64_t t = t0 + __shfl(tile.token, token, kWave);
+        if (token < tile.size && r < a.rank) {
+          float4 sum = red[o * kWave + lane];
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) {
+            const float4 add = red[(w * 2 * RT + o) * kWave + lane];
+            sum.x += add.x; sum.y += add.y; sum.z += add.z; sum.w += add.w;
+          }
+          *reinterpret_cast<float4*>(g.part + ((int64_t)slice * a.m + t) * a.rank + r) = sum;
+        }
+      }
+      __syncthreads();
     }
   }
 }
+
+// -------------------------------------------------------------------- expand
+
+struct ExpandArgs {
+  const uint16_t* p;   // [count][rank][d]
+  const float* scale;
+  const float* part;   // [slices][m][rank]
+  const int32_t* index;
+  const void* base;    // [m][base_stride], or nullptr
+  void* out;           // [m][out_stride]
+  int64_t base_stride, out_stride, m, count;
+  int rank, d, slices;
+};
+
+// Eight sums of the slices of c, in order, times the adapter's scale: the loads of four
+// slices are out together.
+__device__ __forceinline__ void scaled(const float* part, int64_t plane, int slices, float by, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  for (int k = 0; k < slices; k += 4) {
+    float add[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load8<false>(part, min(k + i, slices - 1) * plane, add[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += k + i < slices ? add[i][e] : 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= by;
+}
+
+// What a lane adds to of one tile: eight columns in each of four places, as they are stored.
+template <bool BF16> struct Base { uint4 v[BF16 ? 4 : 8]; };
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(const Base<BF16>& b, int i, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {b.v[i].x, b.v[i].y, b.v[i].z, b.v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 a = b.v[2 * i + k];
+      v[4 * k] = __uint_as_float(a.x);
+      v[4 * k + 1] = __uint_as_float(a.y);
+      v[4 * k + 2] = __uint_as_float(a.z);
+      v[4 * k + 3] = __uint_as_float(a.w);
+    }
+  }
+}
+
+constexpr int kMade = 4;  // tiles whose operands are in LDS together: one a wave
+template <int RS, bool OUT_BF16>
+struct ExpandShared {
+  uint4 c[kMade][RS][OUT_BF16 ? 2 : 3][kWave];
+};
+
+// Workgroup (512 columns, share of the block's tiles, block of tokens), a wave
+// 128 columns.  The tiles' operands (s c, in parts) are made once in LDS, a tile a wave,
+// for the four waves.  Of lane (c, q) = (l % 16, l / 16) the stack's block is rank rows
+// 32 s + 8 q ..., columns 8 pi(c) ... with pi(4 i + j) = 4 j + i: the accumulators of a
+// lane are then, for i = 0..3, the eight columns 8 (4 i + q) ..., so that in a load or
+// store of 16 bytes a token's four lanes touch 64 bytes in a row.  What a tile adds to is
+// requested a tile ahead, the first with the stack's block before the operands are made.
+template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
+__device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT_BF16>& s, int bx, int by, int bz) {
+  constexpr int PARTS = OUT_BF16 ? 2 : 3;
+  const int64_t t0 = (int64_t)bz * kBlockTokens;
+  const int id = block_id(a.index + t0, (int)min((int64_t)kBlockTokens, a.m - t0), a.count);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, q = lane >> 4;
+  const int lowest = a.base == a.out ? 0 : kNoAdapter;  // in place, tokens without an adapter are done
+  uint64_t lead;
+  if constexpr (SINGLE) {
+    if (__builtin_amdgcn_readlane(id, by) < lowest || !leads<16>(id, by)) return;
+    lead = uint64_t(1) << by;
+  } else {
+    lead = leaders<16>(id, lowest);
+  }
+  const int n0 = bx * 512 + wave * 128;
+  const int mine = n0 + ((c & 3) * 4 + (c >> 2)) * 8;  // first column of the lane's block
+  const int64_t plane = a.m * a.rank;
+  uint4 p[RS][8];
+  int held = kNoToken;  // adapter in p
+
+  auto load_p = [&](int who) __attribute__((always_inline)) {
+    if (who == held || who < 0) return;
+    held = who;
+#pragma unroll
+    for (int k = 0; k < RS; ++k) {
+      const int r = k * 32 + q * 8;
+      const bool in = r < a.rank && mine < a.d;
+      const uint16_t* at = a.p + ((int64_t)who * a.rank + r) * a.d + mine;
+      uint4 rows[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rows[e] = in ? load16(at + (int64_t)e * a.d) : zero16();
+      transpose8(rows, p[k]);
+    }
+  };
+  // places past d or the tile read the first place of its last token
+  auto load_base = [&](const Tile& t, Base<BASE_BF16>& b) __attribute__((always_inline)) {
+    const int64_t token = t0 + __shfl(t.token, min(c, t.size - 1), kWave);
+    const char* from = static_cast<const char*>(a.base) + token * a.base_stride * (BASE_BF16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int n = n0 + (i * 4 + q) * 8;
+      n = n < a.d ? n : 0;
+      if constexpr (BASE_BF16) {
+        b.v[i] = *reinterpret_cast<const uint4*>(from + (int64_t)n * 2);
+      } else {
+        b.v[2 * i] = *reinterpret_cast<const uint4*>(from + (int64_t)n * 4);
+        b.v[2 * i + 1] = *reinterpret_cast<const uint4*>(from + (int64_t)n * 4 + 16);
+      }
+    }
+  };
+
+  while (lead) {
+    // the next tiles: this wave's to make, and where each begins
+    uint64_t rest = lead;
+    int made = 0, own = -1;
+#pragma unroll
+    for (int w = 0; w < kMade; ++w)
+      if (rest) {
+        if (w == wave) own = first_of(rest);
+        rest &= rest - 1;
+        ++made;
+      }
+    Tile t = tile_of<16>(id, first_of(lead));
+    Base<BASE_BF16> base{}, ahead{};
+    if (n0 < a.d) {
+      if (a.base) load_base(t, base);
+      load_p(t.id);
+    }
+    if (own >= 0) {
+      const Tile o = tile_of<16>(id, own);
+      const int64_t token = t0 + __shfl(o.token, min(c, o.size - 1), kWave);
+      const float scale = o.id >= 0 ? a.scale[o.id] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < RS; ++k) {
+        const int r = k * 32 + q * 8;
+        uint32_t cut[8][PARTS];
+        float v[8] = {};
+        if (o.id >= 0 && c < o.size && r < a.rank)
+          scaled(a.part + token * a.rank + r, plane, a.slices, scale, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split<PARTS>(v[e], cut[e]);
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e)
+          s.c[wave][k][e][lane] = make_uint4(cut[0][e] | cut[1][e] << 16, cut[2][e] | cut[3][e] << 16,
+                                             cut[4][e] | cut[5][e] << 16, cut[6][e] | cut[7][e] << 16);
+      }
+    }
+    lds_barrier();
+    for (int w = 0; w < made; ++w) {
+      lead &= lead - 1;
+      Tile next = t;
+      if (!SINGLE && w + 1 < made) {
+        next = tile_of<16>(id, first_of(lead));
+        if (n0 < a.d && a.base) load_base(next, ahead);
+      }
+      if (n0 < a.d) {
+        if (!SINGLE) load_p(t.id);
+        floatx4_t acc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        if (t.id >= 0) {
+#pragma unroll
+          for (int k = 0; k < RS; ++k)
+#pragma unroll
+            for (int e = 0; e < PARTS; ++e) {
+              const bf16x8_t h = operand(s.c[w][k][e][lane]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(p[k][j]), h, acc[j], 0, 0, 0);
+            }
+        }
+        const int64_t token = t0 + __shfl(t.token, c, kWave);
+        if (c < t.size) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = n0 + (i * 4 + q) * 8;
+            float v[8] = {};
+            if (a.base) unpack<BASE_BF16>(base, i, v);
+            if (t.id >= 0) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
+            }
+            if (n < a.d) store8<OUT_BF16>(a.out, token * a.out_stride + n, v);
+          }
+        }
+      }
+      if (SINGLE) return;
+      t = next;
+      base = ahead;
+    }
+    if (lead) lds_barrier();  // the operands are made anew
+  }
+}
+
+// Waves of a SIMD that the registers are to leave room for: the loads of several hide each
+// other's waits.
+template <int RS, bool SINGLE> constexpr int expand_waves() { return RS == 1 ? (SINGLE ? 4 : 3) : RS == 2 ? (SINGLE ? 3 : 2) : 1; }
+
+// SINGLE: one block of tokens, whose workgroup y takes the tile that token y leads, if any.
+template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
+__global__ __launch_bounds__(kThreads, (expand_waves<RS, SINGLE>())) void lowrank_expand(ExpandArgs a) {
+  __shared__ ExpandShared<RS, OUT_BF16> s;
+  expand<RS, BASE_BF16, OUT_BF16, SINGLE>(a, s, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
+// ------------------------------------------------------------------ launches
+
+// 16-row tiles of the rank, as an instance has them.
+int rank_tiles(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+int64_t blocks_of(int64_t m) { return (m + kBlockTokens - 1) / kBlockTokens; }
+// One block of tokens: a workgroup a token, those that lead no tile end at once.  The
+// host does not know how many adapters a call meets; more blocks have work enough.
+bool single_block(int64_t m) { return m <= kBlockTokens; }
+
+struct ShrinkPlan {
+  int slices, shares;
+};
+
+// About 512 workgroups, as long as a wave has a step of its own.  Shares of a block's tiles:
+// its two full ones, where adapters come in runs.
+ShrinkPlan shrink_plan(int64_t m, int64_t d) {
+  ShrinkPlan p;
+  m = std::max<int64_t>(m, 1);
+  p.shares = (int)(single_block(m) ? m : 2);
+  const int64_t steps = (d + 31) / 32, groups = blocks_of(m) * p.shares;
+  const int64_t want = (512 + groups - 1) / groups;
+  p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({want, (steps + 3) / 4, 16}));
+  const int64_t per = (steps + p.slices - 1) / p.slices;
+  p.slices = (int)((steps + per - 1) / per);  // none without steps
+  return p;
+}
+
+size_t up256(size_t b) { return (b + 255u) & ~size_t(255); }
+
+template <bool PLAN>
+hipError_t launch_shrink(const ShrinkArgs& a, const PlanArgs& plan, int shares, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.side[0].slices + a.side[1].slices + PLAN), (unsigned)shares,
+                  (unsigned)std::max<int64_t>(1, blocks_of(a.m)));
+  switch (rank_tiles(a.rank)) {
+    case 1: hipLaunchKernelGGL((lowrank_shrink<1, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
+    case 2: hipLaunchKernelGGL((lowrank_shrink<2, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
+    case 4: hipLaunchKernelGGL((lowrank_shrink<4, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
+    default: hipLaunchKernelGGL((lowrank_shrink<8, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
+  }
+  return hipGetLastError();
+}
+
+template <int RS, bool SINGLE>
+hipError_t launch_expand_of(const ExpandArgs& a, bool base_bf16, bool out_bf16, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.d + 511) / 512), (unsigned)(SINGLE ? a.m : 1), (unsigned)blocks_of(a.m));
+  if (base_bf16 && out_bf16)
+    hipLaunchKernelGGL((lowrank_expand<RS, true, true, SINGLE>), grid, dim3(kThreads), 0, stream, a);
+  else if (base_bf16)
+    hipLaunchKernelGGL((lowrank_expand<RS, true, false, SINGLE>), grid, dim3(kThreads), 0, stream, a);
+  else if (out_bf16)
+    hipLaunchKernelGGL((lowrank_expand<RS, false, true, SINGLE>), grid, dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((lowrank_expand<RS, false, false, SINGLE>), grid, dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <bool SINGLE>
+hipError_t launch_expand_as(const ExpandArgs& a, bool base_bf16, bool out_bf16, hipStream_t stream) {
+  return a.rank <= 32 ? launch_expand_of<1, SINGLE>(a, base_bf16, out_bf16, stream)
+         : a.rank <= 64 ? launch_expand_of<2, SINGLE>(a, base_bf16, out_bf16, stream)
+                        : launch_expand_of<4, SINGLE>(a, base_bf16, out_bf16, stream);
+}
+hipError_t launch_expand(const ExpandArgs& a, bool base_bf16, bool out_bf16, hipStream_t stream) {
+  return single_block(a.m) ? launch_expand_as<true>(a, base_bf16, out_bf16, stream)
+                           : launch_expand_as<false>(a, base_bf16, out_bf16, stream);
+}
+
+}  // namespace
+
+size_t lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank) {
+  (void)n;
+  return up256((size_t)shrink_plan(m, k).slices * (size_t)m * (size_t)rank * 4u);
+}
+
+hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream) {
+  const ShrinkPlan plan = shrink_plan(c.m, c.a.k);
+  ShrinkArgs s{};
+  s.side[0] = {c.a.down, c.x, c.x_stride, static_cast<float*>(c.workspace), (int)c.a.k, plan.slices};
+  s.index = c.index;
+  s.m = c.m;
+  s.count = c.a.count;
+  s.rank = (int)c.a.rank;
+  s.single = single_block(c.m);
+  const hipError_t e = launch_shrink<false>(s, PlanArgs{}, plan.shares, stream);
+  if (e != hipSuccess) return e;
+  ExpandArgs x{};
+  x.p = c.a.up;
+  x.scale = c.a.scale;
+  x.part = static_cast<const float*>(c.workspace);
+  x.index = c.index;
+  x.base = c.y;
+  x.out = c.out;
+  x.base_stride = c.y_stride;
+  x.out_stride = c.out_stride;
+  x.m = c.m;
+  x.count = c.a.count;
+  x.rank = (int)c.a.rank;
+  x.d = (int)c.a.n;
+  x.slices = plan.slices;
+  return launch_expand(x, c.y_bf16, c.out_bf16, stream);
+}
+
+// ------------------------------------------------------------------ backward
+
+namespace {
 
 struct OperandArgs {
   GradPlan g;
@@ -629,26 +776,18 @@ struct OperandArgs {
 };
 
 // s c in bfloat16 parts, transposed: what the rows of grad's products read along the
-// tokens.  A thread makes eight ranks of one place.
+// tokens.  A thread makes eight ranks of one place; `group`: 256 places of eight ranks and a side.
 template <int PARTS>
-__global__ __launch_bounds__(kThreads) void lowrank_operands(OperandArgs a) {
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= *a.g.places) return;
-  const int side = blockIdx.z, r = blockIdx.y * 8;
+__device__ __forceinline__ void operands(const OperandArgs& a, int64_t group) {
+  const int64_t groups = (a.cap + kThreads - 1) / kThreads;
+  const int64_t j = group % groups * kThreads + threadIdx.x;
+  const int which = (int)(group / groups);
+  const int side = which / (a.rank / 8), r = which % (a.rank / 8) * 8;
+  if (side > 1 || j >= *a.g.places) return;
   const int t = a.g.order[j];
   float v[8] = {};
-  if (t >= 0) {
-    const float* f = a.part[side] + (int64_t)t * a.rank + r;
-    for (int k = 0; k < a.slices[side]; ++k) {
-      float add[8];
-      load8<false>(f, (int64_t)k * a.m * a.rank, add);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += add[e];
-    }
-    const float by = a.scale[a.index[t]];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= by;
-  }
+  if (t >= 0)
+    scaled(a.part[side] + (int64_t)t * a.rank + r, a.m * a.rank, a.slices[side], a.scale[a.index[t]], v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint32_t cut[PARTS];
@@ -657,6 +796,24 @@ __global__ __launch_bounds__(kThreads) void lowrank_operands(OperandArgs a) {
     for (int k = 0; k < PARTS; ++k)
       a.out[side][((int64_t)k * a.rank + r + e) * a.cap + j] = (uint16_t)cut[k];
   }
+}
+
+template <int PARTS>
+__global__ __launch_bounds__(kThreads) void lowrank_operands(OperandArgs a) {
+  operands<PARTS>(a, blockIdx.x);
+}
+
+// The input's gradient and the operands of the adapters' own: workgroups x < columns expand,
+// the others make operands (a launch less).
+template <int RS, bool BF16, bool GRAD_BF16>
+__global__ __launch_bounds__(kThreads, (expand_waves<RS, false>())) void lowrank_expand_operands(ExpandArgs a, OperandArgs o,
+                                                                                               int columns) {
+  __shared__ ExpandShared<RS, BF16> s;
+  if ((int)blockIdx.x < columns) {
+    expand<RS, BF16, BF16, false>(a, s, blockIdx.x, 0, blockIdx.y);
+    return;
+  }
+  operands<GRAD_BF16 ? 2 : 3>(o, (int64_t)blockIdx.y * ((int)gridDim.x - columns) + ((int)blockIdx.x - columns));
 }
 
 struct GradSide {
@@ -806,9 +963,40 @@ BackwardPlan backward_plan(int64_t m, int64_t k, int64_t n, int64_t rank, int64_
 }
 
 template <int RT>
-void launch_grad_of(const GradArgs& g, bool bf16, dim3 grid, hipStream_t stream) {
+hipError_t launch_grad_of(const GradArgs& g, bool bf16, dim3 grid, hipStream_t stream) {
   if (bf16) hipLaunchKernelGGL((lowrank_grad<RT, true>), grid, dim3(kThreads), 0, stream, g);
   else hipLaunchKernelGGL((lowrank_grad<RT, false>), grid, dim3(kThreads), 0, stream, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad(const GradArgs& g, bool bf16, int64_t items, hipStream_t stream) {
+  const dim3 grid((unsigned)(g.side[0].blocks + g.side[1].blocks), (unsigned)items, (unsigned)(g.rank > 64 ? 2 : 1));
+  return g.rank <= 16 ? launch_grad_of<1>(g, bf16, grid, stream)
+         : g.rank <= 32 ? launch_grad_of<2>(g, bf16, grid, stream) : launch_grad_of<4>(g, bf16, grid, stream);
+}
+
+template <int RS>
+hipError_t launch_both_of(const ExpandArgs& a, const OperandArgs& o, bool bf16, bool grad_bf16, dim3 grid,
+                          int columns, hipStream_t stream) {
+  if (bf16 && grad_bf16)
+    hipLaunchKernelGGL((lowrank_expand_operands<RS, true, true>), grid, dim3(kThreads), 0, stream, a, o, columns);
+  else if (bf16)
+    hipLaunchKernelGGL((lowrank_expand_operands<RS, true, false>), grid, dim3(kThreads), 0, stream, a, o, columns);
+  else if (grad_bf16)
+    hipLaunchKernelGGL((lowrank_expand_operands<RS, false, true>), grid, dim3(kThreads), 0, stream, a, o, columns);
+  else
+    hipLaunchKernelGGL((lowrank_expand_operands<RS, false, false>), grid, dim3(kThreads), 0, stream, a, o, columns);
+  return hipGetLastError();
+}
+
+hipError_t launch_both(const ExpandArgs& a, const OperandArgs& o, bool bf16, bool grad_bf16, int64_t groups,
+                       hipStream_t stream) {
+  const int columns = (a.d + 511) / 512;
+  const int64_t blocks = blocks_of(a.m);
+  const dim3 grid((unsigned)(columns + (groups + blocks - 1) / blocks), (unsigned)blocks);
+  return a.rank <= 32 ? launch_both_of<1>(a, o, bf16, grad_bf16, grid, columns, stream)
+         : a.rank <= 64 ? launch_both_of<2>(a, o, bf16, grad_bf16, grid, columns, stream)
+                        : launch_both_of<4>(a, o, bf16, grad_bf16, grid, columns, stream);
 }
 
 }  // namespace
@@ -817,6 +1005,8 @@ size_t lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t
   return backward_plan(m, k, n, rank, count).bytes;
 }
 
+// Four launches: both shrinks and the plan; dx and the operands; both gradients; their slots
+// joined.
 hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream) {
   const int64_t k = c.a.k, n = c.a.n, rank = c.a.rank;
   const BackwardPlan b = backward_plan(c.m, k, n, rank, c.a.count);
@@ -825,36 +1015,6 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
   float* part_e = reinterpret_cast<float*>(ws + b.part_e);
   const bool grads = c.d_down != nullptr;
   hipError_t err;
-
-  ShrinkArgs s{};
-  const ShrinkSide down{c.a.down, c.x, c.x_stride, part_h, (int)k, b.h.slices};
-  const ShrinkSide up{c.a.up, c.dy, c.dy_stride, part_e, (int)n, b.e.slices};
-  s.side[0] = up;
-  if (grads) s.side[1] = down;
-  s.index = c.index;
-  s.m = c.m;
-  s.count = c.a.count;
-  s.rank = (int)rank;
-  if (c.m > 0 && (err = launch_shrink(s, b.e, stream)) != hipSuccess) return err;
-
-  if (c.dx_out) {
-    ExpandArgs x{};
-    x.p = c.a.down;
-    x.scale = c.a.scale;
-    x.part = part_e;
-    x.index = c.index;
-    x.base = c.dx;
-    x.out = c.dx_out;
-    x.base_stride = c.dx_stride;
-    x.out_stride = c.dx_out_stride;
-    x.m = c.m;
-    x.count = c.a.count;
-    x.rank = (int)rank;
-    x.d = (int)k;
-    x.slices = b.e.slices;
-    if ((err = launch_expand(x, c.dx_bf16, c.dx_bf16, stream)) != hipSuccess) return err;
-  }
-  if (!grads) return hipSuccess;
 
   GradPlan g;
   int32_t* list = reinterpret_cast<int32_t*>(ws + b.lists);
@@ -866,9 +1026,34 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
   g.length = g.from + b.items;
   g.slot = g.length + b.items;
   g.slots = g.slot + b.items;
-  PlanArgs p{g, c.index, c.m, (int)c.a.count, b.seg};
-  hipLaunchKernelGGL(lowrank_plan, dim3(1), dim3(kPlanThreads), 0, stream, p);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
+
+  ShrinkArgs s{};
+  s.side[0] = {c.a.up, c.dy, c.dy_stride, part_e, (int)n, b.e.slices};
+  if (grads) s.side[1] = {c.a.down, c.x, c.x_stride, part_h, (int)k, b.h.slices};
+  s.index = c.index;
+  s.m = c.m;
+  s.count = c.a.count;
+  s.rank = (int)rank;
+  s.single = single_block(c.m);
+  err = grads ? launch_shrink<true>(s, PlanArgs{g, c.index, c.m, (int)c.a.count, b.seg}, b.e.shares, stream)
+              : launch_shrink<false>(s, PlanArgs{}, b.e.shares, stream);
+  if (err != hipSuccess) return err;
+
+  ExpandArgs x{};
+  x.p = c.a.down;
+  x.scale = c.a.scale;
+  x.part = part_e;
+  x.index = c.index;
+  x.base = c.dx;
+  x.out = c.dx_out;
+  x.base_stride = c.dx_stride;
+  x.out_stride = c.dx_out_stride;
+  x.m = c.m;
+  x.count = c.a.count;
+  x.rank = (int)rank;
+  x.d = (int)k;
+  x.slices = b.e.slices;
+  if (!grads) return launch_expand(x, c.dx_bf16, c.dx_bf16, stream);
 
   OperandArgs o{};
   o.g = g;
@@ -883,14 +1068,6 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
   o.m = c.m;
   o.cap = b.cap;
   o.rank = (int)rank;
-  // no tokens: no places and no items, and the join below writes zeros
-  const dim3 og((unsigned)((b.cap + kThreads - 1) / kThreads), (unsigned)(rank / 8), 2);
-  if (c.m > 0) {
-    if (c.grad_bf16) hipLaunchKernelGGL(lowrank_operands<2>, og, dim3(kThreads), 0, stream, o);
-    else hipLaunchKernelGGL(lowrank_operands<3>, og, dim3(kThreads), 0, stream, o);
-  }
-  if ((err = hipGetLastError()) != hipSuccess) return err;
-
   GradArgs ga{};
   ga.g = g;
   ga.side[0] = {c.x, o.out[0], c.x_stride, reinterpret_cast<float*>(ws + b.sums_down), c.d_down, (int)k,
@@ -899,25 +1076,30 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
                 (int)((n + 511) / 512)};
   ga.cap = b.cap;
   ga.rank = (int)rank;
-  const dim3 gg((unsigned)(ga.side[0].blocks + ga.side[1].blocks), (unsigned)b.items, (unsigned)(rank > 64 ? 2 : 1));
-  if (c.m == 0) {
-  } else if (rank <= 16) launch_grad_of<1>(ga, c.grad_bf16, gg, stream);
-  else if (rank <= 32) launch_grad_of<2>(ga, c.grad_bf16, gg, stream);
-  else launch_grad_of<4>(ga, c.grad_bf16, gg, stream);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
+  if (c.m > 0) {  // else there is no item, and the join writes zeros
+    const int64_t groups = (b.cap + kThreads - 1) / kThreads * (rank / 8) * 2;
+    if (c.dx_out) {
+      err = launch_both(x, o, c.dx_bf16, c.grad_bf16, groups, stream);
+    } else {
+      if (c.grad_bf16) hipLaunchKernelGGL(lowrank_operands<2>, dim3((unsigned)groups), dim3(kThreads), 0, stream, o);
+      else hipLaunchKernelGGL(lowrank_operands<3>, dim3((unsigned)groups), dim3(kThreads), 0, stream, o);
+      err = hipGetLastError();
+    }
+    if (err != hipSuccess) return err;
+    if ((err = launch_grad(ga, c.grad_bf16, b.items, stream)) != hipSuccess) return err;
+  }
 
   JoinArgs j{};
   j.slots = g.slots;
-  j.part[0] = ga.side[0].part;
-  j.part[1] = ga.side[1].part;
-  j.out[0] = c.d_down;
-  j.out[1] = c.d_up;
-  j.size[0] = rank * k;
-  j.size[1] = rank * n;
+  for (int i = 0; i < 2; ++i) {
+    j.part[i] = ga.side[i].part;
+    j.out[i] = ga.side[i].out;
+    j.size[i] = rank * ga.side[i].d;
+  }
   const int64_t widest = std::max(j.size[0], j.size[1]);
-  const dim3 jg((unsigned)std::min<int64_t>((widest / 8 + kThreads - 1) / kThreads, 1024), (unsigned)c.a.count, 2);
-  if (c.grad_bf16) hipLaunchKernelGGL(lowrank_join<true>, jg, dim3(kThreads), 0, stream, j);
-  else hipLaunchKernelGGL(lowrank_join<false>, jg, dim3(kThreads), 0, stream, j);
+  const dim3 grid((unsigned)std::min<int64_t>((widest / 8 + kThreads - 1) / kThreads, 1024), (unsigned)c.a.count, 2);
+  if (c.grad_bf16) hipLaunchKernelGGL(lowrank_join<true>, grid, dim3(kThreads), 0, stream, j);
+  else hipLaunchKernelGGL(lowrank_join<false>, grid, dim3(kThreads), 0, stream, j);
   return hipGetLastError();
 }
 
