@@ -197,11 +197,13 @@ struct PlanArgs {
   int count, seg;
 };
 
-constexpr int kPlanBytes = (kWaves * (int)kMaxTrained + 3 * kWaves) * 4;
-constexpr int kPlanAdapters = (int)kMaxTrained / kThreads;  // adapters of a thread
+template <int W> constexpr int plan_bytes() { return (W * (int)kMaxTrained + 3 * W) * 4; }
 
-// One workgroup: a stable counting sort, every wave over a run of the tokens of its own.
+// One workgroup of W waves: a stable counting sort, every wave over a run of the tokens of its own.
+template <int W>
 __device__ void plan_tokens(const PlanArgs& a, int* s) {
+  constexpr int kWaves = W, kThreads = W * kWave;
+  constexpr int kPlanAdapters = (int)kMaxTrained / kThreads;  // adapters of a thread
   constexpr int kAhead = 8;  // vectors of 64 tokens requested together
   int* s_scan = s + kWaves * kMaxTrained;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
@@ -323,14 +325,15 @@ struct ShrinkArgs {
 // two sides of 4096 tokens, 3840 -> 11520, rank 16, where the tokens alone take 27.)
 // RT: 16-row tiles of the rank.  PLAN: the workgroup past the slices sorts the tokens for
 // the gradients, which wait for this launch anyway (9 us as a launch of its own).
-template <int RT, bool PLAN>
-__global__ __launch_bounds__(kThreads) void lowrank_shrink(ShrinkArgs a, PlanArgs plan) {
+template <int RT, int W, bool PLAN>
+__global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanArgs plan) {
+  constexpr int kWaves = W;
   constexpr int kTile = kBlockTokens, kParts = kTile / 16;
   constexpr int kDepth = RT >= 8 ? 1 : RT >= 4 ? 2 : 4;  // steps whose loads are out together
   constexpr int kSums = kWaves * RT * 2 * 4 * kWave;
-  __shared__ float s_red[PLAN && kSums * 4 < kPlanBytes ? kPlanBytes / 4 : kSums];
+  __shared__ float s_red[PLAN && kSums * 4 < plan_bytes<W>() ? plan_bytes<W>() / 4 : kSums];
   if (PLAN && (int)blockIdx.x == a.side[0].slices + a.side[1].slices) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) plan_tokens(plan, reinterpret_cast<int*>(s_red));
+    if (blockIdx.y == 0 && blockIdx.z == 0) plan_tokens<W>(plan, reinterpret_cast<int*>(s_red));
     return;
   }
   const bool second = (int)blockIdx.x >= a.side[0].slices;
@@ -358,14 +361,14 @@ __global__ __launch_bounds__(kThreads) void lowrank_shrink(ShrinkArgs a, PlanArg
     const Tile tile = tile_of<kTile>(id, first_of(lead));
     for (unsigned i = 0; i < gridDim.y; ++i) lead &= lead - 1;
     if (a.single) lead = 0;
-    const uint16_t* p = g.p + (int64_t)tile.id * a.rank * g.d + q * 8;
+    const uint16_t* p = g.p + (int64_t)tile.id * a.rank * g.d;
     uint32_t row[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) row[i] = (uint32_t)min(i * 16 + c, a.rank - 1) * (uint32_t)g.d;
     const uint16_t* v[kParts];
 #pragma unroll
     for (int h = 0; h < kParts; ++h)
-      v[h] = g.v + (t0 + __shfl(tile.token, min(h * 16 + c, tile.size - 1), kWave)) * g.stride + q * 8;
+      v[h] = g.v + (t0 + __shfl(tile.token, min(h * 16 + c, tile.size - 1), kWave)) * g.stride;
     floatx4_t acc[kParts][RT];
 #pragma unroll
     for (int h = 0; h < kParts; ++h)
@@ -380,12 +383,19 @@ __global__ __launch_bounds__(kThreads) void lowrank_shrink(ShrinkArgs a, PlanArg
         uint4 vv[D][H], pp[D][RT];
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-          const int e = (at + u) * 32;
-          const bool in = full || e + q * 8 < g.d;  // d is a multiple of 8
+          const int e = (at + u) * 32 + q * 8;
+          const bool in = full || e < g.d;  // d is a multiple of 8
+          const int col = in ? e : 0;       // past d the row's first columns are read, and dropped
 #pragma unroll
-          for (int h = 0; h < H; ++h) vv[u][h] = in ? load16(v[h] + e) : zero16();
+          for (int h = 0; h < H; ++h) {
+            const uint4 x = load16(v[h] + col);
+            vv[u][h] = in ? x : zero16();
+          }
 #pragma unroll
-          for (int i = 0; i < RT; ++i) pp[u][i] = in ? load16(p + row[i] + e) : zero16();
+          for (int i = 0; i < RT; ++i) {
+            const uint4 x = load16(p + row[i] + col);
+            pp[u][i] = in ? x : zero16();
+          }
         }
 #pragma unroll
         for (int u = 0; u < D; ++u)
@@ -648,19 +658,19 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
 
 // Waves of a SIMD that the registers are to leave room for: the loads of several hide each
 // other's waits.
-template <int RS, bool SINGLE> constexpr int expand_waves() { return RS == 1 ? (SINGLE ? 4 : 3) : RS == 2 ? (SINGLE ? 3 : 2) : 1; }
+template <int RS, bool BASE_BF16, bool SINGLE>
+constexpr int expand_waves() {
+  return RS == 1 ? (SINGLE ? 4 : BASE_BF16 ? 3 : 2) : RS == 2 ? (SINGLE ? 3 : 2) : 1;
+}
 
 // SINGLE: one block of tokens, whose workgroup y takes the tile that token y leads, if any.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
-__global__ __launch_bounds__(kThreads, (expand_waves<RS, SINGLE>())) void lowrank_expand(ExpandArgs a) {
+__global__ __launch_bounds__(kThreads, (expand_waves<RS, BASE_BF16, SINGLE>())) void lowrank_expand(ExpandArgs a) {
   __shared__ ExpandShared<RS, OUT_BF16> s;
   expand<RS, BASE_BF16, OUT_BF16, SINGLE>(a, s, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // ------------------------------------------------------------------ launches
-
-// 16-row tiles of the rank, as an instance has them.
-int rank_tiles(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
 int64_t blocks_of(int64_t m) { return (m + kBlockTokens - 1) / kBlockTokens; }
 // One block of tokens: a workgroup a token, those that lead no tile end at once.  The
@@ -672,7 +682,7 @@ struct ShrinkPlan {
 };
 
 // About 512 workgroups, as long as a wave has a step of its own.  Shares of a block's tiles:
-// its two full ones, where adapters come in runs.
+// two, for the blocks in which one adapter's run ends and another's begins.
 ShrinkPlan shrink_plan(int64_t m, int64_t d) {
   ShrinkPlan p;
   m = std::max<int64_t>(m, 1);
@@ -687,17 +697,23 @@ ShrinkPlan shrink_plan(int64_t m, int64_t d) {
 
 size_t up256(size_t b) { return (b + 255u) & ~size_t(255); }
 
+template <int W, bool PLAN>
+hipError_t launch_shrink_of(const ShrinkArgs& a, const PlanArgs& plan, dim3 grid, hipStream_t stream) {
+  const dim3 threads(W * kWave);
+  if (a.rank <= 16) hipLaunchKernelGGL((lowrank_shrink<1, W, PLAN>), grid, threads, 0, stream, a, plan);
+  else if (a.rank <= 32) hipLaunchKernelGGL((lowrank_shrink<2, W, PLAN>), grid, threads, 0, stream, a, plan);
+  else if (a.rank <= 64) hipLaunchKernelGGL((lowrank_shrink<4, W, PLAN>), grid, threads, 0, stream, a, plan);
+  else if constexpr (W == 4) hipLaunchKernelGGL((lowrank_shrink<8, W, PLAN>), grid, threads, 0, stream, a, plan);
+  return hipGetLastError();
+}
+
 template <bool PLAN>
 hipError_t launch_shrink(const ShrinkArgs& a, const PlanArgs& plan, int shares, hipStream_t stream) {
   const dim3 grid((unsigned)(a.side[0].slices + a.side[1].slices + PLAN), (unsigned)shares,
                   (unsigned)std::max<int64_t>(1, blocks_of(a.m)));
-  switch (rank_tiles(a.rank)) {
-    case 1: hipLaunchKernelGGL((lowrank_shrink<1, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
-    case 2: hipLaunchKernelGGL((lowrank_shrink<2, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
-    case 4: hipLaunchKernelGGL((lowrank_shrink<4, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
-    default: hipLaunchKernelGGL((lowrank_shrink<8, PLAN>), grid, dim3(kThreads), 0, stream, a, plan); break;
-  }
-  return hipGetLastError();
+  // eight waves a workgroup where registers allow: half the slices for the reader to add
+  return a.single || a.rank > 64 ? launch_shrink_of<4, PLAN>(a, plan, grid, stream)
+                                 : launch_shrink_of<8, PLAN>(a, plan, grid, stream);
 }
 
 template <int RS, bool SINGLE>
@@ -806,8 +822,8 @@ __global__ __launch_bounds__(kThreads) void lowrank_operands(OperandArgs a) {
 // The input's gradient and the operands of the adapters' own: workgroups x < columns expand,
 // the others make operands (a launch less).
 template <int RS, bool BF16, bool GRAD_BF16>
-__global__ __launch_bounds__(kThreads, (expand_waves<RS, false>())) void lowrank_expand_operands(ExpandArgs a, OperandArgs o,
-                                                                                               int columns) {
+__global__ __launch_bounds__(kThreads, (expand_waves<RS, BF16, false>())) void lowrank_expand_operands(
+    ExpandArgs a, OperandArgs o, int columns) {
   __shared__ ExpandShared<RS, BF16> s;
   if ((int)blockIdx.x < columns) {
     expand<RS, BF16, BF16, false>(a, s, blockIdx.x, 0, blockIdx.y);
