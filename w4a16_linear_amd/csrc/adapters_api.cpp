@@ -136,12 +136,35 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
 
 // ---------------------------------------------------------- projection's gradient
 
+namespace {
+
+// The workspace's parts: W' transposed ([k][ld]), dy with rows of ld where its own are
+// shorter, the product's split sums, and (codes of other widths) W' as it is dequantized.
+struct BackwardSpace {
+  int64_t ld;
+  size_t padded, part, plain, bytes;
+};
+BackwardSpace backward_space(int64_t m, int64_t n, int64_t k) {
+  BackwardSpace s;
+  s.ld = n % 32 ? (n + 63) / 64 * 64 : n;  // padded rows: whole steps of the product
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    at += (bytes + 255) & ~size_t(255);
+    return at;
+  };
+  s.padded = take((size_t)k * s.ld * 2);
+  s.part = take(n < s.ld ? (size_t)m * s.ld * 2 : 0);
+  s.plain = take(opq::linear_dense_part_bytes(m, k, s.ld));
+  s.bytes = take((size_t)n * k * 2);
+  return s;
+}
+
+}  // namespace
+
 size_t opq_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0 || k % 32 || m > kMaxTokens || n > kMaxLinear || k > kMaxLinear)
     return 0;
-  const size_t ld = (size_t)(n + 31) / 32 * 32;
-  // W', W' transposed (rows of ld), and dy with such rows where its own are shorter
-  return (size_t)n * k * 2 + (size_t)k * ld * 2 + ((size_t)n < ld ? (size_t)m * ld * 2 : 0);
+  return backward_space(m, n, k).bytes;
 }
 
 // The checks of one storage form; `more` its own about shapes and types.
@@ -164,20 +187,24 @@ static int backward_checks(const uint16_t* dy, const uint32_t* packed, const uin
   return OPQ_OK;
 }
 
-// W' is in the workspace's first n k elements.
+// The product, with W' transposed at the workspace's beginning (n > 0).
 static int backward_product(const uint16_t* dy, int64_t m, int64_t n, int64_t k, void* dx,
-                            int dx_dtype, void* workspace, hipStream_t st) {
-  const int64_t ld = (n + 31) / 32 * 32;
-  const uint16_t* w = static_cast<const uint16_t*>(workspace);
-  uint16_t* wt = static_cast<uint16_t*>(workspace) + n * k;
-  int e = n > 0 ? hip_status(opq::launch_transpose(w, n, k, wt, ld, st)) : OPQ_OK;
-  if (e == OPQ_OK && n < ld) {
-    uint16_t* padded = wt + k * ld;
-    e = hip_status(opq::launch_pad_rows(dy, m, n, padded, ld, st));
+                            int dx_dtype, char* ws, hipStream_t st) {
+  const BackwardSpace s = backward_space(m, n, k);
+  if (n < s.ld) {
+    uint16_t* padded = reinterpret_cast<uint16_t*>(ws + s.padded);
+    const int e = hip_status(opq::launch_pad_rows(dy, m, n, padded, s.ld, st));
+    if (e != OPQ_OK) return e;
     dy = padded;
   }
-  if (e != OPQ_OK) return e;
-  return hip_status(opq::launch_linear_dense(dy, wt, nullptr, m, k, ld, dx, dx_dtype == OPQ_BF16, st));
+  float* part = s.plain > s.part ? reinterpret_cast<float*>(ws + s.part) : nullptr;
+  return hip_status(opq::launch_linear_dense(dy, reinterpret_cast<const uint16_t*>(ws), nullptr, m, k, s.ld, dx,
+                                             dx_dtype == OPQ_BF16, part, st));
+}
+
+// No rows of weights: sums of nothing.
+static int no_rows(int64_t m, int64_t k, void* dx, int dx_dtype, hipStream_t st) {
+  return hip_status(opq::launch_linear_dense(nullptr, nullptr, nullptr, m, k, 0, dx, dx_dtype == OPQ_BF16, nullptr, st));
 }
 
 int opq_linear_backward(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
@@ -186,9 +213,15 @@ int opq_linear_backward(const uint16_t* dy, const uint32_t* packed, const uint32
   int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, true, dx, dx_dtype, workspace,
                           workspace_bytes);
   if (e != OPQ_OK || m == 0 || k == 0) return e;
-  e = opq_dequantize(packed, sign, scale, n, k, alpha, static_cast<uint16_t*>(workspace), stream);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n == 0) return no_rows(m, k, dx, dx_dtype, st);
+  opq::Levels lv;
+  opq::levels(alpha, lv.g);
+  e = hip_status(opq::launch_dequantize_transposed(packed, sign, scale, nullptr, n, k, 0, lv,
+                                                   static_cast<uint16_t*>(workspace),
+                                                   backward_space(m, n, k).ld, st));
   if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, workspace, static_cast<hipStream_t>(stream));
+  return backward_product(dy, m, n, k, dx, dx_dtype, static_cast<char*>(workspace), st);
 }
 
 int opq_linear_backward_bits(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
@@ -198,10 +231,19 @@ int opq_linear_backward_bits(const uint16_t* dy, const uint32_t* packed, const u
   int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, bits >= 3 && bits <= 6, dx,
                           dx_dtype, workspace, workspace_bytes);
   if (e != OPQ_OK || m == 0 || k == 0) return e;
-  e = opq_dequantize_bits(packed, sign, scale, n, k, bits, alpha, static_cast<uint16_t*>(workspace),
-                          stream);
+  if (bits == 4)
+    return opq_linear_backward(dy, packed, sign, scale, m, n, k, alpha, dx, dx_dtype, workspace,
+                               workspace_bytes, stream);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n == 0) return no_rows(m, k, dx, dx_dtype, st);
+  char* ws = static_cast<char*>(workspace);
+  const BackwardSpace s = backward_space(m, n, k);
+  uint16_t* w = reinterpret_cast<uint16_t*>(ws + s.plain);
+  e = opq_dequantize_bits(packed, sign, scale, n, k, bits, alpha, w, stream);
   if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, workspace, static_cast<hipStream_t>(stream));
+  e = hip_status(opq::launch_transpose(w, n, k, reinterpret_cast<uint16_t*>(ws), s.ld, st));
+  if (e != OPQ_OK) return e;
+  return backward_product(dy, m, n, k, dx, dx_dtype, ws, st);
 }
 
 int opq_linear_backward_grouped(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
@@ -212,10 +254,18 @@ int opq_linear_backward_grouped(const uint16_t* dy, const uint32_t* packed, cons
   int e = backward_checks(dy, packed, sign, scale16, m, n, k, alpha, group_ok, dx, dx_dtype,
                           workspace, workspace_bytes);
   if (e != OPQ_OK || m == 0 || k == 0) return e;
-  e = opq_dequantize_grouped(packed, sign, scale16, n, k, group, alpha,
-                             static_cast<uint16_t*>(workspace), stream);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n == 0) return no_rows(m, k, dx, dx_dtype, st);
+  opq::DecisionPoints dp;
+  if (!opq::decision_points(alpha, dp.t)) return OPQ_ERR_ALPHA;
+  opq::Levels lv;
+  opq::levels(alpha, lv.g);
+  if (!opq::grouped_supported(dp, lv)) return OPQ_ERR_UNSUPPORTED;
+  e = hip_status(opq::launch_dequantize_transposed(packed, sign, nullptr, scale16, n, k, (int)group, lv,
+                                                   static_cast<uint16_t*>(workspace),
+                                                   backward_space(m, n, k).ld, st));
   if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, workspace, static_cast<hipStream_t>(stream));
+  return backward_product(dy, m, n, k, dx, dx_dtype, static_cast<char*>(workspace), st);
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "opq_adapters.h"
+#include "opq_internal.hpp"
 
 namespace opq {
 
@@ -49,7 +50,12 @@ struct LowrankBackward {
 size_t lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank, int64_t count);
 hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream);
 
-// linear_backward.hip: dst [k][ld] = the transpose of w [n][k] (bfloat16), columns n..ld-1 zero
+// linear_backward.hip: dst [k][ld] = W' (bfloat16) transposed, columns n..ld-1 zero, from 4-bit
+// codes with one max a row (gs 0: scale) or a group (scale16)
+hipError_t launch_dequantize_transposed(const uint32_t* packed, const uint32_t* sign, const float* scale,
+                                        const uint16_t* scale16, int64_t n, int64_t k, int gs, const Levels& lv,
+                                        uint16_t* dst, int64_t ld, hipStream_t stream);
+// dst [k][ld] = the transpose of w [n][k] (bfloat16), columns n..ld-1 zero
 hipError_t launch_transpose(const uint16_t* w, int64_t n, int64_t k, uint16_t* dst, int64_t ld,
                             hipStream_t stream);
 // dst [m][ld] = src [m][n], columns n..ld-1 zero

@@ -737,11 +737,13 @@ __global__ __launch_bounds__(kTThreads, 1) void linear_tiled(
 // Tiled (m > 64): linear_tiled's tile, waves and fragments, with W' staged like
 // x (256 rows x 64 k per stage, same swizzle, buffer loads straight to LDS),
 // two stages of each.  A wave's B fragment is one ds_read_b128 per sub-step.
+// kSplit as in linear_tiled: slices of the k steps, their float32 sums in planes of `part`.
 
-template <bool kHalfTail>
+template <bool kHalfTail, bool kSplit = false>
 __global__ __launch_bounds__(kTThreads, 1) void linear_dense_tiled(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ wd, const float* __restrict__ bias,
-    int m, int n, int k, int tiles_m, void* __restrict__ y, int y_bf16) {
+    int m, int n, int k, int tiles_m, void* __restrict__ y, int y_bf16, int slice_steps,
+    float* __restrict__ part) {
   __shared__ __attribute__((aligned(1024))) uint8_t s_x0[kXStageBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t s_x1[kXStageBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t s_w0[kXStageBytes];
@@ -750,12 +752,17 @@ __global__ __launch_bounds__(kTThreads, 1) void linear_dense_tiled(
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int tile_m = blockIdx.x % tiles_m, tile_n = blockIdx.x / tiles_m;
+  const int tiles = kSplit ? tiles_m * ((n + kTN - 1) / kTN) : 0;
+  const int tile = kSplit ? blockIdx.x % tiles : blockIdx.x;
+  const int slice = kSplit ? blockIdx.x / tiles : 0;
+  const int tile_m = tile % tiles_m, tile_n = tile / tiles_m;
   const int m0 = tile_m * kTM;
   const int n0 = tile_n * kTN;
   const int h = lane >> 5;
   const int brow = n0 + wave * 32 + (lane & 31);
   const int nsteps = (k + kTK - 1) / kTK;
+  const int first = kSplit ? slice * slice_steps : 0;
+  const int last = kSplit ? min(nsteps, first + slice_steps) : nsteps;
 
   // both operands: load i of wave w fills 1 KB block 4w + i of a stage (rows
   // 8(4w + i) + l/8, chunk slot l%8), as in linear_tiled
@@ -807,14 +814,14 @@ __global__ __launch_bounds__(kTThreads, 1) void linear_dense_tiled(
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
   bf16x8_t a_frag[8], b_buf[2];
-  if (nsteps > 0) {
-    load(0, s_x0, s_w0);
+  if (last > first) {
+    load(first, s_x0, s_w0);
     wait_vm<0>();
     lds_barrier_dma();
     read_a(s_x0, 0, a_frag);
-    read_b(s_w0, 0, 0, b_buf[0]);
+    read_b(s_w0, first, 0, b_buf[0]);
   }
-  // step kt: stage kt & 1; the loads of step kt + 1 go to the other stage, which
+  // step kt: stage (kt - first) & 1; the loads of step kt + 1 go to the other stage, which
   // served step kt - 1, and are waited for before this step's barrier
   auto step = [&](int kt, auto par) __attribute__((always_inline)) {
     constexpr int p = decltype(par)::value;
@@ -847,14 +854,19 @@ __global__ __launch_bounds__(kTThreads, 1) void linear_dense_tiled(
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  int kt = 0;
-  for (; kt + 1 < nsteps; kt += 2) {
+  int kt = first;
+  for (; kt + 1 < last; kt += 2) {
     step(kt, StepPos<0>{});
     step(kt + 1, StepPos<1>{});
   }
-  if (kt < nsteps) step(kt, StepPos<0>{});
+  if (kt < last) step(kt, StepPos<0>{});
   wait_vm<0>();  // no load may still be writing LDS when the block ends
 
+  if constexpr (kSplit) {
+    y = part + (int64_t)slice * m * n;
+    y_bf16 = 0;
+    bias = nullptr;
+  }
   const float bv = (bias && brow < n) ? bias[brow] : 0.0f;
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi)
@@ -1097,17 +1109,22 @@ size_t linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return ((size_t)split * (size_t)m * (size_t)n * 4u + 255u) & ~size_t(255);
 }
 
+size_t linear_dense_part_bytes(int64_t m, int64_t n, int64_t k) {
+  return linear_workspace_bytes(m, n, k);  // the same tiles, steps and slices
+}
+
 hipError_t launch_linear_dense(const uint16_t* x, const uint16_t* wd, const float* bias, int64_t m,
-                              int64_t n, int64_t k, void* y, bool y_bf16, hipStream_t stream) {
+                              int64_t n, int64_t k, void* y, bool y_bf16, float* part,
+                              hipStream_t stream) {
   // mid-size m as 64-row slices when cheaper, as for the on-chip decoder (the
   // same cost model holds: W' streams at a similar rate, mostly from the
   // Infinity Cache after the first slice)
-  if (mid_m_as_slices(m, n, k)) {
+  if (mid_m_as_slices(m, n, k, part != nullptr)) {
     const int64_t ybytes = y_bf16 ? 2 : 4;
     for (int64_t r = 0; r < m; r += kSkinnyMaxM) {
       const int64_t mm = m - r < kSkinnyMaxM ? m - r : kSkinnyMaxM;
       const hipError_t e = launch_linear_dense(x + r * k, wd, bias, mm, n, k,
-                                               static_cast<char*>(y) + r * n * ybytes, y_bf16, stream);
+                                               static_cast<char*>(y) + r * n * ybytes, y_bf16, part, stream);
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -1120,9 +1137,21 @@ hipError_t launch_linear_dense(const uint16_t* x, const uint16_t* wd, const floa
                        (int)k, y, (int)y_bf16);
   } else {
     const int64_t tiles_m = (m + kTM - 1) / kTM, tiles_n = (n + kTN - 1) / kTN;
+    int sps = 0;
+    const int split = part ? tiled_split(m, n, k, &sps) : 1;
+    if (split > 1) {
+      hipLaunchKernelGGL((linear_dense_tiled<false, true>), dim3((unsigned)(tiles_m * tiles_n * split)),
+                         dim3(kTThreads), 0, stream, x, wd, bias, (int)m, (int)n, (int)k, (int)tiles_m, y,
+                         (int)y_bf16, sps, part);
+      const int64_t count = m * n;
+      const int64_t rb = std::min<int64_t>((count + 255) / 256, 8192);
+      hipLaunchKernelGGL(linear_split_reduce, dim3((unsigned)rb), dim3(256), 0, stream, part, split,
+                         count, (int)n, bias, y, (int)y_bf16);
+      return hipGetLastError();
+    }
     auto kernel = (k % kTK) ? linear_dense_tiled<true> : linear_dense_tiled<false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n)), dim3(kTThreads), 0, stream, x, wd,
-                       bias, (int)m, (int)n, (int)k, (int)tiles_m, y, (int)y_bf16);
+                       bias, (int)m, (int)n, (int)k, (int)tiles_m, y, (int)y_bf16, 0, nullptr);
   }
   return hipGetLastError();
 }

@@ -518,11 +518,12 @@ struct ExpandShared {
 // for the four waves.  Of lane (c, q) = (l % 16, l / 16) the stack's block is rank rows
 // 32 s + 8 q ..., columns 8 pi(c) ... with pi(4 i + j) = 4 j + i: the accumulators of a
 // lane are then, for i = 0..3, the eight columns 8 (4 i + q) ..., so that in a load or
-// store of 16 bytes a token's four lanes touch 64 bytes in a row.  What a tile adds to is
-// requested a tile ahead, the first with the stack's block before the operands are made.
+// store of 16 bytes a token's four lanes touch 64 bytes in a row.  What the tiles add to is
+// requested with the stack's block before the operands are made.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
 __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT_BF16>& s, int bx, int by, int bz) {
   constexpr int PARTS = OUT_BF16 ? 2 : 3;
+  constexpr int kAhead = SINGLE ? 1 : RS > 1 && BASE_BF16 ? 4 : 2;  // by registers
   const int64_t t0 = (int64_t)bz * kBlockTokens;
   const int id = block_id(a.index + t0, (int)min((int64_t)kBlockTokens, a.m - t0), a.count);
   const int lane = threadIdx.x & (kWave - 1);
@@ -574,21 +575,29 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
   };
 
   while (lead) {
-    // the next tiles: this wave's to make, and where each begins
-    uint64_t rest = lead;
+    // the next tiles, and what they add to, as far ahead as registers allow
+    Tile t[kMade];
     int made = 0, own = -1;
 #pragma unroll
     for (int w = 0; w < kMade; ++w)
-      if (rest) {
-        if (w == wave) own = first_of(rest);
-        rest &= rest - 1;
+      if (lead) {
+        const int at = first_of(lead);
+        if (w == wave) own = at;
+        t[w] = tile_of<16>(id, at);
+        lead &= lead - 1;
         ++made;
+      } else {
+        t[w] = Tile{kNoToken, 0, 0};
       }
-    Tile t = tile_of<16>(id, first_of(lead));
-    Base<BASE_BF16> base{}, ahead{};
+    if (SINGLE) lead = 0;
+    Base<BASE_BF16> base[kAhead] = {};
     if (n0 < a.d) {
-      if (a.base) load_base(t, base);
-      load_p(t.id);
+      if (a.base) {
+#pragma unroll
+        for (int w = 0; w < kAhead; ++w)
+          if (w < made) load_base(t[w], base[w]);
+      }
+      load_p(t[0].id);
     }
     if (own >= 0) {
       const Tile o = tile_of<16>(id, own);
@@ -610,47 +619,41 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
       }
     }
     lds_barrier();
-    for (int w = 0; w < made; ++w) {
-      lead &= lead - 1;
-      Tile next = t;
-      if (!SINGLE && w + 1 < made) {
-        next = tile_of<16>(id, first_of(lead));
-        if (n0 < a.d && a.base) load_base(next, ahead);
-      }
-      if (n0 < a.d) {
-        if (!SINGLE) load_p(t.id);
-        floatx4_t acc[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-        if (t.id >= 0) {
+    for (int w = 0; w < kMade; ++w) {
+      if (w >= made || n0 >= a.d) break;
+      const int who = t[w].id;
+      if (w > 0) load_p(who);
+      floatx4_t acc[8];
 #pragma unroll
-          for (int k = 0; k < RS; ++k)
+      for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+      if (who >= 0) {
 #pragma unroll
-            for (int e = 0; e < PARTS; ++e) {
-              const bf16x8_t h = operand(s.c[w][k][e][lane]);
+        for (int k = 0; k < RS; ++k)
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(p[k][j]), h, acc[j], 0, 0, 0);
-            }
-        }
-        const int64_t token = t0 + __shfl(t.token, c, kWave);
-        if (c < t.size) {
+          for (int e = 0; e < PARTS; ++e) {
+            const bf16x8_t h = operand(s.c[w][k][e][lane]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = n0 + (i * 4 + q) * 8;
-            float v[8] = {};
-            if (a.base) unpack<BASE_BF16>(base, i, v);
-            if (t.id >= 0) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
-            }
-            if (n < a.d) store8<OUT_BF16>(a.out, token * a.out_stride + n, v);
+            for (int j = 0; j < 8; ++j)
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(p[k][j]), h, acc[j], 0, 0, 0);
           }
+      }
+      const int64_t token = t0 + __shfl(t[w].token, c, kWave);
+      if (c < t[w].size) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + (i * 4 + q) * 8;
+          float v[8] = {};
+          if (a.base) unpack<BASE_BF16>(base[w % kAhead], i, v);
+          if (who >= 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
+          }
+          if (n < a.d) store8<OUT_BF16>(a.out, token * a.out_stride + n, v);
         }
       }
       if (SINGLE) return;
-      t = next;
-      base = ahead;
+      if (w + kAhead < kMade && w + kAhead < made && a.base) load_base(t[w + kAhead], base[w % kAhead]);
     }
     if (lead) lds_barrier();  // the operands are made anew
   }
@@ -681,14 +684,18 @@ struct ShrinkPlan {
   int slices, shares;
 };
 
-// About 512 workgroups, as long as a wave has a step of its own.  Shares of a block's tiles:
-// two, for the blocks in which one adapter's run ends and another's begins.
-ShrinkPlan shrink_plan(int64_t m, int64_t d) {
+// About `groups` workgroups, as long as a wave has a step of its own.  Shares of a block's
+// tiles: two, for the blocks in which one adapter's run ends and another's begins.  Forward
+// 256: x was made a moment ago and is in cache, and every workgroup of the expand adds
+// the slices (4096 tokens, 3840 -> 20480, rank 64: 120 us, with 512 124).  Backward 512: dy
+// comes from memory (one adapter, 3840 -> 11520, rank 16: 102 us, with 256 138).
+constexpr int kForwardGroups = 256, kBackwardGroups = 512;
+ShrinkPlan shrink_plan(int64_t m, int64_t d, int64_t groups_wanted) {
   ShrinkPlan p;
   m = std::max<int64_t>(m, 1);
   p.shares = (int)(single_block(m) ? m : 2);
   const int64_t steps = (d + 31) / 32, groups = blocks_of(m) * p.shares;
-  const int64_t want = (512 + groups - 1) / groups;
+  const int64_t want = (groups_wanted + groups - 1) / groups;
   p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({want, (steps + 3) / 4, 16}));
   const int64_t per = (steps + p.slices - 1) / p.slices;
   p.slices = (int)((steps + per - 1) / per);  // none without steps
@@ -745,11 +752,11 @@ hipError_t launch_expand(const ExpandArgs& a, bool base_bf16, bool out_bf16, hip
 
 size_t lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank) {
   (void)n;
-  return up256((size_t)shrink_plan(m, k).slices * (size_t)m * (size_t)rank * 4u);
+  return up256((size_t)shrink_plan(m, k, kForwardGroups).slices * (size_t)m * (size_t)rank * 4u);
 }
 
 hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream) {
-  const ShrinkPlan plan = shrink_plan(c.m, c.a.k);
+  const ShrinkPlan plan = shrink_plan(c.m, c.a.k, kForwardGroups);
   ShrinkArgs s{};
   s.side[0] = {c.a.down, c.x, c.x_stride, static_cast<float*>(c.workspace), (int)c.a.k, plan.slices};
   s.index = c.index;
@@ -950,8 +957,8 @@ struct BackwardPlan {
 
 BackwardPlan backward_plan(int64_t m, int64_t k, int64_t n, int64_t rank, int64_t count) {
   BackwardPlan b{};
-  b.h = shrink_plan(m, k);
-  b.e = shrink_plan(m, n);
+  b.h = shrink_plan(m, k, kBackwardGroups);
+  b.e = shrink_plan(m, n, kBackwardGroups);
   // about 2048 waves in grad, each of at least 32 tokens
   const int64_t columns = (k + 127) / 128 + (n + 127) / 128;
   const int64_t seg = (m * columns / 2048 + 31) / 32 * 32;

@@ -286,7 +286,7 @@ int opq_linear_bits(const uint16_t* x, const uint32_t* packed, const uint32_t* s
         hip_status(opq::launch_dequantize_bits(packed, sign, scale, n, k, bits, lv, wd, false, st));
     if (e != OPQ_OK) return e;
   }
-  return hip_status(opq::launch_linear_dense(x, wd, bias, m, n, k, y, y_dtype == OPQ_BF16, st));
+  return hip_status(opq::launch_linear_dense(x, wd, bias, m, n, k, y, y_dtype == OPQ_BF16, nullptr, st));
 }
 
 int opq_linear_bits_noalloc(const uint16_t* x, const uint32_t* packed, const uint32_t* sign,

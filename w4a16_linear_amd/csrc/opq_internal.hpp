@@ -69,9 +69,12 @@ hipError_t launch_linear(const uint16_t* x, const uint32_t* packed, const uint32
 constexpr size_t kNoAllocScratchBytes = size_t(160) << 20;
 void* noalloc_scratch();
 
-// linear.hip: y = x W'^T (+ bias) with W' bfloat16 [n][k] in device memory
+// linear.hip: y = x W'^T (+ bias) with W' bfloat16 [n][k] in device memory.  part: nullptr, or
+// linear_dense_part_bytes(m, n, k) bytes: products of few tiles then split k
+size_t linear_dense_part_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_linear_dense(const uint16_t* x, const uint16_t* wd, const float* bias, int64_t m,
-                               int64_t n, int64_t k, void* y, bool y_bf16, hipStream_t stream);
+                               int64_t n, int64_t k, void* y, bool y_bf16, float* part,
+                               hipStream_t stream);
 
 // b-bit codes (3..6), codes of a row as a little-endian bit stream along k.
 // quantize.hip
