@@ -102,6 +102,17 @@ __device__ __forceinline__ bf16x8_t operand(uint4 v) { return __builtin_bit_cast
 __device__ __forceinline__ uint4 zero16() { return make_uint4(0u, 0u, 0u, 0u); }
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
+// Rows are loaded as memory wants them: lane l has chunk l % 4 (16 bytes) of row l / 4, four lanes
+// 64 bytes in a row.  (The matrix operands' own order, rows in neighbouring lanes, makes
+// every lane an access of its own: 64 a load, which bound these kernels at a quarter of
+// L1's rate.)  This moves them to the operands' order: lane (c, q) gets chunk q of row c.
+__device__ __forceinline__ uint4 to_operand(uint4 v) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int from = ((lane & 15) * 4 + (lane >> 4)) * 4;
+  return make_uint4((uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.x), (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.y),
+                    (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.z), (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.w));
+}
+
 // Eight rows of eight columns -> the eight columns, each of eight rows.
 __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
 #pragma unroll
@@ -344,6 +355,7 @@ __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanAr
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, q = lane >> 4;
+  const int lr = lane >> 2, lc = lane & 3;  // row and 16-byte chunk of a load
   uint64_t lead;
   if (a.single) {
     if (__builtin_amdgcn_readlane(id, blockIdx.y) < 0 || !leads<kTile>(id, blockIdx.y)) return;
@@ -364,11 +376,11 @@ __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanAr
     const uint16_t* p = g.p + (int64_t)tile.id * a.rank * g.d;
     uint32_t row[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) row[i] = (uint32_t)min(i * 16 + c, a.rank - 1) * (uint32_t)g.d;
+    for (int i = 0; i < RT; ++i) row[i] = (uint32_t)min(i * 16 + lr, a.rank - 1) * (uint32_t)g.d;
     const uint16_t* v[kParts];
 #pragma unroll
     for (int h = 0; h < kParts; ++h)
-      v[h] = g.v + (t0 + __shfl(tile.token, min(h * 16 + c, tile.size - 1), kWave)) * g.stride;
+      v[h] = g.v + (t0 + __shfl(tile.token, min(h * 16 + lr, tile.size - 1), kWave)) * g.stride;
     floatx4_t acc[kParts][RT];
 #pragma unroll
     for (int h = 0; h < kParts; ++h)
@@ -383,7 +395,7 @@ __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanAr
         uint4 vv[D][H], pp[D][RT];
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-          const int e = (at + u) * 32 + q * 8;
+          const int e = (at + u) * 32 + lc * 8;
           const bool in = full || e < g.d;  // d is a multiple of 8
           const int col = in ? e : 0;       // past d the row's first columns are read, and dropped
 #pragma unroll
@@ -398,13 +410,18 @@ __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanAr
           }
         }
 #pragma unroll
-        for (int u = 0; u < D; ++u)
+        for (int u = 0; u < D; ++u) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) vv[u][h] = to_operand(vv[u][h]);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) pp[u][i] = to_operand(pp[u][i]);
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int i = 0; i < RT; ++i)
               acc[h][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(pp[u][i]), operand(vv[u][h]),
                                                                   acc[h][i], 0, 0, 0);
+        }
       };
       const int stop = min(end, whole);
       int at = begin + wave * run;
@@ -483,7 +500,7 @@ __device__ __forceinline__ void scaled(const float* part, int64_t plane, int sli
   for (int e = 0; e < 8; ++e) v[e] *= by;
 }
 
-// What a lane adds to of one tile: eight columns in each of four places, as they are stored.
+// What a lane adds to of one tile: eight columns of four tokens, as they are stored.
 template <bool BF16> struct Base { uint4 v[BF16 ? 4 : 8]; };
 
 template <bool BF16>
@@ -515,11 +532,11 @@ struct ExpandShared {
 
 // Workgroup (512 columns, share of the block's tiles, block of tokens), a wave
 // 128 columns.  The tiles' operands (s c, in parts) are made once in LDS, a tile a wave,
-// for the four waves.  Of lane (c, q) = (l % 16, l / 16) the stack's block is rank rows
-// 32 s + 8 q ..., columns 8 pi(c) ... with pi(4 i + j) = 4 j + i: the accumulators of a
-// lane are then, for i = 0..3, the eight columns 8 (4 i + q) ..., so that in a load or
-// store of 16 bytes a token's four lanes touch 64 bytes in a row.  What the tiles add to is
-// requested with the stack's block before the operands are made.
+// for the four waves.  Lane (c, q) = (l % 16, l / 16) loads rank rows 32 s + 8 q ... of
+// columns 8 c ..., which after the transposition are the product's j-th columns 8 c + j;
+// tokens are its rows, so a lane's accumulators are eight columns in a row of four tokens,
+// and in every load and store sixteen lanes touch 256 bytes in a row.  What the tiles add
+// to is requested with the stack's block before the operands are made.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
 __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT_BF16>& s, int bx, int by, int bz) {
   constexpr int PARTS = OUT_BF16 ? 2 : 3;
@@ -538,7 +555,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
     lead = leaders<16>(id, lowest);
   }
   const int n0 = bx * 512 + wave * 128;
-  const int mine = n0 + ((c & 3) * 4 + (c >> 2)) * 8;  // first column of the lane's block
+  const int mine = n0 + c * 8;  // the lane's first column
   const int64_t plane = a.m * a.rank;
   uint4 p[RS][8];
   int held = kNoToken;  // adapter in p
@@ -557,19 +574,18 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
       transpose8(rows, p[k]);
     }
   };
-  // places past d or the tile read the first place of its last token
+  // places past d or the tile read the first place of a token of it
   auto load_base = [&](const Tile& t, Base<BASE_BF16>& b) __attribute__((always_inline)) {
-    const int64_t token = t0 + __shfl(t.token, min(c, t.size - 1), kWave);
-    const char* from = static_cast<const char*>(a.base) + token * a.base_stride * (BASE_BF16 ? 2 : 4);
+    const int n = mine < a.d ? mine : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      int n = n0 + (i * 4 + q) * 8;
-      n = n < a.d ? n : 0;
+      const int64_t token = t0 + __shfl(t.token, min(q * 4 + i, t.size - 1), kWave);
+      const char* from = static_cast<const char*>(a.base) + (token * a.base_stride + n) * (BASE_BF16 ? 2 : 4);
       if constexpr (BASE_BF16) {
-        b.v[i] = *reinterpret_cast<const uint4*>(from + (int64_t)n * 2);
+        b.v[i] = *reinterpret_cast<const uint4*>(from);
       } else {
-        b.v[2 * i] = *reinterpret_cast<const uint4*>(from + (int64_t)n * 4);
-        b.v[2 * i + 1] = *reinterpret_cast<const uint4*>(from + (int64_t)n * 4 + 16);
+        b.v[2 * i] = *reinterpret_cast<const uint4*>(from);
+        b.v[2 * i + 1] = *reinterpret_cast<const uint4*>(from + 16);
       }
     }
   };
@@ -635,22 +651,19 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
             const bf16x8_t h = operand(s.c[w][k][e][lane]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(p[k][j]), h, acc[j], 0, 0, 0);
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, operand(p[k][j]), acc[j], 0, 0, 0);
           }
       }
-      const int64_t token = t0 + __shfl(t[w].token, c, kWave);
-      if (c < t[w].size) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = n0 + (i * 4 + q) * 8;
-          float v[8] = {};
-          if (a.base) unpack<BASE_BF16>(base[w % kAhead], i, v);
-          if (who >= 0) {
+      for (int i = 0; i < 4; ++i) {
+        const int64_t token = t0 + __shfl(t[w].token, q * 4 + i, kWave);
+        float v[8] = {};
+        if (a.base) unpack<BASE_BF16>(base[w % kAhead], i, v);
+        if (who >= 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
-          }
-          if (n < a.d) store8<OUT_BF16>(a.out, token * a.out_stride + n, v);
+          for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
         }
+        if (q * 4 + i < t[w].size && mine < a.d) store8<OUT_BF16>(a.out, token * a.out_stride + mine, v);
       }
       if (SINGLE) return;
       if (w + kAhead < kMade && w + kAhead < made && a.base) load_base(t[w + kAhead], base[w % kAhead]);
@@ -787,19 +800,26 @@ hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream) {
 
 namespace {
 
+// Element of part k, rank r, place j among grad's operands.
+__device__ __forceinline__ int64_t operand_at(int rank, int64_t cap, int k, int r, int64_t j) {
+  const int tiles = (rank + 15) / 16;
+  return (((k * tiles + r / 16) * (cap / 32) + j / 32) * kWave + j % 32 / 8 * 16 + r % 16) * 8 + j % 8;
+}
+
 struct OperandArgs {
   GradPlan g;
   const float* part[2];  // [slices][m][rank]
   int slices[2];
-  uint16_t* out[2];      // [parts][rank][cap]
+  uint16_t* out[2];      // [parts][16-row tiles of the rank][cap / 32][64 lanes][8]
   const float* scale;
   const int32_t* index;
   int64_t m, cap;
   int rank;
 };
 
-// s c in bfloat16 parts, transposed: what the rows of grad's products read along the
-// tokens.  A thread makes eight ranks of one place; `group`: 256 places of eight ranks and a side.
+// s c in bfloat16 parts, transposed, in the order of grad's operands: of 32 places and 16
+// ranks, lane (c, q) has rank c, places 8 q ..., and its 16 bytes lie beside its neighbours'.
+// A thread makes eight ranks of one place; `group`: 256 places of eight ranks and a side.
 template <int PARTS>
 __device__ __forceinline__ void operands(const OperandArgs& a, int64_t group) {
   const int64_t groups = (a.cap + kThreads - 1) / kThreads;
@@ -816,8 +836,7 @@ __device__ __forceinline__ void operands(const OperandArgs& a, int64_t group) {
     uint32_t cut[PARTS];
     split<PARTS>(v[e], cut);
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k)
-      a.out[side][((int64_t)k * a.rank + r + e) * a.cap + j] = (uint16_t)cut[k];
+    for (int k = 0; k < PARTS; ++k) a.out[side][operand_at(a.rank, a.cap, k, r + e, j)] = (uint16_t)cut[k];
   }
 }
 
@@ -841,7 +860,7 @@ __global__ __launch_bounds__(kThreads, (expand_waves<RS, BF16, false>())) void l
 
 struct GradSide {
   const uint16_t* v;  // [m][stride]
-  const uint16_t* c;  // [parts][rank][cap]
+  const uint16_t* c;  // the operands
   int64_t stride;
   float* part;        // [slots][rank][d]
   void* out;          // [count][rank][d]
@@ -873,9 +892,12 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
   const int n = n0 + c * 8, r0 = blockIdx.z * 64;
   const int from = a.g.from[item], length = a.g.length[item];
   const uint16_t* v = g.v + (n < g.d ? n : 0);
-  const uint16_t* row[RT];
+  const int tiles = (a.rank + 15) / 16;
+  const int64_t plane = (int64_t)tiles * a.cap * 16;  // elements of a part
+  const uint16_t* row[RT];  // a tile past the rank reads the last one, and is dropped
 #pragma unroll
-  for (int i = 0; i < RT; ++i) row[i] = g.c + (int64_t)min(r0 + i * 16 + c, a.rank - 1) * a.cap + from + q * 8;
+  for (int i = 0; i < RT; ++i)
+    row[i] = g.c + ((int64_t)min(r0 / 16 + i, tiles - 1) * a.cap + from) * 16 + lane * 8;
   floatx4_t acc[RT][8];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -892,7 +914,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) h[i][k] = operand(load16(row[i] + (int64_t)k * a.rank * a.cap + at));
+      for (int k = 0; k < PARTS; ++k) h[i][k] = operand(load16(row[i] + k * plane + at * 16));
     transpose8(rows, cols);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -976,8 +998,9 @@ BackwardPlan backward_plan(int64_t m, int64_t k, int64_t n, int64_t rank, int64_
   };
   b.part_h = take((size_t)b.h.slices * m * rank * 4);
   b.part_e = take((size_t)b.e.slices * m * rank * 4);
-  b.operand_h = take((size_t)3 * rank * b.cap * 2);
-  b.operand_e = take((size_t)3 * rank * b.cap * 2);
+  const size_t ranks = (size_t)(rank + 15) / 16 * 16;  // whole tiles
+  b.operand_h = take(3 * ranks * b.cap * 2);
+  b.operand_e = take(3 * ranks * b.cap * 2);
   b.sums_down = take((size_t)b.slots * rank * k * 4);
   b.sums_up = take((size_t)b.slots * rank * n * 4);
   b.lists = take((size_t)(b.cap + 64 + 4 * b.items + 2 * count) * 4);
