@@ -329,6 +329,10 @@ struct ShrinkArgs {
   bool single;  // workgroup y takes the tile that token y leads, if it leads one
 };
 
+// Tokens of a shrink's tile.  Each tile reads the adapter's rows, mostly from L2: past rank 32
+// that costs more than the fewer workgroups of larger tiles do.
+constexpr int shrink_tile(int64_t rank) { return rank > 32 ? kBlockTokens : kBlockTokens / 2; }
+
 // Workgroup (slice of d, share of the block's tiles, block of tokens).  A wave
 // takes a quarter of the slice's 32-wide steps for a tile, all tokens of the block that use
 // one adapter, and all rank rows; the waves' sums meet in LDS, the slices' in the
@@ -339,7 +343,7 @@ struct ShrinkArgs {
 template <int RT, int W, bool PLAN>
 __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanArgs plan) {
   constexpr int kWaves = W;
-  constexpr int kTile = kBlockTokens, kParts = kTile / 16;
+  constexpr int kTile = shrink_tile(RT * 16), kParts = kTile / 16;
   constexpr int kDepth = RT >= 8 ? 1 : RT >= 4 ? 2 : 4;  // steps whose loads are out together
   constexpr int kSums = kWaves * RT * 2 * 4 * kWave;
   __shared__ float s_red[PLAN && kSums * 4 < plan_bytes<W>() ? plan_bytes<W>() / 4 : kSums];
@@ -434,7 +438,7 @@ __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanAr
         }
       }
     };
-    if (tile.size > 32) walk(std::integral_constant<int, 4>{});
+    if (kParts > 2 && tile.size > 32) walk(std::integral_constant<int, kParts>{});
     else if (tile.size > 16) walk(std::integral_constant<int, 2>{});
     else walk(std::integral_constant<int, 1>{});
 
@@ -697,17 +701,20 @@ struct ShrinkPlan {
   int slices, shares;
 };
 
-// About `groups` workgroups, as long as a wave has a step of its own.  Shares of a block's
-// tiles: two, for the blocks in which one adapter's run ends and another's begins.  Forward
-// 256: x was made a moment ago and is in cache, and every workgroup of the expand adds
-// the slices (4096 tokens, 3840 -> 20480, rank 64: 120 us, with 512 124).  Backward 512: dy
-// comes from memory (one adapter, 3840 -> 11520, rank 16: 102 us, with 256 138).
-constexpr int kForwardGroups = 256, kBackwardGroups = 512;
-ShrinkPlan shrink_plan(int64_t m, int64_t d, int64_t groups_wanted) {
+// About `groups_wanted` workgroups, as long as a wave has a step of its own.  Shares of a block's
+// tiles: two, for its two tiles or for the block in which one adapter's run ends and another's
+// begins.  Backward 512: dy comes from memory (8192 tokens of 10240, rank 64: 144 us, with 256
+// 237).  Forward 256, x was made a moment ago and is in cache; 128 past rank 32, where every
+// workgroup of the expand adds as many slices of longer rows (4096 tokens, 3840 -> 20480,
+// rank 64: 111 us, with 256 119; 2047 tokens, 10240 -> 3840, rank 32: 40, with 256 31).
+constexpr int kBackwardGroups = 512;
+constexpr int forward_groups(int64_t rank) { return rank > 32 ? 128 : 256; }
+ShrinkPlan shrink_plan(int64_t m, int64_t d, int64_t rank, int64_t groups_wanted) {
   ShrinkPlan p;
   m = std::max<int64_t>(m, 1);
   p.shares = (int)(single_block(m) ? m : 2);
-  const int64_t steps = (d + 31) / 32, groups = blocks_of(m) * p.shares;
+  const int64_t steps = (d + 31) / 32;
+  const int64_t groups = single_block(m) ? m : blocks_of(m) * (kBlockTokens / shrink_tile(rank));
   const int64_t want = (groups_wanted + groups - 1) / groups;
   p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({want, (steps + 3) / 4, 16}));
   const int64_t per = (steps + p.slices - 1) / p.slices;
@@ -765,11 +772,11 @@ hipError_t launch_expand(const ExpandArgs& a, bool base_bf16, bool out_bf16, hip
 
 size_t lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank) {
   (void)n;
-  return up256((size_t)shrink_plan(m, k, kForwardGroups).slices * (size_t)m * (size_t)rank * 4u);
+  return up256((size_t)shrink_plan(m, k, rank, forward_groups(rank)).slices * (size_t)m * (size_t)rank * 4u);
 }
 
 hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream) {
-  const ShrinkPlan plan = shrink_plan(c.m, c.a.k, kForwardGroups);
+  const ShrinkPlan plan = shrink_plan(c.m, c.a.k, c.a.rank, forward_groups(c.a.rank));
   ShrinkArgs s{};
   s.side[0] = {c.a.down, c.x, c.x_stride, static_cast<float*>(c.workspace), (int)c.a.k, plan.slices};
   s.index = c.index;
@@ -979,8 +986,8 @@ struct BackwardPlan {
 
 BackwardPlan backward_plan(int64_t m, int64_t k, int64_t n, int64_t rank, int64_t count) {
   BackwardPlan b{};
-  b.h = shrink_plan(m, k, kBackwardGroups);
-  b.e = shrink_plan(m, n, kBackwardGroups);
+  b.h = shrink_plan(m, k, rank, kBackwardGroups);
+  b.e = shrink_plan(m, n, rank, kBackwardGroups);
   // about 2048 waves in grad, each of at least 32 tokens
   const int64_t columns = (k + 127) / 128 + (n + 127) / 128;
   const int64_t seg = (m * columns / 2048 + 31) / 32 * 32;
