@@ -10,8 +10,8 @@ from torch's allocator per call, so calls on different streams do not share one.
     y = opq.linear(x, weight, alpha, out_dtype=torch.bfloat16)
     lowrank_add(y, x, stack, index, out=y)        # index: which adapter each token uses, or -1
 
-Under autograd use apply_linear and apply_lowrank (module.AdaptedLinear does); the other
-calls refuse tensors that require grad, as attention's do.
+Under autograd use apply_linear and apply_adapted (module.OPQLinear and module.AdaptedLinear
+do); the other calls refuse tensors that require grad, as attention's do.
 """
 from __future__ import annotations
 
@@ -37,6 +37,7 @@ _SIGNATURES = {
     "opq_linear_backward_grouped": (_I, [_P, _P, _P, _P, _L, _L, _L, _L, _F, _P, _I, _P, _Z, _P]),
 }
 
+MAX_TRAINED = 1024   # adapters of one backward pass
 _FLOATS = (torch.float32, torch.bfloat16)
 _ready: Optional[ctypes.CDLL] = None
 
@@ -170,3 +171,82 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
                    lib.opq_linear_backward(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
                                            weight.scale.data_ptr(), m, n, k, alpha, *tail))
     return out
+
+
+# ------------------------------------------------------------------ autograd
+
+def _dy(dy: torch.Tensor) -> torch.Tensor:
+    """The gradient as the kernels take it: dense, in bfloat16, the type these layers' activations
+    are rounded to on their way in."""
+    return dy.to(torch.bfloat16).contiguous()
+
+
+def _weight(like, tensors):
+    return type(like)(*tensors, *like[3:])
+
+
+class _Linear(torch.autograd.Function):
+    """opq.linear; the weights are stored codes and take no gradient, so nothing of x is kept."""
+
+    @staticmethod
+    def forward(ctx, x, weight, alpha, bias, out_dtype):
+        ctx.save_for_backward(*weight[:3])
+        ctx.how = (weight, alpha, x.dtype)
+        return opq.linear(x.to(torch.bfloat16).contiguous(), weight, alpha, bias=bias, out_dtype=out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        weight, alpha, dtype = ctx.how
+        dx = linear_backward(_dy(dy), _weight(weight, ctx.saved_tensors), alpha, out_dtype=dtype)
+        return dx, None, None, None, None
+
+
+class _Adapted(torch.autograd.Function):
+    """opq.linear with every token's adapter added: one output, written once more in place."""
+
+    @staticmethod
+    def forward(ctx, x, weight, alpha, bias, down, up, scale, index, out_dtype):
+        xb = x.to(torch.bfloat16).contiguous()
+        y = opq.linear(xb, weight, alpha, bias=bias, out_dtype=out_dtype)
+        lowrank_add(y, xb, Adapters(down, up, scale), index, out=y)
+        ctx.save_for_backward(xb, down, up, scale, index, *weight[:3])
+        ctx.how = (weight, alpha, x.dtype)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        xb, down, up, scale, index, *tensors = ctx.saved_tensors
+        weight, alpha, dtype = ctx.how
+        dy, dx = _dy(dy), None
+        wants_x, wants = ctx.needs_input_grad[0], ctx.needs_input_grad[4] or ctx.needs_input_grad[5]
+        if wants_x:
+            dx = linear_backward(dy, _weight(weight, tensors), alpha, out_dtype=dtype)
+        _, d_down, d_up = lowrank_backward(dy, xb, Adapters(down, up, scale), index, dx=dx, out=dx, grad_dtype=down.dtype,
+                                           input_grad=wants_x, adapter_grads=wants)
+        return dx, None, None, None, d_down, d_up, None, None, None
+
+
+def apply_linear(x: torch.Tensor, weight, alpha: float, bias: Optional[torch.Tensor] = None,
+                 out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """opq.linear(x [m, k], float32 or bfloat16) that autograd differentiates with respect to x (not
+    to the stored weights, nor to a bias).  The result has x's type unless out_dtype says otherwise;
+    gradients of gradients are refused."""
+    if bias is not None and bias.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("bias requires grad, which apply_linear does not follow: detach it")
+    return _Linear.apply(x, weight, alpha, bias, out_dtype or x.dtype)
+
+
+def apply_adapted(x: torch.Tensor, weight, alpha: float, bias: Optional[torch.Tensor], adapters: Adapters,
+                  index: torch.Tensor, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """opq.linear of x [m, k] plus every token's adapter (lowrank_add), differentiated with respect
+    to x, adapters.down and adapters.up (not to scale or bias).  Training a stack updates the
+    adapters that `index` names and gives zeros for the others.  Gradients of gradients are refused."""
+    for name, t in (("scale", adapters.scale), ("bias", bias)):
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError(f"{name} requires grad, which apply_adapted does not follow: detach it")
+    if adapters.down.shape[0] > MAX_TRAINED and torch.is_grad_enabled() and any(
+            t.requires_grad for t in (x, adapters.down, adapters.up)):
+        raise ValueError(f"a backward pass takes up to {MAX_TRAINED} adapters, got {adapters.down.shape[0]}")
+    return _Adapted.apply(x, weight, alpha, bias, adapters.down, adapters.up, adapters.scale, index, out_dtype or x.dtype)

@@ -161,4 +161,63 @@ class OPQAttention(nn.Module):
                      token_slots(page_table, dst, cache.page, cache.pages).contiguous())
 
 
-__all__: Sequence[str] = ["OPQAttention", "token_slots"]
+class PagedSequences:
+    """The page table and lengths of a server's rows, over the caches of its layers (which share
+    the table, so have the same pages and page size): rows grow, are forked and dropped, their
+    pages taken, freed and drawn together.  Nothing here waits for the GPU; `missing` (int32 [1], on
+    the device) says after each call how many entries no free page was left for.
+
+        seqs = PagedSequences(rows=32, columns=128, pages=cache.pages, page=cache.page)
+        seqs.room(draft)                                    # pages for the tokens to come
+        y = layer(x, cache, seqs.page_table, seqs.lens)
+        kept, count, following = verify_drafts(...)
+        seqs.accept([cache], kept, count)                   # keeps them, frees the rest
+        seqs.fork([cache], parents)                         # beams, samples, requests gone (-1)
+    """
+
+    def __init__(self, rows: int, columns: int, pages: int, page: int, device="cuda"):
+        self.pages, self.page = pages, page
+        self.page_table = torch.full((rows, columns), -1, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(rows, dtype=torch.int32, device=device)
+        self.missing = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def _caches(self, caches: Sequence[A.PagedCache]) -> None:
+        for cache in caches:
+            if cache.pages != self.pages or cache.page != self.page:
+                raise ValueError(f"the cache has {cache.pages} pages of {cache.page}, the table's are {self.pages} of "
+                                 f"{self.page}")
+
+    def room(self, tokens) -> torch.Tensor:
+        """Pages for `tokens` more tokens in every row (a number, or int32 [rows]); returns `missing`."""
+        self.page_table, self.missing = A.pages_resize(self.page_table, self.lens + tokens, self.pages, self.page)
+        return self.missing
+
+    def accept(self, caches: Sequence[A.PagedCache], kept: torch.Tensor, count: torch.Tensor) -> None:
+        """Keep verified tokens (verify_drafts' kept and count) in every cache, and free the pages
+        that only the others needed."""
+        self._caches(caches)
+        for cache in caches:
+            OPQAttention.accept(cache, self.page_table, self.lens, kept)
+        self.lens = self.lens + count
+        self.room(0)
+
+    def fork(self, caches: Sequence[A.PagedCache], parents: torch.Tensor) -> torch.Tensor:
+        """Row i becomes a copy of row parents[i] (int32; -1: an empty row), its tokens shared
+        page by page but for a last page that is not full; returns `missing`."""
+        self._caches(caches)
+        self.page_table, self.lens, src, dst, self.missing = A.pages_fork(
+            self.page_table, self.lens, parents, self.pages, self.page)
+        for cache in caches:
+            A.cache_copy_pages(cache, src, dst)
+        return self.missing
+
+    def compact(self, caches: Sequence[A.PagedCache]) -> torch.Tensor:
+        """Move the pages in use to the lowest ids; returns their number (int32 [1], on the device)."""
+        self._caches(caches)
+        self.page_table, src, dst, used = A.pages_compact(self.page_table, self.pages)
+        for cache in caches:
+            A.cache_copy_pages(cache, src, dst)
+        return used
+
+
+__all__: Sequence[str] = ["OPQAttention", "PagedSequences", "token_slots"]

@@ -26,7 +26,7 @@ import numpy as np
 import torch
 from torch import nn
 
-from . import opq
+from . import adapters, opq
 
 FORMAT = "opq-int4/1"
 _META_KEY = "opq"
@@ -47,7 +47,9 @@ class OPQLinear(nn.Module):
     float32 [out] (one per output row), or, for 4 bits, float16
     [out, in/group_size] with ``group_size`` in 32, 64, 128, 256.  The bias,
     when present, is float32.  x may be bfloat16 or float32 (it is rounded to
-    bfloat16, the layer's activation type); y has x's dtype."""
+    bfloat16, the layer's activation type); y has x's dtype.  Gradients pass
+    through to x (dx = dy W', dy rounded to bfloat16 as x is); the stored
+    weights take none."""
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True,
                  alpha: float = 0.73, device=None, group_size: Optional[int] = None,
@@ -128,6 +130,9 @@ class OPQLinear(nn.Module):
         if x.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError(f"x must be bfloat16 or float32, got {x.dtype}")
         lead = x.shape[:-1]
+        if x.requires_grad and torch.is_grad_enabled():
+            y = adapters.apply_linear(x.reshape(-1, self.in_features), self.qweight(), self.alpha, self.bias)
+            return y.reshape(*lead, self.out_features)
         x2 = x.reshape(-1, self.in_features).to(torch.bfloat16).contiguous()
         y = opq.linear(x2, self.qweight(), self.alpha, bias=self.bias, out_dtype=x.dtype)
         return y.reshape(*lead, self.out_features)
@@ -136,6 +141,84 @@ class OPQLinear(nn.Module):
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, alpha={self.alpha:.8g}, "
                 f"group_size={self.group_size}, bits={self.bits}")
+
+
+class AdaptedLinear(nn.Module):
+    """An OPQLinear with a stack of low-rank adapters beside it: token t of adapter i gets
+    scale[i] * up[i]^T (down[i] x_t) added to the layer's output.  The base stays as it is
+    stored; ``down`` [adapters, rank, in] and ``up`` [adapters, rank, out] (bfloat16) are the
+    parameters to train, and one layer serves the requests of all of them at once.
+
+    A new stack changes nothing (``up`` starts as zeros).  The rank may be 1..128; it is kept as
+    the next multiple of 8, the rest zeros, which gradients leave zeros.  out_features must be
+    a multiple of 8.  Types stay as they are made (bfloat16, scales float32): convert a model
+    before its layers are quantized and adapted."""
+
+    def __init__(self, base: OPQLinear, count: int, rank: int, scale: float = 1.0):
+        super().__init__()
+        if not isinstance(base, OPQLinear):
+            raise ValueError(f"base must be an OPQLinear, got {type(base).__name__}")
+        if base.out_features % 8:
+            raise ValueError(f"out_features must be a multiple of 8, got {base.out_features}")
+        if count < 1 or not 1 <= rank <= 128:
+            raise ValueError(f"count must be positive and rank 1 to 128, got {count} and {rank}")
+        self.base, self.rank = base, int(rank)
+        held = (rank + 7) // 8 * 8
+        kw = dict(dtype=torch.bfloat16, device=base.packed.device)
+        down = torch.zeros((count, held, base.in_features), **kw)
+        down[:, :rank].normal_(0.0, base.in_features ** -0.5)
+        self.down = nn.Parameter(down)
+        self.up = nn.Parameter(torch.zeros((count, held, base.out_features), **kw))
+        self.register_buffer("scale", torch.full((count,), float(scale), dtype=torch.float32, device=base.packed.device))
+        self.index: Optional[torch.Tensor] = None   # which adapter each token uses: use_adapters
+
+    @torch.no_grad()
+    def set_adapter(self, i: int, down: torch.Tensor, up: torch.Tensor, scale: Optional[float] = None) -> None:
+        """Fill adapter i from two layers' weights: down [rank, in] and up [out, rank] (rank up to
+        this stack's)."""
+        r = down.shape[0]
+        if not 0 <= i < self.down.shape[0]:
+            raise ValueError(f"adapter {i} of {self.down.shape[0]}")
+        if r > self.rank or tuple(down.shape) != (r, self.base.in_features) or tuple(up.shape) != (self.base.out_features, r):
+            raise ValueError(f"adapter must be [r, {self.base.in_features}] and [{self.base.out_features}, r], r up to "
+                             f"{self.rank}, got {tuple(down.shape)} and {tuple(up.shape)}")
+        self.down[i].zero_()
+        self.up[i].zero_()
+        self.down[i, :r].copy_(down)
+        self.up[i, :r].copy_(up.t())
+        if scale is not None:
+            self.scale[i] = float(scale)
+
+    def stack(self) -> adapters.Adapters:
+        return adapters.Adapters(self.down, self.up, self.scale)
+
+    def forward(self, x: torch.Tensor, index: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """index: int32, which adapter each token uses (-1: none): x's shape without its last
+        dimension, or the first of those dimensions (one entry a sequence).  Without it, what
+        use_adapters set; without that, the base alone."""
+        base = self.base
+        index = self.index if index is None else index
+        if index is None:
+            return base(x)
+        lead = x.shape[:-1]
+        if x.shape[-1] != base.in_features or x.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"x must be bfloat16 or float32 [..., {base.in_features}], got {x.dtype} {tuple(x.shape)}")
+        if index.dtype != torch.int32 or index.device != x.device or index.shape != lead[:index.dim()]:
+            raise ValueError(f"index must be int32 {tuple(lead)}, or its first dimensions, on {x.device}, got "
+                             f"{index.dtype} {tuple(index.shape)} on {index.device}")
+        index = index.reshape(index.shape + (1,) * (len(lead) - index.dim())).expand(lead).reshape(-1).contiguous()
+        x2 = x.reshape(-1, base.in_features)
+        if torch.is_grad_enabled() and (x.requires_grad or self.down.requires_grad or self.up.requires_grad):
+            y = adapters.apply_adapted(x2, base.qweight(), base.alpha, base.bias, self.stack(), index)
+        else:
+            x2 = x2.to(torch.bfloat16).contiguous()
+            y = opq.linear(x2, base.qweight(), base.alpha, bias=base.bias, out_dtype=x.dtype)
+            with torch.no_grad():
+                adapters.lowrank_add(y, x2, self.stack(), index, out=y)
+        return y.reshape(*lead, base.out_features)
+
+    def extra_repr(self) -> str:
+        return f"adapters={self.down.shape[0]}, rank={self.rank}"
 
 
 # ---------------------------------------------------------------- conversion
@@ -185,6 +268,36 @@ def replace_with_opq(model: nn.Module, bits: int = 4, alpha: float = 0.73,
             made[id(child)] = OPQLinear.from_linear(child, alpha, group_size, bits)
         setattr(parent, cname, made[id(child)])
     return [full for full, _, _, _ in found]
+
+
+def add_adapters(model: nn.Module, count: int, rank: int, scale: float = 1.0, skip: Iterable[str] = ()) -> List[str]:
+    """Put a stack of `count` low-rank adapters beside every OPQLinear of `model` (in place; those of
+    an AdaptedLinear, names under `skip` and layers whose out_features is no multiple of 8 stay as
+    they are); returns the qualified names.  A layer reached under several names gets one stack."""
+    skip = tuple(skip)
+    made: Dict[int, AdaptedLinear] = {}
+    names = []
+    for parent_name, parent in list(model.named_modules()):
+        if isinstance(parent, AdaptedLinear):
+            continue
+        for cname, child in list(parent._modules.items()):
+            full = f"{parent_name}.{cname}" if parent_name else cname
+            if not isinstance(child, OPQLinear) or child.out_features % 8 or \
+                    any(full == s or full.startswith(s + ".") for s in skip):
+                continue
+            if id(child) not in made:
+                made[id(child)] = AdaptedLinear(child, count, rank, scale)
+            setattr(parent, cname, made[id(child)])
+            names.append(full)
+    return names
+
+
+def use_adapters(model: nn.Module, index: Optional[torch.Tensor]) -> None:
+    """Which adapter each token (or sequence) uses in the forwards that follow, for every
+    AdaptedLinear of `model`; None: the base alone."""
+    for mod in model.modules():
+        if isinstance(mod, AdaptedLinear):
+            mod.index = index
 
 
 # ---------------------------------------------------------------- save / load
