@@ -880,13 +880,17 @@ struct GradArgs {
   int rank;
 };
 
-// Workgroup (512 columns, item, 64 rows of the rank), a wave 128 columns: lane (c, q) holds
-// columns 8 c ... of eight tokens, 8 q ... of each 32, and after the transposition is column
-// 8 c + j of the j-th product.  RT: 16-row tiles of the rank, at most 4 (rank 128 takes two
-// workgroups, by registers).
+// Workgroup (128 columns, item, 64 rows of the rank): its waves take every fourth 32 tokens and
+// meet in LDS, so that an item may be four times as long as one wave's share (with a wave
+// for 128 columns each and items a quarter as long, the slots of a single adapter of 4096 tokens
+// were 16 MB to write and join).  Lane (c, q) holds columns 8 c ... of eight tokens, 8 q ... of
+// each 32, and after the transposition is column 8 c + j of the j-th product.  RT: 16-row
+// tiles of the rank, at most 4 (rank 128 takes two workgroups, by registers).
 template <int RT, bool OUT_BF16>
 __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
   constexpr int PARTS = OUT_BF16 ? 2 : 3;
+  constexpr int kOnce = RT < 2 ? RT : 2;  // row tiles in LDS together
+  __shared__ float s_red[kWaves][kOnce][8][4][kWave];
   const int item = blockIdx.y;
   if (item >= *a.g.items) return;
   const bool second = blockIdx.x >= (unsigned)a.side[0].blocks;
@@ -894,9 +898,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, q = lane >> 4;
-  const int n0 = ((int)blockIdx.x - (second ? a.side[0].blocks : 0)) * 512 + wave * 128;
-  if (n0 >= g.d) return;
-  const int n = n0 + c * 8, r0 = blockIdx.z * 64;
+  const int n = ((int)blockIdx.x - (second ? a.side[0].blocks : 0)) * 128 + c * 8, r0 = blockIdx.z * 64;
   const int from = a.g.from[item], length = a.g.length[item];
   const uint16_t* v = g.v + (n < g.d ? n : 0);
   const int tiles = (a.rank + 15) / 16;
@@ -910,7 +912,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-  for (int at = 0; at < length; at += 32) {
+  for (int at = wave * 32; at < length; at += kWaves * 32) {
     const int4* o = reinterpret_cast<const int4*>(a.g.order + from + at + q * 8);
     const int4 o0 = o[0], o1 = o[1];
     const int t[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
@@ -931,23 +933,36 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
         for (int j = 0; j < 8; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h[i][k], operand(cols[j]), acc[i][j], 0, 0, 0);
   }
-  if (n >= g.d) return;
   const int slot = a.g.slot[item];
   const int64_t first = slot < 0 ? (int64_t)a.g.adapter[item] * a.rank : (int64_t)slot * a.rank;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int i0 = 0; i0 < RT; i0 += kOnce) {
+    if (i0) __syncthreads();  // the last tiles are read
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = r0 + i * 16 + q * 4 + e;
-      if (r < a.rank) {
-        float w[8];
+    for (int i = 0; i < kOnce; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = acc[i][j][e];
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_red[wave][i][j][e][lane] = acc[i0 + i][j][e];
+    __syncthreads();
+    // wave e adds the rows 4 q + e
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i) {
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = s_red[0][i][j][wave][lane];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) w[j] += s_red[k][i][j][wave][lane];
+      }
+      const int r = r0 + (i0 + i) * 16 + q * 4 + wave;
+      if (r < a.rank && n < g.d) {
         const int64_t to = (first + r) * g.d + n;
         if (slot < 0) store8<OUT_BF16>(g.out, to, w);
         else store8<false>(g.part, to, w);
       }
     }
+  }
 }
 
 struct JoinArgs {
@@ -977,6 +992,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_join(JoinArgs a) {
   }
 }
 
+constexpr int kGradGroups = 512;
 struct BackwardPlan {
   ShrinkPlan h, e;
   int64_t cap, items, slots;
@@ -988,10 +1004,10 @@ BackwardPlan backward_plan(int64_t m, int64_t k, int64_t n, int64_t rank, int64_
   BackwardPlan b{};
   b.h = shrink_plan(m, k, rank, kBackwardGroups);
   b.e = shrink_plan(m, n, rank, kBackwardGroups);
-  // about 2048 waves in grad, each of at least 32 tokens
+  // about 512 workgroups in grad, each wave of at least 32 tokens
   const int64_t columns = (k + 127) / 128 + (n + 127) / 128;
-  const int64_t seg = (m * columns / 2048 + 31) / 32 * 32;
-  b.seg = (int)std::max<int64_t>(32, seg);
+  const int64_t seg = (m * columns / kGradGroups + 127) / 128 * 128;
+  b.seg = (int)std::max<int64_t>(128, seg);
   const int64_t met = std::min(m, count);
   b.cap = (m + 32 * met + 63) / 64 * 64;
   b.items = (m + b.seg - 1) / b.seg + met;
@@ -1124,9 +1140,9 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
   GradArgs ga{};
   ga.g = g;
   ga.side[0] = {c.x, o.out[0], c.x_stride, reinterpret_cast<float*>(ws + b.sums_down), c.d_down, (int)k,
-                (int)((k + 511) / 512)};
+                (int)((k + 127) / 128)};
   ga.side[1] = {c.dy, o.out[1], c.dy_stride, reinterpret_cast<float*>(ws + b.sums_up), c.d_up, (int)n,
-                (int)((n + 511) / 512)};
+                (int)((n + 127) / 128)};
   ga.cap = b.cap;
   ga.rank = (int)rank;
   if (c.m > 0) {  // else there is no item, and the join writes zeros
