@@ -962,17 +962,50 @@ __global__ __launch_bounds__((NMB <= 2 ? 16 : 8) * kWave) void linear_dense_skin
 namespace {
 
 // y[mm][c] = sum over s = 0 .. S-1 of part[s][mm][c], in that order, + bias[c]
-// (the split-k planes of linear_tiled).
+// (the split-k planes of the tiled kernels).  kVec: four neighbours a thread, for n
+// a multiple of 4 (a row's four columns; 16-byte planes): 333 x 3840 in six planes 5.6 us,
+// single elements 10.7.
+template <bool kVec>
 __global__ __launch_bounds__(256) void linear_split_reduce(const float* __restrict__ part,
                                                            int nslice, int64_t count, int n,
                                                            const float* __restrict__ bias,
                                                            void* __restrict__ y, int y_bf16) {
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < count;
-       e += (int64_t)gridDim.x * 256) {
-    float v = part[e];
-    for (int s = 1; s < nslice; ++s) v += part[(int64_t)s * count + e];
-    store_y(y, y_bf16, e, v + (bias ? bias[e % n] : 0.0f));
+  constexpr int kWide = kVec ? 4 : 1;
+  for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kWide; e < count;
+       e += (int64_t)gridDim.x * 256 * kWide) {
+    if constexpr (kVec) {
+      floatx4_t v = *reinterpret_cast<const floatx4_t*>(part + e);
+      for (int s = 1; s < nslice; ++s) v += *reinterpret_cast<const floatx4_t*>(part + (int64_t)s * count + e);
+      if (bias) {
+        const int c = (int)(e % n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += bias[c + i];
+      }
+      if (y_bf16) {
+        typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+        const u32x2_t w = {bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16};
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(y) + e));
+      } else {
+        __builtin_nontemporal_store(v, reinterpret_cast<floatx4_t*>(static_cast<float*>(y) + e));
+      }
+    } else {
+      float v = part[e];
+      for (int s = 1; s < nslice; ++s) v += part[(int64_t)s * count + e];
+      store_y(y, y_bf16, e, v + (bias ? bias[e % n] : 0.0f));
+    }
   }
+}
+
+void launch_split_reduce(const float* part, int split, int64_t m, int64_t n, const float* bias, void* y,
+                         bool y_bf16, hipStream_t stream) {
+  const int64_t count = m * n, threads = n % 4 ? count : count / 4;
+  const dim3 grid((unsigned)std::min<int64_t>((threads + 255) / 256, 8192));
+  if (n % 4)
+    hipLaunchKernelGGL(linear_split_reduce<false>, grid, dim3(256), 0, stream, part, split, count, (int)n, bias, y,
+                       (int)y_bf16);
+  else
+    hipLaunchKernelGGL(linear_split_reduce<true>, grid, dim3(256), 0, stream, part, split, count, (int)n, bias, y,
+                       (int)y_bf16);
 }
 
 constexpr int64_t kPartCUs = 256;                        // the part's CUs
@@ -1075,10 +1108,7 @@ hipError_t launch_linear_any(const uint16_t* x, const uint32_t* packed, const ui
       hipLaunchKernelGGL((linear_tiled<false, GS, (GS == 0)>), dim3((unsigned)(tiles_m * tiles_n * split)),
                          dim3(kTThreads), 0, stream, x, packed, sign, scale, scale16, bias, (int)m,
                          (int)n, (int)k, (int)tiles_m, lv, y, (int)y_bf16, sps, part);
-      const int64_t count = m * n;
-      const int64_t rb = std::min<int64_t>((count + 255) / 256, 8192);
-      hipLaunchKernelGGL(linear_split_reduce, dim3((unsigned)rb), dim3(256), 0, stream, part, split,
-                         count, (int)n, bias, y, (int)y_bf16);
+      launch_split_reduce(part, split, m, n, bias, y, y_bf16, stream);
       return hipGetLastError();
     }
     auto kernel = (k % kTK) ? linear_tiled<true, GS> : linear_tiled<false, GS>;
@@ -1143,10 +1173,7 @@ hipError_t launch_linear_dense(const uint16_t* x, const uint16_t* wd, const floa
       hipLaunchKernelGGL((linear_dense_tiled<false, true>), dim3((unsigned)(tiles_m * tiles_n * split)),
                          dim3(kTThreads), 0, stream, x, wd, bias, (int)m, (int)n, (int)k, (int)tiles_m, y,
                          (int)y_bf16, sps, part);
-      const int64_t count = m * n;
-      const int64_t rb = std::min<int64_t>((count + 255) / 256, 8192);
-      hipLaunchKernelGGL(linear_split_reduce, dim3((unsigned)rb), dim3(256), 0, stream, part, split,
-                         count, (int)n, bias, y, (int)y_bf16);
+      launch_split_reduce(part, split, m, n, bias, y, y_bf16, stream);
       return hipGetLastError();
     }
     auto kernel = (k % kTK) ? linear_dense_tiled<true> : linear_dense_tiled<false>;

@@ -22,9 +22,10 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 constexpr int kNoRow = 0x7FFFFFFF;
-// One workgroup: its bytes lie in LDS.
+// One workgroup: what it keeps lies in LDS.
 constexpr int kOnePages = 16384;
 constexpr int64_t kOneEntries = 32768;
+constexpr int kOneRows = 2048;
 
 struct Space {
   uint8_t* named;   // [words * 32] 1: pages named in full (fork), or named at all
@@ -32,6 +33,8 @@ struct Space {
   uint32_t* words;  // [words] the pages in use, a bit each
   int32_t* first;   // [pages] fork: the first row that ends in the page; compact: where it moves
   int32_t* free;    // [pages] free pages in order, as many as are needed
+  int32_t* from;    // [rows] old row of each new one, any for an empty one
+  int32_t* tokens;  // [rows] its tokens
   int32_t* row;     // [rows] resize: entries lacking, then the row's first place in `free`;
                     // fork: the page the row ends in, then its place in `free`; -1: none
   int32_t* total;   // [2] pages needed, pages free
@@ -46,13 +49,8 @@ struct Me {
 };
 
 __device__ __forceinline__ bool named(const PagesArgs& a, int id) { return id >= 0 && id < a.pages; }
-// Tokens of an old row (0 for none), and the entries they need.
-__device__ __forceinline__ int64_t tokens_of(const PagesArgs& a, int row) {
-  if (row < 0 || row >= a.rows) return 0;
-  return min((int64_t)max(a.lens[row], 0), (int64_t)a.columns * a.page);
-}
-__device__ __forceinline__ int entries_of(const PagesArgs& a, int64_t tokens) {
-  return (int)((tokens + a.page - 1) / a.page);
+__device__ __forceinline__ int entries_of(const PagesArgs& a, int tokens) {
+  return (int)(((int64_t)tokens + a.page - 1) / a.page);
 }
 
 template <PagesCall CALL>
@@ -64,6 +62,13 @@ __device__ void clear(const PagesArgs& a, const Space& s, Me me) {
   }
   if (CALL == PagesCall::kFork)
     for (int64_t i = me.thread; i < a.pages; i += me.threads) s.first[i] = kNoRow;
+  if (CALL != PagesCall::kCompact)  // what each row is made from, looked up once
+    for (int64_t row = me.thread; row < a.new_rows; row += me.threads) {
+      const int from = CALL == PagesCall::kFork ? a.parents[row] : (int)row;
+      const bool some = from >= 0 && from < a.rows;
+      s.from[row] = some ? from : 0;
+      s.tokens[row] = some ? (int)min((int64_t)max(a.lens[from], 0), (int64_t)a.columns * a.page) : 0;
+    }
 }
 
 template <PagesCall CALL>
@@ -77,7 +82,7 @@ __device__ void mark(const PagesArgs& a, const Space& s, Me me) {
   for (int64_t row = me.wave(); row < a.new_rows; row += me.waves()) {
     if constexpr (CALL == PagesCall::kResize) {
       const int32_t* in = a.table + row * a.columns;
-      const int need = entries_of(a, tokens_of(a, (int)row));
+      const int need = entries_of(a, s.tokens[row]);
       int lack = 0;
       for (int c0 = 0; c0 < need; c0 += kWave) {
         const int c = c0 + me.lane();
@@ -87,10 +92,8 @@ __device__ void mark(const PagesArgs& a, const Space& s, Me me) {
       }
       if (me.lane() == 0) s.row[row] = lack;
     } else {
-      const int from = a.parents[row];
-      const int64_t tokens = tokens_of(a, from);
-      const int full = (int)(tokens / a.page);
-      const int32_t* in = a.table + (int64_t)(tokens ? from : 0) * a.columns;
+      const int tokens = s.tokens[row], full = tokens / a.page;
+      const int32_t* in = a.table + (int64_t)s.from[row] * a.columns;
       for (int c = me.lane(); c < full; c += kWave)
         if (named(a, in[c])) s.named[in[c]] = 1;
       if (me.lane() == 0) {
@@ -222,7 +225,7 @@ __device__ void write(const PagesArgs& a, const Space& s, Me me) {
     int at = s.row[row];
     if constexpr (CALL == PagesCall::kResize) {
       const int32_t* in = a.table + row * a.columns;
-      const int need = entries_of(a, tokens_of(a, (int)row));
+      const int need = entries_of(a, s.tokens[row]);
       for (int c0 = 0; c0 < a.columns; c0 += kWave) {
         const int c = c0 + me.lane();
         int id = c < need ? in[c] : -1;
@@ -234,10 +237,8 @@ __device__ void write(const PagesArgs& a, const Space& s, Me me) {
         at += __popcll(mask);
       }
     } else {
-      const int from = a.parents[row];
-      const int64_t tokens = tokens_of(a, from);
-      const int need = entries_of(a, tokens);
-      const int32_t* in = a.table + (int64_t)(tokens ? from : 0) * a.columns;
+      const int tokens = s.tokens[row], need = entries_of(a, tokens);
+      const int32_t* in = a.table + (int64_t)s.from[row] * a.columns;
       const int fresh = at >= 0 && at < free ? s.free[at] : -1;
       for (int c = me.lane(); c < a.columns; c += kWave) {
         int id = c < need ? in[c] : -1;
@@ -248,7 +249,7 @@ __device__ void write(const PagesArgs& a, const Space& s, Me me) {
       if (me.lane() == 0) {
         a.src[row] = fresh >= 0 ? in[need - 1] : -1;
         a.dst[row] = fresh;
-        a.out_lens[row] = (int)tokens;
+        a.out_lens[row] = tokens;
       }
     }
   }
@@ -280,10 +281,20 @@ template <PagesCall CALL>
 __global__ __launch_bounds__(kPlanThreads) void pages_one(PagesArgs a, Space s) {
   __shared__ __attribute__((aligned(16))) uint8_t s_named[kOnePages];
   __shared__ __attribute__((aligned(16))) uint8_t s_part[CALL == PagesCall::kFork ? kOnePages : 16];
+  __shared__ int32_t s_first[kOnePages];
+  __shared__ int32_t s_rows[CALL == PagesCall::kCompact ? 1 : 3][kOneRows];
+  __shared__ int32_t s_total[2];
   __shared__ int s_sum[kPlanThreads / kWave];
   const Me me{(int64_t)threadIdx.x, kPlanThreads};
   s.named = s_named;
   s.part = s_part;
+  s.first = s.free = s_first;  // the free pages are listed when nobody asks for first rows any more
+  s.from = s_rows[0];
+  if constexpr (CALL != PagesCall::kCompact) {
+    s.tokens = s_rows[1];
+    s.row = s_rows[2];
+  }
+  s.total = s_total;
   clear<CALL>(a, s, me);
   __syncthreads();
   mark<CALL>(a, s, me);
@@ -298,7 +309,7 @@ size_t up256(size_t b) { return (b + 255u) & ~size_t(255); }
 template <PagesCall CALL>
 hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
   const int64_t entries = (int64_t)a.new_rows * a.columns;
-  if (a.pages <= kOnePages && entries <= kOneEntries) {
+  if (a.pages <= kOnePages && entries <= kOneEntries && a.new_rows <= kOneRows) {
     hipLaunchKernelGGL(pages_one<CALL>, dim3(1), dim3(kPlanThreads), 0, stream, a, s);
     return hipGetLastError();
   }
@@ -306,7 +317,7 @@ hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
     return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((threads + kRowThreads - 1) / kRowThreads, 2048)));
   };
   const dim3 rows = blocks(CALL == PagesCall::kCompact ? entries : (int64_t)a.new_rows * kWave);
-  hipLaunchKernelGGL(pages_clear<CALL>, blocks(CALL == PagesCall::kFork ? a.pages : (a.pages + 15) / 16),
+  hipLaunchKernelGGL(pages_clear<CALL>, blocks(std::max<int64_t>(a.new_rows, CALL == PagesCall::kFork ? a.pages : (a.pages + 15) / 16)),
                      dim3(kRowThreads), 0, stream, a, s);
   hipLaunchKernelGGL(pages_mark<CALL>, rows, dim3(kRowThreads), 0, stream, a, s);
   hipLaunchKernelGGL(pages_plan<CALL>, dim3(1), dim3(kPlanThreads), 0, stream, a, s);
@@ -318,7 +329,7 @@ hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
 
 size_t pages_workspace_bytes(int64_t rows, int64_t pages) {
   const size_t words = (size_t)(pages + 31) / 32, ids = (size_t)pages * 4;
-  return 2 * up256(words * 32) + up256(words * 4) + 2 * up256(ids) + up256((size_t)rows * 4) + 256;
+  return 2 * up256(words * 32) + up256(words * 4) + 2 * up256(ids) + 3 * up256((size_t)rows * 4) + 256;
 }
 
 hipError_t launch_pages(PagesCall call, const PagesArgs& a, hipStream_t stream) {
@@ -336,6 +347,8 @@ hipError_t launch_pages(PagesCall call, const PagesArgs& a, hipStream_t stream) 
   s.words = reinterpret_cast<uint32_t*>(take(words * 4));
   s.first = reinterpret_cast<int32_t*>(take((size_t)a.pages * 4));
   s.free = reinterpret_cast<int32_t*>(take((size_t)a.pages * 4));
+  s.from = reinterpret_cast<int32_t*>(take((size_t)a.new_rows * 4));
+  s.tokens = reinterpret_cast<int32_t*>(take((size_t)a.new_rows * 4));
   s.row = reinterpret_cast<int32_t*>(take((size_t)a.new_rows * 4));
   switch (call) {
     case PagesCall::kResize: return launch<PagesCall::kResize>(a, s, stream);
