@@ -27,7 +27,8 @@ def _weight(opq, n, k, form, alpha, seed=0):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 32, 32), (7, 1, 32), (33, 100, 256), (64, 31, 512), (65, 264, 256), (130, 1000, 768),
-                                   (257, 96, 512), (300, 520, 1024), (333, 3840, 512), (1024, 200, 256)])
+                                   (257, 96, 512), (300, 520, 1024), (333, 3840, 512), (1024, 200, 256),
+                                   (5, 264, 96), (64, 1000, 160), (17, 7, 224), (16, 2000, 1280), (40, 777, 640), (3, 5000, 128)])
 @pytest.mark.parametrize("form", ["row", 32, 128, "3b", "5b"])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_linear_backward(L, gpu_lib, m, n, k, form, out):
@@ -47,3 +48,35 @@ def test_linear_backward(L, gpu_lib, m, n, k, form, out):
     assert got.dtype == out and got.shape == (m, k)
     assert ((got.double() - want).abs() <= bound).all(), float(((got.double() - want).abs() - bound).max())
     assert torch.equal(got, L.linear_backward(dy, w, alpha, out_dtype=out))
+
+
+@pytest.mark.parametrize("m", [31, 100, 128, 129])
+@pytest.mark.parametrize("form", ["row", 64, 256])
+def test_at_the_change_of_paths(L, gpu_lib, m, form):
+    opq, alpha, n, k = gpu_lib, 0.73, 1100, 768
+    w = _weight(opq, n, k, form, alpha)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m)
+    dy = torch.randn((m, n), generator=g, device=DEV).to(torch.bfloat16)
+    got = L.linear_backward(dy, w, alpha, out_dtype=torch.float32).double()
+    full = opq.dequantize(w, alpha).double()
+    want = dy.double() @ full
+    bound = (n + 64) * 2.0 ** -24 * (dy.double().abs() @ full.abs())
+    assert ((got - want).abs() <= bound + 2.0 ** -24 * (want.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("m", [4, 200])
+def test_an_infinite_last_row(L, gpu_lib, m):
+    """Rows past the last one are not the last one again: an infinity in it stays an infinity."""
+    opq, n, k = gpu_lib, 45, 128
+    w = _weight(opq, n, k, "row", 1.0)
+    w = w._replace(scale=w.scale.clone())
+    w.scale[-1] = float("inf")
+    full = opq.dequantize(w, 1.0).double()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m)
+    dy = torch.randn((m, n), generator=g, device=DEV).to(torch.bfloat16)
+    want = dy.double() @ full
+    got = L.linear_backward(dy, w, 1.0, out_dtype=torch.float32).double()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isposinf(), want.isposinf())
+    assert torch.equal(got.isneginf(), want.isneginf())

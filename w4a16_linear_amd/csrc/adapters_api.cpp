@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -154,7 +155,7 @@ BackwardSpace backward_space(int64_t m, int64_t n, int64_t k) {
   };
   s.padded = take((size_t)k * s.ld * 2);
   s.part = take(n < s.ld ? (size_t)m * s.ld * 2 : 0);
-  s.plain = take(opq::linear_dense_part_bytes(m, k, s.ld));
+  s.plain = take(std::max(opq::linear_dense_part_bytes(m, k, s.ld), opq::backward_short_plan(m, n, k).part_bytes));
   s.bytes = take((size_t)n * k * 2);
   return s;
 }
@@ -187,19 +188,46 @@ static int backward_checks(const uint16_t* dy, const uint32_t* packed, const uin
   return OPQ_OK;
 }
 
+// dy with rows as the kernels read them: its own, or copied to rows of ld.
+static int backward_rows(const uint16_t** dy, int64_t* ldy, int64_t m, int64_t n, const BackwardSpace& s,
+                         char* ws, hipStream_t st) {
+  *ldy = n;
+  if (n == s.ld) return OPQ_OK;
+  uint16_t* padded = reinterpret_cast<uint16_t*>(ws + s.padded);
+  const int e = hip_status(opq::launch_pad_rows(*dy, m, n, padded, s.ld, st));
+  *dy = padded;
+  *ldy = s.ld;
+  return e;
+}
+
 // The product, with W' transposed at the workspace's beginning (n > 0).
 static int backward_product(const uint16_t* dy, int64_t m, int64_t n, int64_t k, void* dx,
                             int dx_dtype, char* ws, hipStream_t st) {
   const BackwardSpace s = backward_space(m, n, k);
-  if (n < s.ld) {
-    uint16_t* padded = reinterpret_cast<uint16_t*>(ws + s.padded);
-    const int e = hip_status(opq::launch_pad_rows(dy, m, n, padded, s.ld, st));
-    if (e != OPQ_OK) return e;
-    dy = padded;
-  }
-  float* part = s.plain > s.part ? reinterpret_cast<float*>(ws + s.part) : nullptr;
+  int64_t ldy;
+  const int e = backward_rows(&dy, &ldy, m, n, s, ws, st);
+  if (e != OPQ_OK) return e;
+  float* part = opq::linear_dense_part_bytes(m, k, s.ld) ? reinterpret_cast<float*>(ws + s.part) : nullptr;
   return hip_status(opq::launch_linear_dense(dy, reinterpret_cast<const uint16_t*>(ws), nullptr, m, k, s.ld, dx,
                                              dx_dtype == OPQ_BF16, part, st));
+}
+
+// 4-bit codes, one max a row or a group (gs > 0), n > 0.
+static int backward_codes(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
+                          const float* scale, const uint16_t* scale16, int64_t m, int64_t n, int64_t k,
+                          int gs, const opq::Levels& lv, void* dx, int dx_dtype, char* ws, hipStream_t st) {
+  const BackwardSpace s = backward_space(m, n, k);
+  if (opq::backward_short_plan(m, n, k).taken) {
+    int64_t ldy = n;
+    const int e = n % 8 ? backward_rows(&dy, &ldy, m, n, s, ws, st) : OPQ_OK;
+    if (e != OPQ_OK) return e;
+    return hip_status(opq::launch_backward_short(dy, ldy, packed, sign, scale, scale16, m, n, k, gs, lv, dx,
+                                                 dx_dtype == OPQ_BF16, reinterpret_cast<float*>(ws + s.part), st));
+  }
+  const int e = hip_status(opq::launch_dequantize_transposed(packed, sign, scale, scale16, n, k, gs, lv,
+                                                             reinterpret_cast<uint16_t*>(ws), s.ld, st));
+  if (e != OPQ_OK) return e;
+  return backward_product(dy, m, n, k, dx, dx_dtype, ws, st);
 }
 
 // No rows of weights: sums of nothing.
@@ -217,11 +245,8 @@ int opq_linear_backward(const uint16_t* dy, const uint32_t* packed, const uint32
   if (n == 0) return no_rows(m, k, dx, dx_dtype, st);
   opq::Levels lv;
   opq::levels(alpha, lv.g);
-  e = hip_status(opq::launch_dequantize_transposed(packed, sign, scale, nullptr, n, k, 0, lv,
-                                                   static_cast<uint16_t*>(workspace),
-                                                   backward_space(m, n, k).ld, st));
-  if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, static_cast<char*>(workspace), st);
+  return backward_codes(dy, packed, sign, scale, nullptr, m, n, k, 0, lv, dx, dx_dtype,
+                        static_cast<char*>(workspace), st);
 }
 
 int opq_linear_backward_bits(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
@@ -261,11 +286,8 @@ int opq_linear_backward_grouped(const uint16_t* dy, const uint32_t* packed, cons
   opq::Levels lv;
   opq::levels(alpha, lv.g);
   if (!opq::grouped_supported(dp, lv)) return OPQ_ERR_UNSUPPORTED;
-  e = hip_status(opq::launch_dequantize_transposed(packed, sign, nullptr, scale16, n, k, (int)group, lv,
-                                                   static_cast<uint16_t*>(workspace),
-                                                   backward_space(m, n, k).ld, st));
-  if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, static_cast<char*>(workspace), st);
+  return backward_codes(dy, packed, sign, nullptr, scale16, m, n, k, (int)group, lv, dx, dx_dtype,
+                        static_cast<char*>(workspace), st);
 }
 
 }  // extern "C"

@@ -50,7 +50,25 @@ struct LowrankBackward {
 size_t lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank, int64_t count);
 hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream);
 
-// linear_backward.hip: dst [k][ld] = W' (bfloat16) transposed, columns n..ld-1 zero, from 4-bit
+// linear_backward.hip: the gradient of few tokens straight from 4-bit codes.  dy has rows of ldy
+// elements, n rounded up to 8 at least, zeros past n; part: the plan's bytes.  Up to 128 tokens,
+// where a call takes (this kernel / W' transposed and the dense product, us) at 8, 64, 128 and
+// 256 tokens: 3840 x 3840 16/23, 26/29, 33/42, 57/37; 11520 x 3840 27/38, 43/51, 82/80, 129/67;
+// 20480 x 3840 38/73, 61/95, 125/143, 214/108
+constexpr int64_t kBackwardShortTokens = 128;
+struct BackwardShort {
+  bool taken;
+  int64_t rows, slices;  // weight rows of a slice
+  size_t part_bytes;
+};
+BackwardShort backward_short_plan(int64_t m, int64_t n, int64_t k);
+hipError_t launch_backward_short(const uint16_t* dy, int64_t ldy, const uint32_t* packed, const uint32_t* sign,
+                                 const float* scale, const uint16_t* scale16, int64_t m, int64_t n, int64_t k,
+                                 int gs, const Levels& lv, void* out, bool bf16, float* part, hipStream_t stream);
+// linear.hip: out [m][n] = the sums of `split` float32 planes of `part`, in order
+hipError_t launch_split_sums(const float* part, int split, int64_t m, int64_t n, void* out, bool bf16,
+                             hipStream_t stream);
+// dst [k][ld] = W' (bfloat16) transposed, columns n..ld-1 zero, from 4-bit
 // codes with one max a row (gs 0: scale) or a group (scale16)
 hipError_t launch_dequantize_transposed(const uint32_t* packed, const uint32_t* sign, const float* scale,
                                         const uint16_t* scale16, int64_t n, int64_t k, int gs, const Levels& lv,

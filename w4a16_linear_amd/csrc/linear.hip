@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "adapters_internal.hpp"
 #include "decode.hpp"
 #include "device_common.hpp"
 #include "group.hpp"
@@ -1137,6 +1138,12 @@ size_t linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const int split = tiled_split(m, n, k, nullptr);
   if (split <= 1) return 0;
   return ((size_t)split * (size_t)m * (size_t)n * 4u + 255u) & ~size_t(255);
+}
+
+hipError_t launch_split_sums(const float* part, int split, int64_t m, int64_t n, void* out, bool bf16,
+                             hipStream_t stream) {
+  launch_split_reduce(part, split, m, n, nullptr, out, bf16, stream);
+  return hipGetLastError();
 }
 
 size_t linear_dense_part_bytes(int64_t m, int64_t n, int64_t k) {

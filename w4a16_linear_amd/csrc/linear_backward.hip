@@ -27,6 +27,144 @@ __device__ __forceinline__ void store_columns(const uint32_t (&row)[8][4], uint1
   }
 }
 
+// Few tokens: dx straight from the 4-bit codes, which are read once and W' nowhere written.
+// Workgroup (128 columns of k, a slice of the weights' rows, 16 MT tokens).  Of 32 rows, lane
+// (c, q) = (l % 16, l / 16) decodes the word of columns 8 c ... of rows 8 q ... and turns
+// the 8 x 8 block in registers: it is column 8 c + j of the j-th product, tokens are the
+// rows.  The rows' tables (16 bfloat16 entries as byte planes, one for each group in the
+// columns) are made in LDS for 256 rows at a time, while the codes of those rows are on
+// their way; a wave takes two of their eight steps.  The waves' sums meet in LDS, the
+// slices' in linear.hip's split reduction.  Bound by the decoder's VALU work, which every 64
+// tokens repeat (20480 x 3840 at 8 tokens: 49 MB of codes in 38 us, sums of the slices and
+// both launches with it).
+template <int MT, int GS>
+__global__ __launch_bounds__(kThreads) void backward_short(
+    const uint16_t* __restrict__ dy, int64_t ldy, const uint32_t* __restrict__ packed,
+    const uint32_t* __restrict__ sign, const float* __restrict__ scale, const uint16_t* __restrict__ scale16,
+    int m, int n, int n_read, int k, Levels lv, int slice_rows, void* __restrict__ out, int out_bf16,
+    float* __restrict__ part) {
+  constexpr int kWaves = kThreads / kWave, kChunk = 256, kMine = kChunk / 32 / kWaves;
+  constexpr int G = GS == 0 || GS >= 128 ? 1 : 128 / GS;  // tables of a row
+  __shared__ __attribute__((aligned(16))) uint32_t s_tab[kChunk * G * 8];
+  __shared__ float s_red[kWaves][8][4][kWave];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, q = lane >> 4;
+  const int k0 = blockIdx.x * 128, col = k0 + c * 8, kk = min(col, k - 8);
+  const int begin = blockIdx.y * slice_rows, end = min(n, begin + slice_rows);
+  const int m0 = blockIdx.z * (16 * MT);
+  const int group = GS == 0 || GS >= 128 ? 0 : c * 8 / (GS ? GS : 1);
+  floatx4_t acc[MT][8];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[t][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  for (int r0 = begin; r0 < end; r0 += kChunk) {
+    uint32_t word[kMine][8], sg[kMine][8];
+    uint4 a[kMine][MT];
+#pragma unroll
+    for (int s = 0; s < kMine; ++s) {
+      const int r = r0 + (wave + s * kWaves) * 32 + q * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t at = min(r + e, n - 1);
+        word[s][e] = packed[at * (k / 8) + kk / 8];
+        sg[s][e] = sign[at * (k / 32) + kk / 32] >> (8 * (c & 3));
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint4 v = *reinterpret_cast<const uint4*>(dy + (int64_t)min(m0 + t * 16 + c, m - 1) * ldy +
+                                                        min(r, n_read - 8));
+        a[s][t] = r < min(end, n_read) ? v : make_uint4(0u, 0u, 0u, 0u);  // rows past the slice count nothing
+      }
+    }
+    if (r0 > begin) __syncthreads();  // the last rows' tables are read
+    {
+      const int64_t r = min(r0 + (int)threadIdx.x, n - 1);
+      const bool past = r0 + (int)threadIdx.x >= n;  // the last row's codes with tables of zeros
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float top;
+        if constexpr (GS > 0) top = f16_value(scale16[r * (k / (GS ? GS : 1)) + min(k0 / (GS ? GS : 1) + g, k / (GS ? GS : 1) - 1)]);
+        else top = scale[r];
+        const RowLut t = make_row_lut(lv, past ? 0.f : top);
+        uint32_t* to = s_tab + (threadIdx.x * G + g) * 8;
+        *reinterpret_cast<uint4*>(to) = make_uint4(t.lo[0], t.lo[1], t.lo[2], t.lo[3]);
+        *reinterpret_cast<uint4*>(to + 4) = make_uint4(t.hi[0], t.hi[1], t.hi[2], t.hi[3]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kMine; ++s) {
+      const int local = (wave + s * kWaves) * 32 + q * 8;
+      if (r0 + (wave + s * kWaves) * 32 >= end) continue;
+      uint32_t row[8][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(s_tab + ((local + e) * G + group) * 8);
+        const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(s_tab + ((local + e) * G + group) * 8 + 4);
+        RowLut t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          t.lo[i] = lo[i];
+          t.hi[i] = hi[i];
+        }
+        decode_word_split(word[s][e], sg[s][e], t, row[e]);
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = __builtin_amdgcn_perm(row[2 * i + 1][p], row[2 * i][p], 0x05040100u);
+          hi[i] = __builtin_amdgcn_perm(row[2 * i + 1][p], row[2 * i][p], 0x07060302u);
+        }
+        const bf16x8_t w0 = __builtin_bit_cast(bf16x8_t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        const bf16x8_t w1 = __builtin_bit_cast(bf16x8_t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const bf16x8_t x = __builtin_bit_cast(bf16x8_t, a[s][t]);
+          acc[t][2 * p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w0, acc[t][2 * p], 0, 0, 0);
+          acc[t][2 * p + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w1, acc[t][2 * p + 1], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    if (t) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s_red[wave][j][e][lane] = acc[t][j][e];
+    __syncthreads();
+    // wave e adds the tokens 4 q + e
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = s_red[0][j][wave][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v[j] += s_red[w][j][wave][lane];
+    }
+    const int token = m0 + t * 16 + q * 4 + wave;
+    if (token < m && col < k) {
+      if (part) {
+        float4* to = reinterpret_cast<float4*>(part + ((int64_t)blockIdx.y * m + token) * k + col);
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else if (out_bf16) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (int64_t)token * k + col) =
+            make_uint4(bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16,
+                       bf16_rne(v[4]) | bf16_rne(v[5]) << 16, bf16_rne(v[6]) | bf16_rne(v[7]) << 16);
+      } else {
+        float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + (int64_t)token * k + col);
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+  }
+}
+
 // dst [k][ld] = W' transposed, straight from 4-bit codes: 0.625 B read and 2 B written a
 // weight, where the dequantizer and a transposition move another 4 (11520 x 3840: 57 us).
 // A lane decodes 32 k of eight rows, 8 k at a time, and turns each 8 x 8 block in
@@ -65,12 +203,13 @@ __global__ __launch_bounds__(kThreads) void dequantize_transposed(
       if (r0 + i >= n) {
         codes[i] = make_uint4(0u, 0u, 0u, 0u);
         signs[i] = 0u;
+        tops[i] = 0u;
       }
     }
     if constexpr (GS == 0) {
       // entry q of row t / 4 as bytes of the planes: thread t makes q = 4 (t % 4) ...
       const int t = threadIdx.x, j = t & 3;
-      const float top = scale[min(row0 + (t >> 2), n - 1)];
+      const float top = row0 + (t >> 2) < n ? scale[row0 + (t >> 2)] : 0.f;
       uint32_t lo = 0u, hi = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -142,6 +281,62 @@ __global__ __launch_bounds__(kThreads) void pad_rows(const uint16_t* __restrict_
 }
 
 }  // namespace
+
+namespace {
+
+constexpr int kShortTokens = 64;  // of a workgroup
+
+template <int GS>
+hipError_t short_of(int tiles, dim3 grid, const uint16_t* dy, int64_t ldy, const uint32_t* packed,
+                    const uint32_t* sign, const float* scale, const uint16_t* scale16, int m, int n, int n_read,
+                    int k, const Levels& lv, int rows, void* out, int bf16, float* part, hipStream_t stream) {
+  auto kernel = tiles == 1 ? backward_short<1, GS> : tiles == 2 ? backward_short<2, GS> : backward_short<4, GS>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, dy, ldy, packed, sign, scale, scale16, m, n, n_read, k,
+                     lv, rows, out, bf16, part);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Slices of about 512 workgroups in all, each of at least 256 rows, their sums at most 32 MB.
+BackwardShort backward_short_plan(int64_t m, int64_t n, int64_t k) {
+  BackwardShort p{};
+  p.taken = m > 0 && n > 0 && m <= kBackwardShortTokens;
+  if (!p.taken) return p;
+  const int64_t groups = (k + 127) / 128 * ((m + kShortTokens - 1) / kShortTokens);
+  int64_t s = std::min((512 + groups - 1) / groups, (n + 255) / 256);
+  s = std::max<int64_t>(1, std::min<int64_t>(s, (int64_t(32) << 20) / (m * k * 4)));
+  p.rows = ((n + s - 1) / s + 255) / 256 * 256;
+  p.slices = (n + p.rows - 1) / p.rows;
+  p.part_bytes = p.slices > 1 ? (size_t)p.slices * m * k * 4 : 0;
+  return p;
+}
+
+hipError_t launch_backward_short(const uint16_t* dy, int64_t ldy, const uint32_t* packed, const uint32_t* sign,
+                                 const float* scale, const uint16_t* scale16, int64_t m, int64_t n, int64_t k,
+                                 int gs, const Levels& lv, void* out, bool bf16, float* part, hipStream_t stream) {
+  const BackwardShort p = backward_short_plan(m, n, k);
+  const int tiles = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+  const dim3 grid((unsigned)((k + 127) / 128), (unsigned)p.slices, (unsigned)((m + 16 * tiles - 1) / (16 * tiles)));
+  const int n_read = (int)(ldy > n ? ldy : n);  // dy's rows are zeros past n where they are longer
+  if (p.slices == 1) part = nullptr;
+  hipError_t e = hipErrorInvalidValue;
+#define OPQ_SHORT(G)                                                                                        \
+  case G:                                                                                                   \
+    e = short_of<G>(tiles, grid, dy, ldy, packed, sign, scale, scale16, (int)m, (int)n, n_read, (int)k, lv, \
+                    (int)p.rows, out, (int)bf16, part, stream);                                             \
+    break;
+  switch (gs) {
+    OPQ_SHORT(0)
+    OPQ_SHORT(32)
+    OPQ_SHORT(64)
+    OPQ_SHORT(128)
+    OPQ_SHORT(256)
+  }
+#undef OPQ_SHORT
+  if (e != hipSuccess || !part) return e;
+  return launch_split_sums(part, (int)p.slices, m, k, out, bf16, stream);
+}
 
 hipError_t launch_dequantize_transposed(const uint32_t* packed, const uint32_t* sign, const float* scale,
                                         const uint16_t* scale16, int64_t n, int64_t k, int gs, const Levels& lv,
