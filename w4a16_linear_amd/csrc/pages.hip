@@ -152,6 +152,14 @@ __device__ void plan(const PagesArgs& a, const Space& s, int* s_sum) {
   const int words = (a.pages + 31) / 32;
   const int per = (words + kPlanThreads - 1) / kPlanThreads;
   const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+  // pages that a row needs; the first rows' are on their way while the words are made
+  const auto needs = [&](int64_t row) {
+    if (CALL == PagesCall::kCompact || row >= a.new_rows) return 0;
+    const int v = s.row[row];
+    if (CALL == PagesCall::kResize) return v;
+    return v >= 0 && (s.named[v] || s.first[v] != (int)row) ? 1 : 0;
+  };
+  const int soon = needs(tid);
   int all, mine = 0;  // words w0 .. w1 - 1 are this thread's alone
   for (int w = w0; w < w1; ++w) {
     uint32_t bits = bits_of(s.named + w * 32);
@@ -186,12 +194,7 @@ __device__ void plan(const PagesArgs& a, const Space& s, int* s_sum) {
   int needed = 0;
   for (int64_t r0 = 0; r0 < a.new_rows; r0 += kPlanThreads) {
     const int64_t row = r0 + tid;
-    int v = row < a.new_rows ? s.row[row] : 0;
-    if constexpr (CALL == PagesCall::kFork) {
-      const int id = row < a.new_rows ? v : -1;
-      v = id >= 0 && (s.named[id] ||
-                      __hip_atomic_load(s.first + id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != (int)row);
-    }
+    const int v = r0 ? needs(row) : soon;
     const int before = scan(v, s_sum, &all);
     if (row < a.new_rows) s.row[row] = CALL == PagesCall::kFork && !v ? -1 : needed + before;
     needed += all;
