@@ -79,6 +79,9 @@ CASES = [  # m, k, n, rank, adapters, index
     (256, 736, 640, 40, 300, "mixed"), (257, 288, 264, 128, 3, "runs"), (130, 96, 2048, 128, 9, "mixed"),
     (777, 1056, 904, 72, 4, "runs"), (1025, 320, 384, 16, 1, "one"), (600, 64, 512, 8, 2, "none"),
     (515, 2048, 128, 48, 40, "outside"),
+    # one launch for few tokens, and past each of its limits
+    (50, 2048, 2056, 32, 6, "mixed"), (64, 72, 4104, 8, 70, "outside"), (48, 2056, 264, 32, 5, "mixed"),
+    (64, 64, 8456, 16, 9, "outside"), (65, 136, 72, 24, 4, "one"),
 ]
 
 

@@ -170,17 +170,32 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{a, b}), bf16x2_t));
 }
 
-template <bool BF16>
+// Sixteen bytes read or written once (STREAM: around the caches' other contents).
+template <bool STREAM>
+__device__ __forceinline__ uint4 load_once(const char* p) {
+  const u32x4_t* v = reinterpret_cast<const u32x4_t*>(p);
+  if constexpr (STREAM) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(v));
+  return __builtin_bit_cast(uint4, *v);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_once(void* p, u32x4_t v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x4_t*>(p));
+  else *static_cast<u32x4_t*>(p) = v;
+}
+
+template <bool BF16, bool STREAM>
 __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8]) {
   if constexpr (BF16) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    store_once<STREAM>(static_cast<uint16_t*>(p) + at, u32x4_t{w[0], w[1], w[2], w[3]});
   } else {
-    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    f[0] = make_float4(v[0], v[1], v[2], v[3]);
-    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    float* f = static_cast<float*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      store_once<STREAM>(f + 4 * i, u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                            __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])});
   }
 }
 
@@ -334,10 +349,10 @@ struct ShrinkArgs {
 constexpr int shrink_tile(int64_t rank) { return rank > 32 ? kBlockTokens : kBlockTokens / 2; }
 
 // Workgroup (slice of d, share of the block's tiles, block of tokens).  A wave
-// takes a quarter of the slice's 32-wide steps for a tile, all tokens of the block that use
+// takes its share of the slice's 32-wide steps for a tile, all tokens of the block that use
 // one adapter, and all rank rows; the waves' sums meet in LDS, the slices' in the
-// reader.  (Tiles of 32 tokens read the stack twice as often, from L2: 39 us for the
-// two sides of 4096 tokens, 3840 -> 11520, rank 16, where the tokens alone take 27.)
+// reader.  (The two sides of 4096 tokens, 3840 -> 11520, rank 16: 35 us, where reading the
+// tokens alone takes 27.)
 // RT: 16-row tiles of the rank.  PLAN: the workgroup past the slices sorts the tokens for
 // the gradients, which wait for this launch anyway (9 us as a launch of its own).
 template <int RT, int W, bool PLAN>
@@ -540,7 +555,9 @@ struct ExpandShared {
 // columns 8 c ..., which after the transposition are the product's j-th columns 8 c + j;
 // tokens are its rows, so a lane's accumulators are eight columns in a row of four tokens,
 // and in every load and store sixteen lanes touch 256 bytes in a row.  What the tiles add
-// to is requested with the stack's block before the operands are made.
+// to is requested with the stack's block before the operands are made.  It and the result
+// pass the caches by, which are for the stack and c (4096 tokens, 3840 -> 20480, rank 64:
+// 111 us with ordinary loads and stores, 99 so); one block of tokens is small enough for both.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
 __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT_BF16>& s, int bx, int by, int bz) {
   constexpr int PARTS = OUT_BF16 ? 2 : 3;
@@ -586,10 +603,10 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
       const int64_t token = t0 + __shfl(t.token, min(q * 4 + i, t.size - 1), kWave);
       const char* from = static_cast<const char*>(a.base) + (token * a.base_stride + n) * (BASE_BF16 ? 2 : 4);
       if constexpr (BASE_BF16) {
-        b.v[i] = *reinterpret_cast<const uint4*>(from);
+        b.v[i] = load_once<!SINGLE>(from);
       } else {
-        b.v[2 * i] = *reinterpret_cast<const uint4*>(from);
-        b.v[2 * i + 1] = *reinterpret_cast<const uint4*>(from + 16);
+        b.v[2 * i] = load_once<!SINGLE>(from);
+        b.v[2 * i + 1] = load_once<!SINGLE>(from + 16);
       }
     }
   };
@@ -667,7 +684,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
         }
-        if (q * 4 + i < t[w].size && mine < a.d) store8<OUT_BF16>(a.out, token * a.out_stride + mine, v);
+        if (q * 4 + i < t[w].size && mine < a.d) store8<OUT_BF16, !SINGLE>(a.out, token * a.out_stride + mine, v);
       }
       if (SINGLE) return;
       if (w + kAhead < kMade && w + kAhead < made && a.base) load_base(t[w + kAhead], base[w % kAhead]);
@@ -690,6 +707,147 @@ __global__ __launch_bounds__(kThreads, (expand_waves<RS, BASE_BF16, SINGLE>())) 
   expand<RS, BASE_BF16, OUT_BF16, SINGLE>(a, s, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
+// ---------------------------------------------------------- few tokens, one launch
+
+constexpr int kFewWaves = 16, kFewThreads = kFewWaves * kWave;
+struct FewArgs {
+  const uint16_t* down;
+  const uint16_t* up;
+  const float* scale;
+  const uint16_t* x;
+  const int32_t* index;
+  const void* base;  // or nullptr
+  void* out;
+  int64_t x_stride, base_stride, out_stride, count;
+  int m, rank, k, n;
+};
+
+// One block of tokens.  Workgroup (a token that leads a tile, 2048 columns of the output): its
+// sixteen waves take up to four of the shrink's steps at a time and meet in LDS; then each
+// expands 128 columns, whose rows of the stack and tokens to add to were requested first.
+// Every workgroup of a tile makes the tile's c anew, from rows of `down` that are in L2
+// after the first: workgroups of one tile are a multiple of 8 apart, on one XCD.
+// Bound by latency: index, rows, their sums, the product and the store follow one another
+// (3840 -> 3840, rank 8, 1 token: 7.7 us, of which the second round of loads is 2).
+template <int RT, bool BASE_BF16, bool OUT_BF16>
+__global__ __launch_bounds__(kFewThreads) void lowrank_add_few(FewArgs a) {
+  constexpr int PARTS = OUT_BF16 ? 2 : 3, kDepth = BASE_BF16 ? 4 : 2;  // by registers
+  __shared__ float4 s_red[kFewWaves][RT][kWave];
+  __shared__ float4 s_sum[RT][kWave];
+  const int id = block_id(a.index, a.m, a.count);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, q = lane >> 4;
+  const int lowest = a.base == a.out ? 0 : kNoAdapter;  // in place, tokens without an adapter are done
+  if (__builtin_amdgcn_readlane(id, blockIdx.x) < lowest || !leads<16>(id, blockIdx.x)) return;
+  const Tile tile = tile_of<16>(id, blockIdx.x);
+  const bool has = tile.id >= 0;
+  const int mine = blockIdx.y * (kFewWaves * 128) + wave * 128 + c * 8;  // the lane's first column
+  const int at = mine < a.n ? mine : 0;
+  const float scale = has ? a.scale[tile.id] : 0.0f;
+  Base<BASE_BF16> base{};
+  auto load_base = [&]() __attribute__((always_inline)) {
+    if (!a.base) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t token = __shfl(tile.token, min(q * 4 + i, tile.size - 1), kWave);
+      const char* from = static_cast<const char*>(a.base) + (token * a.base_stride + at) * (BASE_BF16 ? 2 : 4);
+      if constexpr (BASE_BF16) {
+        base.v[i] = load_once<false>(from);
+      } else {
+        base.v[2 * i] = load_once<false>(from);
+        base.v[2 * i + 1] = load_once<false>(from + 16);
+      }
+    }
+  };
+  if (BASE_BF16 || !has) load_base();  // float32 has to wait for registers
+  floatx4_t acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  if (has) {
+    uint4 rows[8], p[8];
+    {
+      const uint16_t* from = a.up + ((int64_t)tile.id * a.rank + min(q * 8, a.rank - 8)) * a.n + at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rows[e] = load16(from + (int64_t)e * a.n);
+    }
+    const int lr = lane >> 2, lc = lane & 3;  // row and 16-byte chunk of a load
+    const uint16_t* x = a.x + (int64_t)__shfl(tile.token, min(lr, tile.size - 1), kWave) * a.x_stride;
+    const uint16_t* down = a.down + (int64_t)tile.id * a.rank * a.k;
+    floatx4_t sum[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) sum[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    for (int step = wave * kDepth; step * 32 < a.k; step += kFewWaves * kDepth) {
+      uint4 v[kDepth], w[kDepth][RT];
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) {
+        const int e = (step + u) * 32 + lc * 8;
+        const bool in = e < a.k;      // k is a multiple of 8
+        const int col = in ? e : 0;   // past k the row's first columns are read, and dropped
+        const uint4 y = load16(x + col);
+        v[u] = in ? y : zero16();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const uint4 z = load16(down + (int64_t)min(i * 16 + lr, a.rank - 1) * a.k + col);
+          w[u][i] = in ? z : zero16();
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) {
+        const bf16x8_t y = operand(to_operand(v[u]));
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(to_operand(w[u][i])), y, sum[i], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) s_red[wave][i][lane] = make_float4(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
+    __syncthreads();
+    if (wave < RT) {
+      float4 all = s_red[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) {
+        const float4 add = s_red[w][wave][lane];
+        all.x += add.x; all.y += add.y; all.z += add.z; all.w += add.w;
+      }
+      s_sum[wave][lane] = all;
+    }
+    __syncthreads();
+    // lane (c, q): ranks 8 q ... of token c, which lanes c + 16 (2 q % 4) and the next sixteen hold
+    float v[8] = {};
+    if (q / 2 < RT && q * 8 < a.rank && c < tile.size) {
+      const float4 lo = s_sum[q / 2][c + 32 * (q & 1)], hi = s_sum[q / 2][c + 32 * (q & 1) + 16];
+      v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+      v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    }
+    uint32_t cut[8][PARTS];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split<PARTS>(v[e] * scale, cut[e]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rows[e] = q * 8 < a.rank ? rows[e] : zero16();
+    transpose8(rows, p);
+    if (!BASE_BF16) load_base();
+#pragma unroll
+    for (int e = 0; e < PARTS; ++e) {
+      const bf16x8_t h = operand(make_uint4(cut[0][e] | cut[1][e] << 16, cut[2][e] | cut[3][e] << 16,
+                                            cut[4][e] | cut[5][e] << 16, cut[6][e] | cut[7][e] << 16));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, operand(p[j]), acc[j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t token = __shfl(tile.token, min(q * 4 + i, tile.size - 1), kWave);
+    float v[8] = {};
+    if (a.base) unpack<BASE_BF16>(base, i, v);
+    if (has) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
+    }
+    if (q * 4 + i < tile.size && mine < a.n) store8<OUT_BF16, false>(a.out, token * a.out_stride + mine, v);
+  }
+}
+
 // ------------------------------------------------------------------ launches
 
 int64_t blocks_of(int64_t m) { return (m + kBlockTokens - 1) / kBlockTokens; }
@@ -706,7 +864,7 @@ struct ShrinkPlan {
 // begins.  Backward 512: dy comes from memory (8192 tokens of 10240, rank 64: 144 us, with 256
 // 237).  Forward 256, x was made a moment ago and is in cache; 128 past rank 32, where every
 // workgroup of the expand adds as many slices of longer rows (4096 tokens, 3840 -> 20480,
-// rank 64: 111 us, with 256 119; 2047 tokens, 10240 -> 3840, rank 32: 40, with 256 31).
+// rank 64: 98 us, with 256 103; 2047 tokens, 10240 -> 3840, rank 32: 41, with 256 32).
 constexpr int kBackwardGroups = 512;
 constexpr int forward_groups(int64_t rank) { return rank > 32 ? 128 : 256; }
 ShrinkPlan shrink_plan(int64_t m, int64_t d, int64_t rank, int64_t groups_wanted) {
@@ -770,12 +928,55 @@ hipError_t launch_expand(const ExpandArgs& a, bool base_bf16, bool out_bf16, hip
 
 }  // namespace
 
+namespace {
+
+// Adapters small enough to be read anew by every workgroup, and no more of those than the card
+// takes at once (calls in a graph, this kernel / both, us: 3840 -> 3840, rank 16, 1 token
+// 7.8/8.2, 48 tokens 9.1/11.3; 1024 -> 1024, 48 tokens 5.9/8.6; past the rules rank 32 of
+// 3840 -> 3840, 1 token 9.2/8.6, and 48 tokens of 3840 -> 11520, rank 16, 16.8/15.6).
+constexpr int64_t kFewElements = 1 << 16, kFewGroups = 256;
+bool few(int64_t m, int64_t k, int64_t n, int64_t rank) {
+  return single_block(m) && rank <= 32 && k * rank <= kFewElements &&
+         m * ((n + kFewWaves * 128 - 1) / (kFewWaves * 128)) <= kFewGroups;
+}
+
+template <int RT>
+hipError_t launch_few_of(const FewArgs& a, bool base_bf16, bool out_bf16, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.m + 7) / 8 * 8, (unsigned)(a.n + kFewWaves * 128 - 1) / (kFewWaves * 128));
+  auto kernel = base_bf16 ? out_bf16 ? lowrank_add_few<RT, true, true> : lowrank_add_few<RT, true, false>
+                : out_bf16 ? lowrank_add_few<RT, false, true> : lowrank_add_few<RT, false, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kFewThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 size_t lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank) {
   (void)n;
   return up256((size_t)shrink_plan(m, k, rank, forward_groups(rank)).slices * (size_t)m * (size_t)rank * 4u);
 }
 
 hipError_t launch_lowrank_add(const LowrankAdd& c, hipStream_t stream) {
+  if (few(c.m, c.a.k, c.a.n, c.a.rank)) {
+    FewArgs f{};
+    f.down = c.a.down;
+    f.up = c.a.up;
+    f.scale = c.a.scale;
+    f.x = c.x;
+    f.index = c.index;
+    f.base = c.y;
+    f.out = c.out;
+    f.x_stride = c.x_stride;
+    f.base_stride = c.y_stride;
+    f.out_stride = c.out_stride;
+    f.count = c.a.count;
+    f.m = (int)c.m;
+    f.rank = (int)c.a.rank;
+    f.k = (int)c.a.k;
+    f.n = (int)c.a.n;
+    return c.a.rank <= 16 ? launch_few_of<1>(f, c.y_bf16, c.out_bf16, stream)
+                          : launch_few_of<2>(f, c.y_bf16, c.out_bf16, stream);
+  }
   const ShrinkPlan plan = shrink_plan(c.m, c.a.k, c.a.rank, forward_groups(c.a.rank));
   ShrinkArgs s{};
   s.side[0] = {c.a.down, c.x, c.x_stride, static_cast<float*>(c.workspace), (int)c.a.k, plan.slices};
@@ -958,8 +1159,8 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
       const int r = r0 + (i0 + i) * 16 + q * 4 + wave;
       if (r < a.rank && n < g.d) {
         const int64_t to = (first + r) * g.d + n;
-        if (slot < 0) store8<OUT_BF16>(g.out, to, w);
-        else store8<false>(g.part, to, w);
+        if (slot < 0) store8<OUT_BF16, false>(g.out, to, w);
+        else store8<false, false>(g.part, to, w);
       }
     }
   }
@@ -988,7 +1189,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_join(JoinArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += add[e];
     }
-    store8<OUT_BF16>(a.out[side], id * size + at, v);
+    store8<OUT_BF16, false>(a.out[side], id * size + at, v);
   }
 }
 
