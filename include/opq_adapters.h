@@ -58,7 +58,8 @@ size_t opq_lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank
  * does not depend on the other tokens of the call, whose number sets in how many pieces
  * sums over k are taken; results repeat bit for bit.
  * m up to 2^22, k and n up to 2^20, m * k and m * n up to 2^39 with their strides,
- * count up to 2^30 (OPQ_ERR_UNSUPPORTED past them).
+ * count up to 2^30 (OPQ_ERR_UNSUPPORTED past them, and for y itself as out with another
+ * type or stride).  out must not overlap the other inputs.
  * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALIGN, OPQ_ERR_DTYPE,
  * OPQ_ERR_WORKSPACE, OPQ_ERR_UNSUPPORTED, OPQ_ERR_HIP.
  */
@@ -98,7 +99,8 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
  * values opq_dequantize* writes.  Up to 128 tokens of 4-bit codes are multiplied as
  * the codes are decoded; otherwise W' goes transposed into the workspace, then a dense
  * product makes dx.  Both are bf16 matrix-core products with float32 sums.
- *   dy     device, [m][n] bfloat16, dense;  dx  device out, [m][k] of dx_dtype, dense
+ *   dy     device, [m][n] bfloat16, dense;  dx  device out, [m][k] of dx_dtype, dense;
+ *          it must not overlap the inputs
  *   workspace  at least opq_linear_backward_workspace_bytes(m, n, k) bytes, no
  *          initialisation; calls that may overlap need their own
  * The other arguments as in opq_linear, opq_linear_bits and opq_linear_grouped; n up to

@@ -141,3 +141,13 @@ def test_binding_refuses_what_it_cannot_pass_on():
     w = opq.QuantizedWeight(torch.zeros(32, 8, dtype=torch.int32), torch.zeros(32, 2, dtype=torch.int32), torch.zeros(32))
     with pytest.raises(ValueError, match="CUDA"):
         L.linear_backward(torch.zeros(3, 32, dtype=torch.bfloat16), w, 0.73)
+
+
+def test_in_place_means_the_same_rows(lib):
+    """y as out (dx as dx_out) with another stride or type would leave rows without an adapter unwritten."""
+    def add(m, ys, yd, od, out=FAKE):
+        return lib.opq_lowrank_add(ctypes.byref(_stack()), FAKE, 64, FAKE, m, FAKE, ys, yd, out, 128, od, FAKE, 1 << 40, None)
+
+    assert add(3, 136, 1, 1) == UNSUPPORTED and add(3, 128, 0, 1) == UNSUPPORTED and add(1, 128, 1, 0) == UNSUPPORTED
+    assert lib.opq_lowrank_backward(ctypes.byref(_stack()), FAKE, 128, FAKE, 64, FAKE, 3, FAKE, 72, 1, FAKE, 64, FAKE, FAKE, 0,
+                                    FAKE, 1 << 40, None) == UNSUPPORTED

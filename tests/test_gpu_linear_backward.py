@@ -80,3 +80,15 @@ def test_an_infinite_last_row(L, gpu_lib, m):
     got = L.linear_backward(dy, w, 1.0, out_dtype=torch.float32).double()
     assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isposinf(), want.isposinf())
     assert torch.equal(got.isneginf(), want.isneginf())
+
+
+@pytest.mark.parametrize("m", [8, 200])
+def test_out_beside_dy_not_over_it(L, gpu_lib, m):
+    w = _weight(gpu_lib, 256, 256, "row", 0.73)
+    held = torch.randn((2 * m, 256), device=DEV).to(torch.bfloat16)
+    want = L.linear_backward(held[:m].clone(), w, 0.73)
+    assert torch.equal(L.linear_backward(held[:m], w, 0.73, out=held[m:]), want)
+    assert torch.equal(held[m:], want)
+    for out in (held[:m], held[1:m + 1]):
+        with pytest.raises(ValueError, match="share"):
+            L.linear_backward(held[:m], w, 0.73, out=out)

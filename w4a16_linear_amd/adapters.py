@@ -143,6 +143,9 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
             raise RuntimeError("out requires grad, which this call does not follow")
         if not out.is_inference():
             torch.autograd.graph.increment_version(out)
+        near = out.data_ptr() - dy.data_ptr()
+        if out.numel() and dy.numel() and -out.numel() * out.element_size() < near < dy.numel() * 2:
+            raise ValueError("out must not share memory with dy")
     for name, t in (("out", out), ("packed", weight.packed), ("sign", weight.sign), ("scale", weight[2])):
         if t.device != dy.device:
             raise ValueError(f"{name} must be on {dy.device}, got {t.device}")

@@ -165,7 +165,9 @@ class PagedSequences:
     """The page table and lengths of a server's rows, over the caches of its layers (which share
     the table, so have the same pages and page size): rows grow, are forked and dropped, their
     pages taken, freed and drawn together.  Nothing here waits for the GPU; `missing` (int32 [1], on
-    the device) says after each call how many entries no free page was left for.
+    the device) says after each call how many entries no free page was left for.  A row holds up to
+    columns * page tokens, which nothing here counts: tokens past them have no slot.  Rows grow; one
+    that is cut back into a page that others name has to be forked before it is written again.
 
         seqs = PagedSequences(rows=32, columns=128, pages=cache.pages, page=cache.page)
         seqs.room(draft)                                    # pages for the tokens to come

@@ -65,6 +65,7 @@ int opq_lowrank_add(const opq_lowrank* adapters, const uint16_t* x, int64_t x_st
   if (!sizes_supported(m, a.k, a.n) || a.count > (int64_t(1) << 30) || !within(m, x_stride) ||
       (y && !within(m, y_stride)) || !within(m, out_stride))
     return OPQ_ERR_UNSUPPORTED;
+  if (m > 0 && y == out && ((m > 1 && y_stride != out_stride) || y_dtype != out_dtype)) return OPQ_ERR_UNSUPPORTED;
   if (m == 0) return OPQ_OK;
   opq::LowrankAdd c{};
   c.a = a;
@@ -114,6 +115,7 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
   if (!sizes_supported(m, a.k, a.n) || a.count > opq::kMaxTrained || !within(m, dy_stride) ||
       !within(m, x_stride) || (dx && !within(m, dx_stride)) || (dx_out && !within(m, dx_out_stride)))
     return OPQ_ERR_UNSUPPORTED;
+  if (m > 1 && dx_out && dx == dx_out && dx_stride != dx_out_stride) return OPQ_ERR_UNSUPPORTED;
   if ((m == 0 || !dx_out) && (a.count == 0 || !d_down)) return OPQ_OK;
   opq::LowrankBackward c{};
   c.a = a;

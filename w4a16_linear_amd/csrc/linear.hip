@@ -964,7 +964,7 @@ namespace {
 
 // y[mm][c] = sum over s = 0 .. S-1 of part[s][mm][c], in that order, + bias[c]
 // (the split-k planes of the tiled kernels).  kVec: four neighbours a thread, for n
-// a multiple of 4 (a row's four columns; 16-byte planes): 333 x 3840 in six planes 5.6 us,
+// a multiple of 4 (a row's four columns; 16-byte planes): 333 x 3840 in five planes 6.6 us,
 // single elements 10.7.
 template <bool kVec>
 __global__ __launch_bounds__(256) void linear_split_reduce(const float* __restrict__ part,
@@ -977,11 +977,9 @@ __global__ __launch_bounds__(256) void linear_split_reduce(const float* __restri
     if constexpr (kVec) {
       floatx4_t v = *reinterpret_cast<const floatx4_t*>(part + e);
       for (int s = 1; s < nslice; ++s) v += *reinterpret_cast<const floatx4_t*>(part + (int64_t)s * count + e);
-      if (bias) {
-        const int c = (int)(e % n);
+      const int c = (int)(e % n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += bias[c + i];
-      }
+      for (int i = 0; i < 4; ++i) v[i] += bias ? bias[c + i] : 0.0f;
       if (y_bf16) {
         typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
         const u32x2_t w = {bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16};

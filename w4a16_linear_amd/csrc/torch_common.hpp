@@ -41,8 +41,8 @@ inline const Tensor& tensor_of(PyObject* o, const char* name) {
 // come back without one, and nothing would say so.
 inline const Tensor& plain(const Tensor& t, const char* name) {
   TORCH_CHECK(!(t.requires_grad() && at::GradMode::is_enabled()), name,
-              " requires grad, which this call does not follow (apply_rotary turns positions "
-              "under autograd): detach it, or call under torch.no_grad()");
+              " requires grad, which this call does not follow (apply_rotary, apply_linear and "
+              "apply_adapted work under autograd): detach it, or call under torch.no_grad()");
   return t;
 }
 // A tensor whose memory this call writes: autograd learns of it, as of every in-place
