@@ -96,7 +96,7 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
 
 /*
  * dx = dy W': the gradient of the input of y = x W'^T, with W' [n][k] the bfloat16
- * values opq_dequantize* writes.  Up to 128 tokens of 4-bit codes are multiplied as
+ * values opq_dequantize* writes.  Up to 512 tokens of 4-bit codes are multiplied as
  * the codes are decoded; otherwise W' goes transposed into the workspace, then a dense
  * product makes dx.  Both are bf16 matrix-core products with float32 sums.
  *   dy     device, [m][n] bfloat16, dense;  dx  device out, [m][k] of dx_dtype, dense;

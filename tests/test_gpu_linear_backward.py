@@ -28,7 +28,8 @@ def _weight(opq, n, k, form, alpha, seed=0):
 
 @pytest.mark.parametrize("m,n,k", [(1, 32, 32), (7, 1, 32), (33, 100, 256), (64, 31, 512), (65, 264, 256), (130, 1000, 768),
                                    (257, 96, 512), (300, 520, 1024), (333, 3840, 512), (1024, 200, 256),
-                                   (5, 264, 96), (64, 1000, 160), (17, 7, 224), (16, 2000, 1280), (40, 777, 640), (3, 5000, 128)])
+                                   (5, 264, 96), (64, 1000, 160), (17, 7, 224), (16, 2000, 1280), (40, 777, 640), (3, 5000, 128),
+                                   (140, 5, 96), (256, 1023, 160), (385, 96, 32), (512, 300, 544)])
 @pytest.mark.parametrize("form", ["row", 32, 128, "3b", "5b"])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_linear_backward(L, gpu_lib, m, n, k, form, out):
@@ -50,7 +51,7 @@ def test_linear_backward(L, gpu_lib, m, n, k, form, out):
     assert torch.equal(got, L.linear_backward(dy, w, alpha, out_dtype=out))
 
 
-@pytest.mark.parametrize("m", [31, 100, 128, 129])
+@pytest.mark.parametrize("m", [31, 100, 128, 129, 256, 257, 384, 385, 512, 513])
 @pytest.mark.parametrize("form", ["row", 64, 256])
 def test_at_the_change_of_paths(L, gpu_lib, m, form):
     opq, alpha, n, k = gpu_lib, 0.73, 1100, 768

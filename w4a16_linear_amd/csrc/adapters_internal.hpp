@@ -51,11 +51,12 @@ size_t lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t
 hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream);
 
 // linear_backward.hip: the gradient of few tokens straight from 4-bit codes.  dy has rows of ldy
-// elements, n rounded up to 8 at least, zeros past n; part: the plan's bytes.  Up to 128 tokens,
-// where a call takes (this kernel / W' transposed and the dense product, us) at 8, 64, 128 and
-// 256 tokens: 3840 x 3840 16/23, 26/29, 33/42, 57/37; 11520 x 3840 27/38, 43/51, 82/80, 129/67;
-// 20480 x 3840 38/73, 61/95, 125/143, 214/108
-constexpr int64_t kBackwardShortTokens = 128;
+// elements, n rounded up to 8 at least, zeros past n; part: the plan's bytes.  Up to 512 tokens,
+// the most that one workgroup holds sums of; a call takes (so / W' transposed and the dense product,
+// us) at 8, 64, 128, 333 and 512 tokens: 3840 x 3840 16/23, 26/29, 23/42, 34/41, 43/46; 11520 x 3840
+// 27/38, 43/51, 44/80, 64/88, 79/92; 20480 x 3840 38/73, 61/95, 67/143, 96/133, 119/142.  Two
+// workgroups' tokens decode twice: 1024 would take twice the 512, against 60, 120 and 217
+constexpr int64_t kBackwardShortTokens = 512;
 struct BackwardShort {
   bool taken;
   int64_t rows, slices;  // weight rows of a slice
