@@ -146,7 +146,7 @@ def _link_extension(objs: list, verbose: bool) -> None:
     tmp = EXT_LIB + ".tmp"
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     # torch's libraries are loaded by `import torch`; libopq.so lies beside the extension
-    cmd = [cxx, "-shared", "-fPIC", "-o", tmp] + objs + ["-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu",
+    cmd = [cxx, "-shared", "-fPIC", "-o", tmp] + objs + ["-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip",
            "-ltorch_python", "-L", HERE, "-l:libopq.so", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -1,8 +1,6 @@
 // The adapters' calls on torch tensors: checks, outputs and marshalling of adapters.py
 // in C++, for the reason attention_torch.cpp gives (a call for a few tokens is a few
 // microseconds).  Nothing here computes; every call ends in libopq (include/opq_adapters.h).
-#include <ATen/ops/empty.h>
-
 #include "opq_adapters.h"
 #include "torch_common.hpp"
 
@@ -90,7 +88,7 @@ PyObject* lowrank_add(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const OnDevice on(x);
   Tensor out;
   if (a[4] == Py_None) {
-    out = at::empty({m, s.a.n}, x.options().dtype(int_of(a[5]) ? at::kBFloat16 : at::kFloat));
+    out = fresh({m, s.a.n}, int_of(a[5]) ? at::kBFloat16 : at::kFloat, x);
   } else {
     out = matrix(a[4], "out", m, s.a.n, dev);
     TORCH_CHECK_VALUE(at::has_internal_overlap(out) != at::MemOverlap::Yes, "out must not be expanded");
@@ -136,7 +134,7 @@ PyObject* lowrank_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (want_dx) {
     if (a[5] == Py_None) {
       const at::ScalarType type = dx.defined() ? dx.scalar_type() : int_of(a[6]) ? at::kBFloat16 : at::kFloat;
-      out = at::empty({m, s.a.k}, dy.options().dtype(type));
+      out = fresh({m, s.a.k}, type, dy);
     } else {
       out = matrix(a[5], "out", m, s.a.k, dev);
       TORCH_CHECK_VALUE(at::has_internal_overlap(out) != at::MemOverlap::Yes, "out must not be expanded");
@@ -151,9 +149,9 @@ PyObject* lowrank_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool bf16 = int_of(a[7]) != 0;
   Tensor down, up;
   if (want) {
-    const auto options = dy.options().dtype(bf16 ? at::kBFloat16 : at::kFloat);
-    down = at::empty({s.a.count, s.a.rank, s.a.k}, options);
-    up = at::empty({s.a.count, s.a.rank, s.a.n}, options);
+    const at::ScalarType type = bf16 ? at::kBFloat16 : at::kFloat;
+    down = fresh({s.a.count, s.a.rank, s.a.k}, type, dy);
+    up = fresh({s.a.count, s.a.rank, s.a.n}, type, dy);
   }
   size_t bytes = opq_lowrank_backward_workspace_bytes(m, s.a.k, s.a.n, s.a.rank, s.a.count);
   const Tensor ws = workspace_of(a[10], &bytes, dy);

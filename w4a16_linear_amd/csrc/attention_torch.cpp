@@ -280,7 +280,7 @@ PyObject* pages_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor t[2];
   PyObject* given[2] = {nullptr, nullptr};
   if (a[4] == Py_None) {
-    t[0] = at::empty(table.sizes(), table.options());
+    t[0] = fresh(table.sizes(), at::kInt, table);
   } else {
     t[0] = tensor_of(given[0] = a[4], "out");
     dense(t[0], "out", at::kInt, table.sizes(), table.device());
@@ -288,7 +288,7 @@ PyObject* pages_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       "out must be page_table itself or share no memory with it");
     TORCH_CHECK_VALUE(!share(t[0], lens), "out must not share memory with lens");
   }
-  t[1] = at::empty({1}, table.options());
+  t[1] = fresh({1}, at::kInt, table);
   size_t bytes = opq_pages_workspace_bytes(rows, pages);
   const Tensor ws = workspace_of(a[5], &bytes, table);
   check("opq_pages_resize",
@@ -316,15 +316,15 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor t[5];
   PyObject* given[5] = {};
   if (a[5] == Py_None) {
-    t[0] = at::empty({made, columns}, table.options());
+    t[0] = fresh({made, columns}, at::kInt, table);
   } else {
     t[0] = tensor_of(given[0] = a[5], "out");
     dense(t[0], "out", at::kInt, {made, columns}, table.device());
     TORCH_CHECK_VALUE(!share(t[0], table) && !share(t[0], lens) && !share(t[0], parents),
                       "out must not share memory with page_table, lens or parents: rows are copied from rows");
   }
-  for (int i = 1; i < 4; ++i) t[i] = at::empty({made}, table.options());
-  t[4] = at::empty({1}, table.options());
+  for (int i = 1; i < 4; ++i) t[i] = fresh({made}, at::kInt, table);
+  t[4] = fresh({1}, at::kInt, table);
   size_t bytes = opq_pages_workspace_bytes(made, pages);
   const Tensor ws = workspace_of(a[6], &bytes, table);
   check("opq_pages_fork",
@@ -346,7 +346,7 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor t[4];
   PyObject* given[4] = {};
   if (a[2] == Py_None) {
-    t[0] = at::empty(table.sizes(), table.options());
+    t[0] = fresh(table.sizes(), at::kInt, table);
   } else {
     t[0] = tensor_of(given[0] = a[2], "out");
     dense(t[0], "out", at::kInt, table.sizes(), table.device());
@@ -354,9 +354,9 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       "out must be page_table itself or share no memory with it");
   }
   const int64_t moves = std::max<int64_t>(0, std::min(pages / 2, rows * columns));
-  t[1] = at::empty({moves}, table.options());
-  t[2] = at::empty({moves}, table.options());
-  t[3] = at::empty({1}, table.options());
+  t[1] = fresh({moves}, at::kInt, table);
+  t[2] = fresh({moves}, at::kInt, table);
+  t[3] = fresh({1}, at::kInt, table);
   size_t bytes = opq_pages_workspace_bytes(rows, pages);
   const Tensor ws = workspace_of(a[3], &bytes, table);
   check("opq_pages_compact",
@@ -394,8 +394,7 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* parents = a[4] == Py_None ? nullptr : dense(a[4], "parents", at::kInt, {batch, draft}, dev);
   const void* counts = a[5] == Py_None ? nullptr : dense(a[5], "counts", at::kInt, {batch}, dev);
   const OnDevice on(p);
-  const auto options = p.options().dtype(at::kInt);
-  Tensor t[3] = {at::empty({batch, draft}, options), at::empty({batch}, options), at::empty({batch}, options)};
+  Tensor t[3] = {fresh({batch, draft}, at::kInt, p), fresh({batch}, at::kInt, p), fresh({batch}, at::kInt, p)};
   size_t bytes = opq_verify_drafts_workspace_bytes(batch, vocab);
   const Tensor ws = workspace_of(a[6], &bytes, p);
   // a draft of one token has no draft probabilities to point to

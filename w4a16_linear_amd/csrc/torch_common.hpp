@@ -5,6 +5,7 @@
 #include <ATen/MemoryOverlap.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -104,12 +105,18 @@ inline void arguments(Py_ssize_t n, Py_ssize_t want) {
   TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n);
 }
 
+// A dense tensor of the allocator's on `like`'s device: what at::empty comes to, without the
+// dispatcher and the options (pages_fork, with six of them: 7.8 to 6.7 us of host time).
+inline Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+  return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);
+}
+
 // A workspace of the caller's, or of the allocator: of the current stream, so calls on
 // different streams do not share one.
 inline Tensor workspace_of(PyObject* o, size_t* bytes, const Tensor& like) {
   if (o == Py_None) {
     if (*bytes == 0) return Tensor();
-    return at::empty({(int64_t)*bytes}, like.options().dtype(at::kByte));
+    return fresh({(int64_t)*bytes}, at::kByte, like);
   }
   const Tensor& ws = tensor_of(o, "workspace");
   TORCH_CHECK_VALUE(ws.is_contiguous() && ws.device() == like.device(),
