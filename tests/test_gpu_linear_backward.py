@@ -93,3 +93,37 @@ def test_out_beside_dy_not_over_it(L, gpu_lib, m):
     for out in (held[:m], held[1:m + 1]):
         with pytest.raises(ValueError, match="share"):
             L.linear_backward(held[:m], w, 0.73, out=out)
+
+
+def test_every_path_in_a_graph_and_on_a_stream(L, gpu_lib):
+    """Captured, replayed on new contents between eager calls, and beside calls on another stream."""
+    opq, n, k = gpu_lib, 1100, 768
+    w = _weight(opq, n, k, "row", 0.73)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    sizes = (8, 64, 100, 300, 512, 600)
+    dys = [torch.randn((m, n), generator=g, device=DEV).to(torch.bfloat16) for m in sizes]
+    outs = [torch.empty((m, k), dtype=torch.bfloat16, device=DEV) for m in sizes]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for dy, out in zip(dys, outs):
+            L.linear_backward(dy, w, 0.73, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for dy, out in zip(dys, outs):
+            L.linear_backward(dy, w, 0.73, out=out)
+    for _ in range(3):
+        for dy in dys:
+            dy.copy_(torch.randn(dy.shape, generator=g, device=DEV))
+        want = [L.linear_backward(dy, w, 0.73) for dy in dys]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            beside = [L.linear_backward(dy, w, 0.73) for dy in dys]
+        graph.replay()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, beside, outs):
+            assert torch.equal(a, b) and torch.equal(a, c)
