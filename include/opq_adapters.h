@@ -53,8 +53,8 @@ size_t opq_lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank
  *   workspace  at least opq_lowrank_workspace_bytes(m, k, n, rank) bytes, no
  *          initialisation; calls that may overlap need their own
  * Products of bfloat16 are summed in float32.  For the second product s_i D_i x is
- * taken in two bfloat16 parts (16 bits) for a bfloat16 out and in three (24 bits, all of
- * a float32) for a float32 one; the sum with y is float32, rounded once.  A token's result
+ * taken in three bfloat16 parts (24 bits, all of a float32); the sum with y is float32,
+ * rounded once: a bfloat16 out is the float32 one rounded.  A token's result
  * does not depend on the other tokens of the call, whose number sets in how many pieces
  * sums over k are taken; results repeat bit for bit.
  * m up to 2^22, k and n up to 2^20, m * k and m * n up to 2^39 with their strides,
@@ -84,8 +84,8 @@ size_t opq_lowrank_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int
  *   d_down, d_up  device out, dense [count][rank][k], [count][rank][n] of grad_dtype;
  *           both NULL: not wanted
  *   workspace  as for opq_lowrank_add
- * Roundings as opq_lowrank_add: e and h enter their products in two bfloat16 parts for
- * bfloat16 results, in three for float32 ones; sums are float32 and in a fixed order.
+ * Roundings as opq_lowrank_add: e and h enter their products with all their 24 bits;
+ * sums are float32 and in a fixed order.
  * Limits as opq_lowrank_add, and count up to 1024.  Errors as opq_lowrank_add.
  */
 int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_t dy_stride,

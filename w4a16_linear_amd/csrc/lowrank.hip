@@ -25,10 +25,11 @@
 // columns are independent in the matrix product, so what is in another token's row
 // never reaches a token.
 //
-// Rounding: c is float32.  Entering a second product it is cut into bfloat16
-// parts: two (16 bits) where the result is bfloat16 itself, three (24 bits, all
-// of it) where it is float32.  Parts are cut by truncation, so none overflows;
-// the last one is rounded.
+// Rounding: c is float32.  Entering a second product it is cut into three bfloat16
+// parts, all of its 24 bits, whatever the result's type: a bfloat16 result is the float32
+// one rounded.  (With two parts, 16 bits: 4096 tokens, 3840 -> 20480, rank 64 99 us for
+// 102; one token, rank 8 7.7 for 8.0; gradients of one adapter 77 for 77.6.)  Parts are
+// cut by truncation, so none overflows; the last one is rounded.
 #include <algorithm>
 
 #include "adapters_internal.hpp"
@@ -41,6 +42,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kBlockTokens = kWave;  // tokens a wave groups: one a lane
 constexpr int kNoAdapter = -1, kNoToken = -2;
+constexpr int kCuts = 3;  // bfloat16 parts of a float32
 
 // -------------------------------------------------------------- token tiles
 
@@ -130,19 +132,18 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
   }
 }
 
-// v as a sum of PARTS bfloat16 values, the first ones cut off (an infinity or NaN is
-// all in the first), the last one rounded.
-template <int PARTS>
-__device__ __forceinline__ void split(float v, uint32_t (&part)[PARTS]) {
+// v as a sum of bfloat16 values, the first ones cut off (an infinity or NaN is all in
+// the first), the last one rounded.
+__device__ __forceinline__ void split(float v, uint32_t (&part)[kCuts]) {
   const bool finite = (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
 #pragma unroll
-  for (int p = 0; p < PARTS - 1; ++p) {
+  for (int p = 0; p < kCuts - 1; ++p) {
     uint32_t b = __float_as_uint(v) & 0xFFFF0000u;
     if (p == 0 && v != v) b = 0x7FC00000u;
     part[p] = b >> 16;
     v = finite ? v - __uint_as_float(b) : 0.0f;
   }
-  part[PARTS - 1] = bf16_rne(v);
+  part[kCuts - 1] = bf16_rne(v);
 }
 
 template <bool BF16>
@@ -544,9 +545,9 @@ __device__ __forceinline__ void unpack(const Base<BF16>& b, int i, float (&v)[8]
 }
 
 constexpr int kMade = 4;  // tiles whose operands are in LDS together: one a wave
-template <int RS, bool OUT_BF16>
+template <int RS>
 struct ExpandShared {
-  uint4 c[kMade][RS][OUT_BF16 ? 2 : 3][kWave];
+  uint4 c[kMade][RS][kCuts][kWave];
 };
 
 // Workgroup (512 columns, share of the block's tiles, block of tokens), a wave
@@ -559,8 +560,7 @@ struct ExpandShared {
 // pass the caches by, which are for the stack and c (4096 tokens, 3840 -> 20480, rank 64:
 // 111 us with ordinary loads and stores, 99 so); one block of tokens is small enough for both.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
-__device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT_BF16>& s, int bx, int by, int bz) {
-  constexpr int PARTS = OUT_BF16 ? 2 : 3;
+__device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS>& s, int bx, int by, int bz) {
   constexpr int kAhead = SINGLE ? 1 : RS > 1 && BASE_BF16 ? 4 : 2;  // by registers
   const int64_t t0 = (int64_t)bz * kBlockTokens;
   const int id = block_id(a.index + t0, (int)min((int64_t)kBlockTokens, a.m - t0), a.count);
@@ -643,14 +643,14 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
 #pragma unroll
       for (int k = 0; k < RS; ++k) {
         const int r = k * 32 + q * 8;
-        uint32_t cut[8][PARTS];
+        uint32_t cut[8][kCuts];
         float v[8] = {};
         if (o.id >= 0 && c < o.size && r < a.rank)
           scaled(a.part + token * a.rank + r, plane, a.slices, scale, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) split<PARTS>(v[e], cut[e]);
+        for (int e = 0; e < 8; ++e) split(v[e], cut[e]);
 #pragma unroll
-        for (int e = 0; e < PARTS; ++e)
+        for (int e = 0; e < kCuts; ++e)
           s.c[wave][k][e][lane] = make_uint4(cut[0][e] | cut[1][e] << 16, cut[2][e] | cut[3][e] << 16,
                                              cut[4][e] | cut[5][e] << 16, cut[6][e] | cut[7][e] << 16);
       }
@@ -668,7 +668,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS, OUT
 #pragma unroll
         for (int k = 0; k < RS; ++k)
 #pragma unroll
-          for (int e = 0; e < PARTS; ++e) {
+          for (int e = 0; e < kCuts; ++e) {
             const bf16x8_t h = operand(s.c[w][k][e][lane]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -703,7 +703,7 @@ constexpr int expand_waves() {
 // SINGLE: one block of tokens, whose workgroup y takes the tile that token y leads, if any.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
 __global__ __launch_bounds__(kThreads, (expand_waves<RS, BASE_BF16, SINGLE>())) void lowrank_expand(ExpandArgs a) {
-  __shared__ ExpandShared<RS, OUT_BF16> s;
+  __shared__ ExpandShared<RS> s;
   expand<RS, BASE_BF16, OUT_BF16, SINGLE>(a, s, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
@@ -731,7 +731,7 @@ struct FewArgs {
 // (3840 -> 3840, rank 8, 1 token: 7.7 us, of which the second round of loads is 2).
 template <int RT, bool BASE_BF16, bool OUT_BF16>
 __global__ __launch_bounds__(kFewThreads) void lowrank_add_few(FewArgs a) {
-  constexpr int PARTS = OUT_BF16 ? 2 : 3, kDepth = BASE_BF16 ? 4 : 2;  // by registers
+  constexpr int kDepth = BASE_BF16 ? 4 : 2;  // by registers
   __shared__ float4 s_red[kFewWaves][RT][kWave];
   __shared__ float4 s_sum[RT][kWave];
   const int id = block_id(a.index, a.m, a.count);
@@ -820,15 +820,15 @@ __global__ __launch_bounds__(kFewThreads) void lowrank_add_few(FewArgs a) {
       v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
       v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
     }
-    uint32_t cut[8][PARTS];
+    uint32_t cut[8][kCuts];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split<PARTS>(v[e] * scale, cut[e]);
+    for (int e = 0; e < 8; ++e) split(v[e] * scale, cut[e]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) rows[e] = q * 8 < a.rank ? rows[e] : zero16();
     transpose8(rows, p);
     if (!BASE_BF16) load_base();
 #pragma unroll
-    for (int e = 0; e < PARTS; ++e) {
+    for (int e = 0; e < kCuts; ++e) {
       const bf16x8_t h = operand(make_uint4(cut[0][e] | cut[1][e] << 16, cut[2][e] | cut[3][e] << 16,
                                             cut[4][e] | cut[5][e] << 16, cut[6][e] | cut[7][e] << 16));
 #pragma unroll
@@ -1028,7 +1028,6 @@ struct OperandArgs {
 // s c in bfloat16 parts, transposed, in the order of grad's operands: of 32 places and 16
 // ranks, lane (c, q) has rank c, places 8 q ..., and its 16 bytes lie beside its neighbours'.
 // A thread makes eight ranks of one place; `group`: 256 places of eight ranks and a side.
-template <int PARTS>
 __device__ __forceinline__ void operands(const OperandArgs& a, int64_t group) {
   const int64_t groups = (a.cap + kThreads - 1) / kThreads;
   const int64_t j = group % groups * kThreads + threadIdx.x;
@@ -1041,29 +1040,26 @@ __device__ __forceinline__ void operands(const OperandArgs& a, int64_t group) {
     scaled(a.part[side] + (int64_t)t * a.rank + r, a.m * a.rank, a.slices[side], a.scale[a.index[t]], v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    uint32_t cut[PARTS];
-    split<PARTS>(v[e], cut);
+    uint32_t cut[kCuts];
+    split(v[e], cut);
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) a.out[side][operand_at(a.rank, a.cap, k, r + e, j)] = (uint16_t)cut[k];
+    for (int k = 0; k < kCuts; ++k) a.out[side][operand_at(a.rank, a.cap, k, r + e, j)] = (uint16_t)cut[k];
   }
 }
 
-template <int PARTS>
-__global__ __launch_bounds__(kThreads) void lowrank_operands(OperandArgs a) {
-  operands<PARTS>(a, blockIdx.x);
-}
+__global__ __launch_bounds__(kThreads) void lowrank_operands(OperandArgs a) { operands(a, blockIdx.x); }
 
 // The input's gradient and the operands of the adapters' own: workgroups x < columns expand,
 // the others make operands (a launch less).
-template <int RS, bool BF16, bool GRAD_BF16>
+template <int RS, bool BF16>
 __global__ __launch_bounds__(kThreads, (expand_waves<RS, BF16, false>())) void lowrank_expand_operands(
     ExpandArgs a, OperandArgs o, int columns) {
-  __shared__ ExpandShared<RS, BF16> s;
+  __shared__ ExpandShared<RS> s;
   if ((int)blockIdx.x < columns) {
     expand<RS, BF16, BF16, false>(a, s, blockIdx.x, 0, blockIdx.y);
     return;
   }
-  operands<GRAD_BF16 ? 2 : 3>(o, (int64_t)blockIdx.y * ((int)gridDim.x - columns) + ((int)blockIdx.x - columns));
+  operands(o, (int64_t)blockIdx.y * ((int)gridDim.x - columns) + ((int)blockIdx.x - columns));
 }
 
 struct GradSide {
@@ -1089,7 +1085,6 @@ struct GradArgs {
 // tiles of the rank, at most 4 (rank 128 takes two workgroups, by registers).
 template <int RT, bool OUT_BF16>
 __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
-  constexpr int PARTS = OUT_BF16 ? 2 : 3;
   constexpr int kOnce = RT < 2 ? RT : 2;  // row tiles in LDS together
   __shared__ float s_red[kWaves][kOnce][8][4][kWave];
   const int item = blockIdx.y;
@@ -1120,16 +1115,16 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
     uint4 rows[8], cols[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) rows[e] = t[e] >= 0 ? load16(v + t[e] * g.stride) : zero16();
-    bf16x8_t h[RT][PARTS];
+    bf16x8_t h[RT][kCuts];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) h[i][k] = operand(load16(row[i] + k * plane + at * 16));
+      for (int k = 0; k < kCuts; ++k) h[i][k] = operand(load16(row[i] + k * plane + at * 16));
     transpose8(rows, cols);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k)
+      for (int k = 0; k < kCuts; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h[i][k], operand(cols[j]), acc[i][j], 0, 0, 0);
@@ -1223,8 +1218,8 @@ BackwardPlan backward_plan(int64_t m, int64_t k, int64_t n, int64_t rank, int64_
   b.part_h = take((size_t)b.h.slices * m * rank * 4);
   b.part_e = take((size_t)b.e.slices * m * rank * 4);
   const size_t ranks = (size_t)(rank + 15) / 16 * 16;  // whole tiles
-  b.operand_h = take(3 * ranks * b.cap * 2);
-  b.operand_e = take(3 * ranks * b.cap * 2);
+  b.operand_h = take(kCuts * ranks * b.cap * 2);
+  b.operand_e = take(kCuts * ranks * b.cap * 2);
   b.sums_down = take((size_t)b.slots * rank * k * 4);
   b.sums_up = take((size_t)b.slots * rank * n * 4);
   b.lists = take((size_t)(b.cap + 64 + 4 * b.items + 2 * count) * 4);
@@ -1246,27 +1241,20 @@ hipError_t launch_grad(const GradArgs& g, bool bf16, int64_t items, hipStream_t 
 }
 
 template <int RS>
-hipError_t launch_both_of(const ExpandArgs& a, const OperandArgs& o, bool bf16, bool grad_bf16, dim3 grid,
-                          int columns, hipStream_t stream) {
-  if (bf16 && grad_bf16)
-    hipLaunchKernelGGL((lowrank_expand_operands<RS, true, true>), grid, dim3(kThreads), 0, stream, a, o, columns);
-  else if (bf16)
-    hipLaunchKernelGGL((lowrank_expand_operands<RS, true, false>), grid, dim3(kThreads), 0, stream, a, o, columns);
-  else if (grad_bf16)
-    hipLaunchKernelGGL((lowrank_expand_operands<RS, false, true>), grid, dim3(kThreads), 0, stream, a, o, columns);
-  else
-    hipLaunchKernelGGL((lowrank_expand_operands<RS, false, false>), grid, dim3(kThreads), 0, stream, a, o, columns);
+hipError_t launch_both_of(const ExpandArgs& a, const OperandArgs& o, bool bf16, dim3 grid, int columns,
+                          hipStream_t stream) {
+  if (bf16) hipLaunchKernelGGL((lowrank_expand_operands<RS, true>), grid, dim3(kThreads), 0, stream, a, o, columns);
+  else hipLaunchKernelGGL((lowrank_expand_operands<RS, false>), grid, dim3(kThreads), 0, stream, a, o, columns);
   return hipGetLastError();
 }
 
-hipError_t launch_both(const ExpandArgs& a, const OperandArgs& o, bool bf16, bool grad_bf16, int64_t groups,
-                       hipStream_t stream) {
+hipError_t launch_both(const ExpandArgs& a, const OperandArgs& o, bool bf16, int64_t groups, hipStream_t stream) {
   const int columns = (a.d + 511) / 512;
   const int64_t blocks = blocks_of(a.m);
   const dim3 grid((unsigned)(columns + (groups + blocks - 1) / blocks), (unsigned)blocks);
-  return a.rank <= 32 ? launch_both_of<1>(a, o, bf16, grad_bf16, grid, columns, stream)
-         : a.rank <= 64 ? launch_both_of<2>(a, o, bf16, grad_bf16, grid, columns, stream)
-                        : launch_both_of<4>(a, o, bf16, grad_bf16, grid, columns, stream);
+  return a.rank <= 32 ? launch_both_of<1>(a, o, bf16, grid, columns, stream)
+         : a.rank <= 64 ? launch_both_of<2>(a, o, bf16, grid, columns, stream)
+                        : launch_both_of<4>(a, o, bf16, grid, columns, stream);
 }
 
 }  // namespace
@@ -1349,10 +1337,9 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
   if (c.m > 0) {  // else there is no item, and the join writes zeros
     const int64_t groups = (b.cap + kThreads - 1) / kThreads * (rank / 8) * 2;
     if (c.dx_out) {
-      err = launch_both(x, o, c.dx_bf16, c.grad_bf16, groups, stream);
+      err = launch_both(x, o, c.dx_bf16, groups, stream);
     } else {
-      if (c.grad_bf16) hipLaunchKernelGGL(lowrank_operands<2>, dim3((unsigned)groups), dim3(kThreads), 0, stream, o);
-      else hipLaunchKernelGGL(lowrank_operands<3>, dim3((unsigned)groups), dim3(kThreads), 0, stream, o);
+      hipLaunchKernelGGL(lowrank_operands, dim3((unsigned)groups), dim3(kThreads), 0, stream, o);
       err = hipGetLastError();
     }
     if (err != hipSuccess) return err;
