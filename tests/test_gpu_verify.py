@@ -178,3 +178,47 @@ def test_refusals(A):
             call()
     with pytest.raises(RuntimeError):
         A.verify_drafts(p.requires_grad_(), t, u)
+
+
+def _sequence(p, t, u, parents):
+    one = [torch.tensor(x, device=DEV)[None] for x in (p, t, u, parents)]
+    return one[0].float(), one[1].to(torch.int32), one[2].float(), one[3].to(torch.int32)
+
+
+def test_a_token_before_its_parent_is_nobodys_sibling(A):
+    """Entries under a node that do not come after it were never tested: a later token equal to one
+    of them is tested as any other."""
+    p = [[0.0, 0.0, 1.0, 0.0], [0.25] * 4, [0.0, 0.8, 0.0, 0.2], [0.25] * 4, [0.25] * 4]
+    s = _sequence(p, [0, 1, 2, 3, 1], [0.5, 0.5, 0.1, 0.9, 0.1], [-1, 2, 0, 2, 2])
+    assert SO.verify(p, [0, 1, 2, 3, 1], [0.5, 0.5, 0.1, 0.9, 0.1], None, [-1, 2, 0, 2, 2])[0] == [0, 2, 4, -1, -1]
+    _check(A.verify_drafts(*s[:3], parents=s[3]), *s[:3], None, s[3])
+    even = [[1 / 16] * 16] * 5
+    s = _sequence(even, [0, 7, 3, 9, 7], [0.5, 0.5, 0.01, 0.9, 0.01], [-1, 2, 0, 2, 2])
+    _check(A.verify_drafts(*s[:3], parents=s[3]), *s[:3], None, s[3])
+    # a node's children in its own 64 tokens and in the next ones, equal to a token before the
+    # node (not tested) and to one after it (tested)
+    for second in (7, 9):
+        parents, t = [-1] * 130, [5] * 130
+        parents[3], t[3] = 20, 7
+        parents[20], t[20] = 0, 1
+        parents[40], t[40] = 20, 9
+        parents[100], t[100] = 20, second
+        parents[129], t[129] = 20, 2
+        u = [0.5] + [0.9] * 129
+        u[20] = u[100] = 0.01
+        s = _sequence([[1 / 16] * 16] * 130, t, u, parents)
+        _check(A.verify_drafts(*s[:3], parents=s[3]), *s[:3], None, s[3])
+
+
+@pytest.mark.parametrize("draft", [5, 63, 130])
+def test_trees_with_parents_on_either_side(A, draft):
+    rng = np.random.default_rng(draft)
+    batch, vocab = 96, 6
+    p = torch.from_numpy(rng.dirichlet(np.ones(vocab), (batch, draft)).astype(np.float32)).to(DEV)
+    t = torch.from_numpy(rng.integers(0, vocab, (batch, draft)).astype(np.int32)).to(DEV)
+    u = np.where(np.arange(draft) % 9 == 0, 0.01, 0.2 + 0.6 * rng.random((batch, draft))).astype(np.float32)
+    u = torch.from_numpy(u).to(DEV)
+    at = np.arange(draft) // 9 * 9                           # every ninth hangs under the ninth before, the rest beside it
+    par = np.where(np.arange(draft) % 9 == 0, at - 9, at + 9 * rng.integers(0, 2, (batch, draft))).astype(np.int32)
+    parents = torch.from_numpy(par).to(DEV)
+    _check(A.verify_drafts(p, t, u, parents=parents), p, t, u, None, parents)

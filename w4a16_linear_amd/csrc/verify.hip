@@ -8,8 +8,8 @@
 // sequence, finds the piece that u0 falls into and the token in it.
 //
 // Sums are float64: a float32 sum over 10^5 weights is off by 10^-6 of the whole, the
-// weight of many tokens of a long tail.  Acceptance is a product of two float32 values in
-// float64, which is exact.
+// weight of many tokens of a long tail.  u q is a product of two float32 values in float64,
+// which is exact; Z, a float64 sum of float32 values, and u Z are rounded.
 #include <algorithm>
 
 #include "attention_internal.hpp"
@@ -73,12 +73,12 @@ __device__ int walk(const VerifyArgs& a, int b, int count, int32_t* kept, Found*
       todo = at == 63 ? 0 : ~uint64_t(0) << (at + 1);
       double pd = readlane_f(px, at);
       const double ud = readlane_f(u, at), qd = readlane_f(qx, at);
-      if (!a.q && tested) {  // an earlier sibling's token again counts nothing
+      if (!a.q && tested) {  // an earlier sibling's token again counts nothing; siblings come after the node
         const int x = __builtin_amdgcn_readlane(token, at);
-        bool again = __ballot(in && lane < at && parent == node && token == x);
+        bool again = __ballot(in && t > node && lane < at && parent == node && token == x);
         for (int s0 = node / kWave * kWave; s0 < t0 && !again; s0 += kWave) {
           const int s = s0 + lane;
-          again = __ballot(s > 0 && (parents ? parents[s] : s - 1) == node && tokens[s] == x);
+          again = __ballot(s > node && (parents ? parents[s] : s - 1) == node && tokens[s] == x);
         }
         if (again) pd = 0.0;
       }
