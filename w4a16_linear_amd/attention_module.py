@@ -166,8 +166,15 @@ class PagedSequences:
     the table, so have the same pages and page size): rows grow, are forked and dropped, their
     pages taken, freed and drawn together.  Nothing here waits for the GPU; `missing` (int32 [1], on
     the device) says after each call how many entries no free page was left for.  A row holds up to
-    columns * page tokens, which nothing here counts: tokens past them have no slot.  Rows grow; one
-    that is cut back into a page that others name has to be forked before it is written again.
+    columns * page tokens.  Rows grow; one that is cut back into a page that others name has to be
+    forked before it is written again.
+
+    `lens` counts the tokens that pages hold, never more: a row that a fork found no page for ends
+    with its last full page, and accepted tokens end before the first that had no slot (for want of a
+    free page, or past the row's columns).  `lost` (int32 [rows], on the device) is how many tokens a
+    row is short of by that; it goes with the row's forks and ends with the row, so one look at it
+    after any number of steps tells which rows went wrong.  Whoever runs those tokens again sets it
+    back to 0.
 
         seqs = PagedSequences(rows=32, columns=128, pages=cache.pages, page=cache.page)
         seqs.room(draft)                                    # pages for the tokens to come
@@ -182,6 +189,7 @@ class PagedSequences:
         self.page_table = torch.full((rows, columns), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(rows, dtype=torch.int32, device=device)
         self.missing = torch.zeros(1, dtype=torch.int32, device=device)
+        self.lost = torch.zeros(rows, dtype=torch.int32, device=device)
 
     def _caches(self, caches: Sequence[A.PagedCache]) -> None:
         for cache in caches:
@@ -196,21 +204,40 @@ class PagedSequences:
 
     def accept(self, caches: Sequence[A.PagedCache], kept: torch.Tensor, count: torch.Tensor) -> None:
         """Keep verified tokens (verify_drafts' kept and count) in every cache, and free the pages
-        that only the others needed."""
+        that only the others needed.  Of tokens that have no slot, and those after them, none is kept."""
         self._caches(caches)
         for cache in caches:
             OPQAttention.accept(cache, self.page_table, self.lens, kept)
+        if kept.shape[1]:
+            slots = token_slots(self.page_table, torch.where(kept >= 0, self.lens[:, None] + kept, -1), self.page, self.pages)
+            places = torch.arange(kept.shape[1], dtype=torch.int32, device=kept.device)
+            first = torch.where((kept >= 0) & (slots < 0), places, 2 ** 31 - 1).amin(1)   # without a slot
+            stored = torch.minimum(count, first)
+            self.lost, count = self.lost + (count - stored), stored
         self.lens = self.lens + count
         self.room(0)
 
     def fork(self, caches: Sequence[A.PagedCache], parents: torch.Tensor) -> torch.Tensor:
         """Row i becomes a copy of row parents[i] (int32; -1: an empty row), its tokens shared
-        page by page but for a last page that is not full; returns `missing`."""
+        page by page but for a last page that is not full; returns `missing`, the rows that
+        end with their last full page because no page was free."""
         self._caches(caches)
-        self.page_table, self.lens, src, dst, self.missing = A.pages_fork(
+        rows = self.lost.shape[0]
+        self.page_table, lens, src, dst, self.missing = A.pages_fork(
             self.page_table, self.lens, parents, self.pages, self.page)
         for cache in caches:
             A.cache_copy_pages(cache, src, dst)
+        if rows:
+            kept = self.lost[parents.clamp(0, rows - 1).long()]
+            self.lost = torch.where((parents >= 0) & (parents < rows), kept, 0)
+        else:
+            self.lost = torch.zeros_like(lens)
+        if self.page_table.shape[1]:
+            full = torch.div((lens - 1).clamp_min(0), self.page, rounding_mode="floor")   # pages before the last
+            last = torch.gather(self.page_table, 1, full[:, None].long())[:, 0]
+            held = torch.where((lens > 0) & (last < 0), full * self.page, lens)
+            self.lost, lens = self.lost + (lens - held), held
+        self.lens = lens
         return self.missing
 
     def compact(self, caches: Sequence[A.PagedCache]) -> torch.Tensor:
