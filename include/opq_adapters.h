@@ -104,7 +104,7 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
  *   workspace  at least opq_linear_backward_workspace_bytes(m, n, k) bytes, no
  *          initialisation; calls that may overlap need their own
  * The other arguments as in opq_linear, opq_linear_bits and opq_linear_grouped; n up to
- * 65536, k up to 65536 and a multiple of 32, m up to 2^22, m * n and m * k up to 2^39.
+ * 65536 (the sums of more rows are those of blocks of them, added), k up to 65536 and a multiple of 32, m up to 2^22, m * n and m * k up to 2^39.
  * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALPHA, OPQ_ERR_ALIGN, OPQ_ERR_DTYPE,
  * OPQ_ERR_WORKSPACE, OPQ_ERR_UNSUPPORTED, OPQ_ERR_HIP.
  */

@@ -127,3 +127,59 @@ def test_every_path_in_a_graph_and_on_a_stream(L, gpu_lib):
         torch.cuda.synchronize()
         for a, b, c in zip(want, beside, outs):
             assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("m", [3, 100, 600])
+@pytest.mark.parametrize("form", ["row", 128, "5b"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_a_vocabulary_of_rows(L, gpu_lib, m, form, out):
+    """More rows than one call of the library takes, as the head of a large vocabulary has."""
+    opq, alpha, n, k = gpu_lib, 0.73, 2 * 65536 + 1000, 256
+    w = _weight(opq, n, k, form, alpha)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m)
+    dy = torch.randn((m, n), generator=g, device=DEV).to(torch.bfloat16)
+    got = L.linear_backward(dy, w, alpha, out_dtype=out)
+    full = opq.dequantize(w, alpha).double()
+    want = dy.double() @ full
+    bound = (n + 64) * 2.0 ** -24 * (dy.double().abs() @ full.abs())
+    bound = bound + (2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -24) * (want.abs() + bound)
+    assert got.dtype == out and ((got.double() - want).abs() <= bound).all()
+    # exact sums: every row counts once, and rows of blocks are not mixed up
+    one = torch.zeros((m, n), dtype=torch.bfloat16, device=DEV)
+    at = torch.randint(0, n, (m,), generator=g, device=DEV)
+    one[torch.arange(m, device=DEV), at] = 2.0
+    held = torch.empty((m, k), dtype=out, device=DEV)
+    room = torch.empty(L.linear_backward_workspace_bytes(m, n, k), dtype=torch.uint8, device=DEV)
+    assert L.linear_backward(one, w, alpha, out=held, workspace=room) is held
+    assert torch.equal(held.double(), 2.0 * full[at])
+    if room.numel():
+        with pytest.raises(ValueError):
+            L.linear_backward(one, w, alpha, workspace=room[:1])
+
+
+def test_more_tokens_than_one_call(L, gpu_lib):
+    w = _weight(gpu_lib, 8, 32, "row", 0.73)
+    m = (1 << 22) + 77
+    dy = torch.zeros((m, 8), dtype=torch.bfloat16, device=DEV)
+    at = torch.arange(0, m, 4099, device=DEV)
+    at = torch.cat((at, torch.tensor([m - 1, m - 77, m - 78], device=DEV)))
+    dy[at, at % 8] = 2.0
+    got = L.linear_backward(dy, w, 0.73)
+    want = torch.zeros((m, 32), dtype=torch.bfloat16, device=DEV)
+    want[at] = (2.0 * gpu_lib.dequantize(w, 0.73).double()[at % 8]).to(torch.bfloat16)
+    assert torch.equal(got, want)
+
+
+def test_a_layer_with_a_vocabulary(L, gpu_lib):
+    from w4a16_linear_amd.module import AdaptedLinear, OPQLinear
+    layer = OPQLinear.from_linear(torch.nn.Linear(64, 70000, bias=False).to(DEV))
+    x = torch.randn((5, 64), device=DEV, requires_grad=True)
+    dy = torch.randn((5, 70000), device=DEV)
+    want = dy.to(torch.bfloat16).double() @ layer.dequantized_weight().double()
+    bound = (70000 + 64) * 2.0 ** -24 * (dy.to(torch.bfloat16).double().abs() @ layer.dequantized_weight().double().abs())
+    (got,) = torch.autograd.grad(layer(x), x, dy)
+    assert ((got.double() - want).abs() <= bound + 2.0 ** -24 * want.abs()).all()
+    adapted = AdaptedLinear(layer, 2, 8)                    # up is zeros: the same gradient
+    (got2,) = torch.autograd.grad(adapted(x, torch.zeros(5, dtype=torch.int32, device=DEV)), x, dy)
+    assert torch.equal(got2, got)

@@ -104,8 +104,15 @@ def lowrank_backward(dy: torch.Tensor, x: torch.Tensor, adapters: Adapters, inde
 
 # ------------------------------------------------------- through the projection
 
+# what one call of the library takes; more tokens or weight rows go to it in blocks
+_TOKENS, _ROWS = 1 << 22, 1 << 16
+
+
 def linear_backward_workspace_bytes(m: int, n: int, k: int) -> int:
-    return int(load().opq_linear_backward_workspace_bytes(m, n, k))
+    """Workspace bytes of linear_backward: of its largest block."""
+    sizes = [(a, b) for a in {min(m, _TOKENS), m % _TOKENS if m > _TOKENS else 0}
+             for b in {min(n, _ROWS), n % _ROWS if n > _ROWS else 0}]
+    return max(int(load().opq_linear_backward_workspace_bytes(a, b, k)) for a, b in sizes)
 
 
 def _check_rows(qw, n: int, k: int) -> None:
@@ -116,13 +123,25 @@ def _check_rows(qw, n: int, k: int) -> None:
         raise ValueError(f"weight buffers do not match n={n}, k={k}")
 
 
+def _backward_call(dy, weight, alpha, out, workspace) -> None:
+    """One call of the library, its tensors checked, on their device."""
+    (m, n), k = dy.shape, weight.shape[1]
+    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    name = "opq_linear_backward" + ("_bits" if isinstance(weight, opq.BitsWeight) else
+                                    "_grouped" if isinstance(weight, opq.GroupedWeight) else "")
+    _check(name, getattr(load(), name)(
+        dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(), weight[2].data_ptr(), m, n, k, *weight[3:], alpha,
+        out.data_ptr(), OPQ_BF16 if out.dtype == torch.bfloat16 else OPQ_F32, opq._ptr(workspace), room,
+        opq._stream(dy.device)))
+
+
 def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.Tensor] = None,
                     out_dtype: torch.dtype = torch.bfloat16,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx [m, k] = dy [m, n] W', the gradient of opq.linear's x: dy bfloat16, weight any of
     opq's stored forms.  `workspace`: a device tensor of linear_backward_workspace_bytes(m, n, k)
-    bytes (by default one of torch's allocator)."""
-    lib = load()
+    bytes (by default one of torch's allocator).  More than 65536 weight rows (a vocabulary's) are
+    taken in blocks, whose float32 sums are added in order."""
     opq._need_cuda("dy", dy, torch.bfloat16, 2)
     if torch.is_grad_enabled() and dy.requires_grad:
         raise RuntimeError("dy requires grad, which this call does not follow: detach it, or call under "
@@ -136,7 +155,7 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
         out = torch.empty((m, k), dtype=out_dtype, device=dy.device)
     else:
         opq._need_cuda("out", out, out.dtype, 2)
-        bf16 = _float("out", out.dtype)
+        _float("out", out.dtype)
         if tuple(out.shape) != (m, k):
             raise ValueError(f"out must have shape {(m, k)}, got {tuple(out.shape)}")
         if torch.is_grad_enabled() and out.requires_grad:
@@ -149,30 +168,35 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
     for name, t in (("out", out), ("packed", weight.packed), ("sign", weight.sign), ("scale", weight[2])):
         if t.device != dy.device:
             raise ValueError(f"{name} must be on {dy.device}, got {t.device}")
+    if isinstance(weight, opq.BitsWeight):
+        opq._check_bits(weight, n, k)
+    elif isinstance(weight, opq.GroupedWeight):
+        opq._check_grouped(weight, n, k)
+    else:
+        _check_rows(weight, n, k)
     need = linear_backward_workspace_bytes(m, n, k)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
     elif workspace.device != dy.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dy.device}")
-    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    tail = (out.data_ptr(), OPQ_BF16 if out.dtype == torch.bfloat16 else OPQ_F32, opq._ptr(workspace), room)
     with torch.cuda.device(dy.device):
-        tail = tail + (opq._stream(dy.device),)
-        if isinstance(weight, opq.BitsWeight):
-            opq._check_bits(weight, n, k)
-            _check("opq_linear_backward_bits",
-                   lib.opq_linear_backward_bits(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
-                                                weight.scale.data_ptr(), m, n, k, weight.bits, alpha, *tail))
-        elif isinstance(weight, opq.GroupedWeight):
-            opq._check_grouped(weight, n, k)
-            _check("opq_linear_backward_grouped",
-                   lib.opq_linear_backward_grouped(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
-                                                   weight.scale16.data_ptr(), m, n, k, weight.group, alpha, *tail))
-        else:
-            _check_rows(weight, n, k)
-            _check("opq_linear_backward",
-                   lib.opq_linear_backward(dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(),
-                                           weight.scale.data_ptr(), m, n, k, alpha, *tail))
+        if m <= _TOKENS and n <= _ROWS:
+            _backward_call(dy, weight, alpha, out, workspace)
+            return out
+        for t in range(0, m, _TOKENS):
+            some, to = dy[t:t + _TOKENS], out[t:t + _TOKENS]
+            if n <= _ROWS:
+                _backward_call(some, weight, alpha, to, workspace)
+                continue
+            total = to if to.dtype == torch.float32 else torch.empty(to.shape, device=dy.device)
+            part = torch.empty_like(total)
+            for r in range(0, n, _ROWS):
+                block = type(weight)(*(w[r:r + _ROWS] for w in weight[:3]), *weight[3:])
+                _backward_call(some[:, r:r + _ROWS].contiguous(), block, alpha, part if r else total, workspace)
+                if r:
+                    total.add_(part)
+            if total is not to:
+                to.copy_(total)
     return out
 
 
