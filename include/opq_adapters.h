@@ -54,7 +54,8 @@ size_t opq_lowrank_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t rank
  *          initialisation; calls that may overlap need their own
  * Products of bfloat16 are summed in float32.  For the second product s_i D_i x is
  * taken in three bfloat16 parts (24 bits, all of a float32); the sum with y is float32,
- * rounded once: a bfloat16 out is the float32 one rounded.  A token's result
+ * rounded once: a bfloat16 out is the float32 one rounded.  Infinities and NaN come out
+ * where the formula has them.  A token's result
  * does not depend on the other tokens of the call, whose number sets in how many pieces
  * sums over k are taken; results repeat bit for bit.
  * m up to 2^22, k and n up to 2^20, m * k and m * n up to 2^39 with their strides,

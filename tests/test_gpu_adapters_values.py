@@ -1,4 +1,5 @@
-"""What the adapters' sums hold: bfloat16 results that are the float32 ones rounded."""
+"""What the adapters' sums hold: infinities as the definition has them, and bfloat16
+results that are the float32 ones rounded."""
 import pytest
 import torch
 
@@ -6,9 +7,10 @@ from test_gpu_adapters import DEV, _gen, _index, _stack
 
 pytestmark = pytest.mark.gpu
 
-# one launch; a wide block of tokens; one adapter's and mixed tokens of several blocks, each width of ranks
+TYPES = [torch.float32, torch.bfloat16]
+# one launch; a wide block of tokens; mixed tokens of several blocks, each width of ranks; several items of one adapter
 SIZES = [(1, 256, 264, 8, 3), (40, 256, 264, 16, 3), (50, 2048, 1032, 32, 5), (64, 256, 264, 64, 3), (300, 256, 1032, 8, 2),
-         (300, 128, 520, 40, 5), (200, 128, 264, 128, 3)]
+         (300, 128, 520, 40, 5), (200, 128, 264, 128, 3), (700, 128, 264, 16, 1)]
 
 
 @pytest.fixture(scope="module")
@@ -16,6 +18,74 @@ def L(gpu_lib):
     from w4a16_linear_amd import adapters
     adapters.load()
     return adapters
+
+
+def _small(shape, g, top=1):
+    """Small whole numbers, none zero: products' sums have few bits, so that of their three parts
+    of eight bits the later ones are zeros."""
+    t = torch.randint(1, top + 1, shape, generator=g, device=DEV)
+    return (t * (2 * torch.randint(0, 2, shape, generator=g, device=DEV) - 1)).to(torch.bfloat16)
+
+
+def _same(got, want):
+    """Equal where the definition gives a number, and the same infinity or NaN where it gives one."""
+    got = got.double()
+    assert torch.equal(got.isnan(), want.isnan()), (int(got.isnan().sum()), int(want.isnan().sum()))
+    assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
+
+
+def _products(c, p):
+    """c @ p in float64 with every infinity and NaN as one element after another gives it."""
+    return (c[:, :, None] * p[None]).sum(1) if c.shape[0] * p.numel() < 2e8 else torch.cat(
+        [(row[:, :, None] * p[None]).sum(1) for row in c.split(16)])
+
+
+@pytest.mark.parametrize("m,k,n,rank,count", SIZES)
+@pytest.mark.parametrize("out", TYPES)
+def test_infinite_weights(L, m, k, n, rank, count, out):
+    g = _gen(m + k)
+    x = _small((m, k), g)
+    down = _small((count, rank, k), g)
+    down[:, :, 2] = 0                                       # k - 1 odd terms: h is never 0
+    up = _small((count, rank, n), g, 3)
+    up[0, 1, 5], up[0, 2, 6], up[count - 1, 3, n - 1] = float("inf"), -float("inf"), float("nan")
+    up[count - 1, 0, 7], up[count - 1, 4, 7] = float("inf"), float("inf")
+    a = L.Adapters(down, up, torch.ones(count, device=DEV))
+    index = _index("mixed", m, count, g) if m > 1 else torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = _small((m, n), g).to(out)
+    got = L.lowrank_add(y, x, a, index, out_dtype=out)
+    want = y.double()
+    for i in range(count):
+        at = torch.nonzero(index == i)[:, 0]
+        want[at] += _products(x[at].double() @ down[i].double().T, up[i].double())
+    assert want.isinf().any()
+    _same(got, want)
+    fine = want.isfinite()
+    assert torch.equal(got[fine].double(), want[fine].to(out).double())       # whole numbers: nothing is rounded before
+
+
+@pytest.mark.parametrize("m,k,n,rank,count", SIZES)
+@pytest.mark.parametrize("kind", TYPES)
+def test_infinite_gradients(L, m, k, n, rank, count, kind):
+    g = _gen(m + n)
+    x, dy = _small((m, k), g), _small((m, n), g)
+    down, up = _small((count, rank, k), g), _small((count, rank, n), g)
+    t = m // 2
+    dy[t, 3], x[t, 4] = float("inf"), -float("inf")
+    down[0, 1, 6] = float("inf")
+    a = L.Adapters(down, up, torch.full((count,), 0.5, device=DEV))
+    index = _index("mixed", m, count, g) if m > 1 else torch.zeros(1, dtype=torch.int32, device=DEV)
+    index[t] = 0
+    dx, ddown, dup = L.lowrank_backward(dy, x, a, index, dx_dtype=kind, grad_dtype=kind)
+    want = torch.zeros((m, k), dtype=torch.float64, device=DEV)
+    for i in range(count):
+        at = torch.nonzero(index == i)[:, 0]
+        xd, dd, ud, wd = (v.double() for v in (x[at], dy[at], up[i], down[i]))
+        h, e = _products(xd, wd.T) * 0.5, _products(dd, ud.T) * 0.5
+        want[at] = _products(e, wd)
+        _same(ddown[i], _products(e.T, xd))
+        _same(dup[i], _products(h.T, dd))
+    _same(dx, want)
 
 
 @pytest.mark.parametrize("m,k,n,rank,count", SIZES)

@@ -29,7 +29,10 @@
 // parts, all of its 24 bits, whatever the result's type: a bfloat16 result is the float32
 // one rounded.  (With two parts, 16 bits: 4096 tokens, 3840 -> 20480, rank 64 99 us for
 // 102; one token, rank 8 7.7 for 8.0; gradients of one adapter 77 for 77.6.)  Parts are
-// cut by truncation, so none overflows; the last one is rounded.
+// cut by truncation, so none overflows; the last one is rounded.  A later part may be zero where
+// c is not, and zero times an infinite weight or gradient is NaN.  A sum that comes out NaN
+// has an infinity or NaN among its operands, so the definition makes it one too, and
+// the first parts alone, which have c's sign, say which: such sums are made of those.
 #include <algorithm>
 
 #include "adapters_internal.hpp"
@@ -113,6 +116,26 @@ __device__ __forceinline__ uint4 to_operand(uint4 v) {
   const int from = ((lane & 15) * 4 + (lane >> 4)) * 4;
   return make_uint4((uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.x), (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.y),
                     (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.z), (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.w));
+}
+
+// Whether a sum of the wave's may be NaN (it is one, or two are opposite infinities).
+__device__ __forceinline__ bool some_nan(const floatx4_t (&acc)[8]) {
+  float all = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) all += (acc[j][0] + acc[j][1]) + (acc[j][2] + acc[j][3]);
+  return __ballot(all != all);
+}
+
+// NaN in sums replaced by what `first` gives for operand j, the product of the first parts.
+template <typename F>
+__device__ __forceinline__ void mend(floatx4_t (&acc)[8], F first) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const floatx4_t by = first(j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = acc[j][i] != acc[j][i] ? by[i] : acc[j][i];
+    __builtin_amdgcn_sched_barrier(0);  // rarely run: registers count here, not time
+  }
 }
 
 // Eight rows of eight columns -> the eight columns, each of eight rows.
@@ -674,6 +697,14 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS>& s,
             for (int j = 0; j < 8; ++j)
               acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, operand(p[k][j]), acc[j], 0, 0, 0);
           }
+        if (some_nan(acc))
+          mend(acc, [&](int j) __attribute__((always_inline)) {
+            floatx4_t by = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < RS; ++k)
+              by = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(s.c[w][k][0][lane]), operand(p[k][j]), by, 0, 0, 0);
+            return by;
+          });
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -814,25 +845,43 @@ __global__ __launch_bounds__(kFewThreads) void lowrank_add_few(FewArgs a) {
     }
     __syncthreads();
     // lane (c, q): ranks 8 q ... of token c, which lanes c + 16 (2 q % 4) and the next sixteen hold
-    float v[8] = {};
-    if (q / 2 < RT && q * 8 < a.rank && c < tile.size) {
-      const float4 lo = s_sum[q / 2][c + 32 * (q & 1)], hi = s_sum[q / 2][c + 32 * (q & 1) + 16];
-      v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-      v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-    }
     uint32_t cut[8][kCuts];
+    auto cuts = [&]() __attribute__((always_inline)) {
+      float v[8] = {};
+      if (q / 2 < RT && q * 8 < a.rank && c < tile.size) {
+        const float4 lo = s_sum[q / 2][c + 32 * (q & 1)], hi = s_sum[q / 2][c + 32 * (q & 1) + 16];
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split(v[e] * scale, cut[e]);
+      for (int e = 0; e < 8; ++e) split(v[e] * scale, cut[e]);
+    };
+    auto part = [&](int e) __attribute__((always_inline)) {
+      return operand(make_uint4(cut[0][e] | cut[1][e] << 16, cut[2][e] | cut[3][e] << 16,
+                                cut[4][e] | cut[5][e] << 16, cut[6][e] | cut[7][e] << 16));
+    };
+    cuts();
 #pragma unroll
     for (int e = 0; e < 8; ++e) rows[e] = q * 8 < a.rank ? rows[e] : zero16();
     transpose8(rows, p);
-    if (!BASE_BF16) load_base();
+    if (!BASE_BF16) {
+      __builtin_amdgcn_sched_barrier(0);  // neither sooner nor later: by registers
+      load_base();
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int e = 0; e < kCuts; ++e) {
-      const bf16x8_t h = operand(make_uint4(cut[0][e] | cut[1][e] << 16, cut[2][e] | cut[3][e] << 16,
-                                            cut[4][e] | cut[5][e] << 16, cut[6][e] | cut[7][e] << 16));
+      const bf16x8_t h = part(e);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, operand(p[j]), acc[j], 0, 0, 0);
+    }
+    if (some_nan(acc)) {
+      __builtin_amdgcn_sched_barrier(0);
+      cuts();  // made anew: kept, they would cost registers
+      const bf16x8_t h = part(0);
+      mend(acc, [&](int j) __attribute__((always_inline)) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, operand(p[j]), floatx4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      });
     }
   }
 #pragma unroll
@@ -1153,6 +1202,22 @@ __global__ __launch_bounds__(kThreads) void lowrank_grad(GradArgs a) {
       }
       const int r = r0 + (i0 + i) * 16 + q * 4 + wave;
       if (r < a.rank && n < g.d) {
+        float all = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) all += w[j];
+        if (all != all) {  // NaN: the item's sums of the first parts, token by token
+          float by[8] = {};
+#pragma unroll 1
+          for (int at = from; at < from + length; ++at) {
+            const float c0 = __uint_as_float((uint32_t)g.c[operand_at(a.rank, a.cap, 0, r, at)] << 16);
+            float x[8];
+            load8<true>(v, a.g.order[at] * g.stride, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) by[j] += c0 * x[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = w[j] != w[j] ? by[j] : w[j];
+        }
         const int64_t to = (first + r) * g.d + n;
         if (slot < 0) store8<OUT_BF16, false>(g.out, to, w);
         else store8<false, false>(g.part, to, w);
