@@ -183,3 +183,19 @@ def test_a_layer_with_a_vocabulary(L, gpu_lib):
     adapted = AdaptedLinear(layer, 2, 8)                    # up is zeros: the same gradient
     (got2,) = torch.autograd.grad(adapted(x, torch.zeros(5, dtype=torch.int32, device=DEV)), x, dy)
     assert torch.equal(got2, got)
+
+
+@pytest.mark.parametrize("m", [8, 200])
+def test_a_refused_call_wrote_nothing(L, gpu_lib, m):
+    """Autograd is not told of memory that a refused call did not write."""
+    w = _weight(gpu_lib, 256, 256, "row", 0.73)
+    dy = torch.randn((m, 256), device=DEV).to(torch.bfloat16)
+    out = torch.zeros((m, 256), device=DEV)
+    before = out._version
+    for call in (lambda: L.linear_backward(dy, w, -1.0, out=out), lambda: L.linear_backward(dy, w._replace(scale=w.scale.cpu()), 0.73, out=out),
+                 lambda: L.linear_backward(dy, w, 0.73, out=out, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(ValueError):
+            call()
+    assert out._version == before and not out.any()
+    L.linear_backward(dy, w, 0.73, out=out)
+    assert out._version > before

@@ -135,6 +135,27 @@ def _backward_call(dy, weight, alpha, out, workspace) -> None:
         opq._stream(dy.device)))
 
 
+def _backward_blocks(dy, weight, alpha, out, workspace) -> None:
+    """linear_backward, its tensors checked, as calls of the library."""
+    m, n = dy.shape
+    if m <= _TOKENS and n <= _ROWS:
+        return _backward_call(dy, weight, alpha, out, workspace)
+    for t in range(0, m, _TOKENS):
+        some, to = dy[t:t + _TOKENS], out[t:t + _TOKENS]
+        if n <= _ROWS:
+            _backward_call(some, weight, alpha, to, workspace)
+            continue
+        total = to if to.dtype == torch.float32 else torch.empty(to.shape, device=dy.device)
+        part = torch.empty_like(total)
+        for r in range(0, n, _ROWS):
+            block = type(weight)(*(w[r:r + _ROWS] for w in weight[:3]), *weight[3:])
+            _backward_call(some[:, r:r + _ROWS].contiguous(), block, alpha, part if r else total, workspace)
+            if r:
+                total.add_(part)
+        if total is not to:
+            to.copy_(total)
+
+
 def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.Tensor] = None,
                     out_dtype: torch.dtype = torch.bfloat16,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -150,7 +171,8 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
     n, k = weight.shape
     if dy.shape[1] != n:
         raise ValueError(f"dy has n={dy.shape[1]}, weight has n={n}")
-    if out is None:
+    given = out is not None
+    if not given:
         _float("out_dtype", out_dtype)
         out = torch.empty((m, k), dtype=out_dtype, device=dy.device)
     else:
@@ -160,8 +182,6 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
             raise ValueError(f"out must have shape {(m, k)}, got {tuple(out.shape)}")
         if torch.is_grad_enabled() and out.requires_grad:
             raise RuntimeError("out requires grad, which this call does not follow")
-        if not out.is_inference():
-            torch.autograd.graph.increment_version(out)
         near = out.data_ptr() - dy.data_ptr()
         if out.numel() and dy.numel() and -out.numel() * out.element_size() < near < dy.numel() * 2:
             raise ValueError("out must not share memory with dy")
@@ -180,23 +200,9 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
     elif workspace.device != dy.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dy.device}")
     with torch.cuda.device(dy.device):
-        if m <= _TOKENS and n <= _ROWS:
-            _backward_call(dy, weight, alpha, out, workspace)
-            return out
-        for t in range(0, m, _TOKENS):
-            some, to = dy[t:t + _TOKENS], out[t:t + _TOKENS]
-            if n <= _ROWS:
-                _backward_call(some, weight, alpha, to, workspace)
-                continue
-            total = to if to.dtype == torch.float32 else torch.empty(to.shape, device=dy.device)
-            part = torch.empty_like(total)
-            for r in range(0, n, _ROWS):
-                block = type(weight)(*(w[r:r + _ROWS] for w in weight[:3]), *weight[3:])
-                _backward_call(some[:, r:r + _ROWS].contiguous(), block, alpha, part if r else total, workspace)
-                if r:
-                    total.add_(part)
-            if total is not to:
-                to.copy_(total)
+        _backward_blocks(dy, weight, alpha, out, workspace)
+    if given and not out.is_inference():   # written, so autograd learns of it
+        torch.autograd.graph.increment_version(out)
     return out
 
 
