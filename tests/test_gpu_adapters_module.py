@@ -304,3 +304,28 @@ def test_in_a_graph(L, gpu_lib, m):
         want = step(x, y, i)
         torch.cuda.synchronize()
         assert all(torch.equal(r, e) for r, e in zip(res, want))
+
+
+@pytest.mark.parametrize("n", [10, 1000])
+def test_gradients_that_start_anywhere(gpu_lib, n):
+    """What a backward pass hands on may be a part of a longer tensor: of a concatenation's, say."""
+    from w4a16_linear_amd.module import AdaptedLinear, OPQLinear
+    lin = torch.nn.Linear(64, n).to(DEV)
+    base = OPQLinear.from_linear(lin)
+    g = _gen(n)
+    x = torch.randn((7, 64), generator=g, device=DEV).to(torch.bfloat16).requires_grad_()
+    dy = torch.randn((7, n), generator=g, device=DEV).to(torch.bfloat16)
+    layers = [base] if n % 8 else [base, AdaptedLinear(base, 2, 8)]
+    for layer in layers:
+        args = () if layer is base else (torch.zeros(7, dtype=torch.int32, device=DEV),)
+        (want,) = torch.autograd.grad(layer(x, *args), x, dy)
+        long = torch.empty(7 * n + 3, dtype=torch.bfloat16, device=DEV)
+        for start in (1, 3):
+            odd = long[start:start + 7 * n].view(7, n)
+            odd.copy_(dy)
+            (got,) = torch.autograd.grad(layer(x, *args), x, odd)
+            assert torch.equal(got, want)
+        (got,) = torch.autograd.grad(torch.cat((layer(x[:3], *(a[:3] for a in args)), layer(x[3:], *(a[3:] for a in args)))), x, dy)
+        (a,) = torch.autograd.grad(layer(x[:3], *(a[:3] for a in args)), x, dy[:3].clone())
+        (b,) = torch.autograd.grad(layer(x[3:], *(a[3:] for a in args)), x, dy[3:].clone())
+        assert torch.equal(got, a + b)

@@ -209,9 +209,11 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
 # ------------------------------------------------------------------ autograd
 
 def _dy(dy: torch.Tensor) -> torch.Tensor:
-    """The gradient as the kernels take it: dense, in bfloat16, the type these layers' activations
-    are rounded to on their way in."""
-    return dy.to(torch.bfloat16).contiguous()
+    """The gradient as the kernels take it: dense, from a 16-byte boundary on (a part of a longer
+    gradient may start anywhere), in bfloat16, the type these layers' activations are rounded to on
+    their way in."""
+    dy = dy.to(torch.bfloat16).contiguous()
+    return dy if dy.data_ptr() % 16 == 0 else dy.clone()
 
 
 def _weight(like, tensors):
