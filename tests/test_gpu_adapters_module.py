@@ -329,3 +329,21 @@ def test_gradients_that_start_anywhere(gpu_lib, n):
         (a,) = torch.autograd.grad(layer(x[:3], *(a[:3] for a in args)), x, dy[:3].clone())
         (b,) = torch.autograd.grad(layer(x[3:], *(a[3:] for a in args)), x, dy[3:].clone())
         assert torch.equal(got, a + b)
+
+
+def test_layers_made_in_inference_mode(gpu_lib):
+    """Codes made under inference_mode have no versions to watch; gradients pass through them all the same."""
+    from w4a16_linear_amd.module import AdaptedLinear, OPQLinear
+    lin = torch.nn.Linear(64, 32).to(DEV)
+    with torch.inference_mode():
+        base = OPQLinear.from_linear(lin)
+    plain = OPQLinear.from_linear(lin)
+    x = torch.randn((5, 64), device=DEV, requires_grad=True)
+    (want,) = torch.autograd.grad(plain(x).sum(), x)
+    (got,) = torch.autograd.grad(base(x).sum(), x)
+    assert torch.equal(got, want)
+    layer = AdaptedLinear(base, 2, 8)
+    with torch.no_grad():
+        layer.up.normal_()
+    layer(x, torch.zeros(5, dtype=torch.int32, device=DEV)).sum().backward()
+    assert layer.down.grad.isfinite().all() and layer.down.grad.any() and x.grad is not None

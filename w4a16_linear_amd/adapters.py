@@ -216,8 +216,10 @@ def _dy(dy: torch.Tensor) -> torch.Tensor:
     return dy if dy.data_ptr() % 16 == 0 else dy.clone()
 
 
-def _weight(like, tensors):
-    return type(like)(*tensors, *like[3:])
+def _watched(weight):
+    """A weight's tensors that autograd can watch for changes: those of inference mode have no
+    version, and cannot be saved."""
+    return [t for t in weight[:3] if not t.is_inference()]
 
 
 class _Linear(torch.autograd.Function):
@@ -225,7 +227,7 @@ class _Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, alpha, bias, out_dtype):
-        ctx.save_for_backward(*weight[:3])
+        ctx.save_for_backward(*_watched(weight))
         ctx.how = (weight, alpha, x.dtype)
         return opq.linear(x.to(torch.bfloat16).contiguous(), weight, alpha, bias=bias, out_dtype=out_dtype)
 
@@ -233,7 +235,8 @@ class _Linear(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         weight, alpha, dtype = ctx.how
-        dx = linear_backward(_dy(dy), _weight(weight, ctx.saved_tensors), alpha, out_dtype=dtype)
+        ctx.saved_tensors   # raises if the weight was changed
+        dx = linear_backward(_dy(dy), weight, alpha, out_dtype=dtype)
         return dx, None, None, None, None
 
 
@@ -245,19 +248,19 @@ class _Adapted(torch.autograd.Function):
         xb = x.to(torch.bfloat16).contiguous()
         y = opq.linear(xb, weight, alpha, bias=bias, out_dtype=out_dtype)
         lowrank_add(y, xb, Adapters(down, up, scale), index, out=y)
-        ctx.save_for_backward(xb, down, up, scale, index, *weight[:3])
+        ctx.save_for_backward(xb, down, up, scale, index, *_watched(weight))
         ctx.how = (weight, alpha, x.dtype)
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        xb, down, up, scale, index, *tensors = ctx.saved_tensors
+        xb, down, up, scale, index = ctx.saved_tensors[:5]
         weight, alpha, dtype = ctx.how
         dy, dx = _dy(dy), None
         wants_x, wants = ctx.needs_input_grad[0], ctx.needs_input_grad[4] or ctx.needs_input_grad[5]
         if wants_x:
-            dx = linear_backward(dy, _weight(weight, tensors), alpha, out_dtype=dtype)
+            dx = linear_backward(dy, weight, alpha, out_dtype=dtype)
         _, d_down, d_up = lowrank_backward(dy, xb, Adapters(down, up, scale), index, dx=dx, out=dx, grad_dtype=down.dtype,
                                            input_grad=wants_x, adapter_grads=wants)
         return dx, None, None, None, d_down, d_up, None, None, None
