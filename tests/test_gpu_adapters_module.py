@@ -347,3 +347,34 @@ def test_layers_made_in_inference_mode(gpu_lib):
         layer.up.normal_()
     layer(x, torch.zeros(5, dtype=torch.int32, device=DEV)).sum().backward()
     assert layer.down.grad.isfinite().all() and layer.down.grad.any() and x.grad is not None
+
+
+def test_layers_share_no_workspace(L, gpu_lib, monkeypatch):
+    """Layers of one model on two streams at once: every forward has a workspace of its own."""
+    from w4a16_linear_amd.module import OPQLinear
+    m = 700                                                                     # a split contraction, or W' decoded beside
+    sets = []
+    for s, form in enumerate(({}, dict(bits=5))):
+        layer = _layer(2048, 256, 3, 8, seed=s, **form)
+        x = torch.randn((m, 2048), generator=_gen(s), device=DEV).to(torch.bfloat16)
+        index = _index("mixed", m, 3, _gen(s))
+        y = gpu_lib.linear(x, layer.base.qweight(), layer.base.alpha, bias=layer.base.bias, out_dtype=torch.bfloat16)
+        with torch.no_grad():
+            sets.append((layer, x, index, y, L.lowrank_add(y, x, layer.stack(), index)))
+    assert all(gpu_lib.linear_workspace_bytes(m, 256, 2048, bits) for bits in (4, 5))
+    monkeypatch.setattr(gpu_lib, "shared_workspace", lambda *a: pytest.fail("a workspace that others use"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for s, stream in enumerate(streams):
+            layer, x, index, _, _ = sets[s]
+            with torch.cuda.stream(stream):
+                tracked = x.detach().clone().requires_grad_()
+                with torch.no_grad():
+                    got[s].append((layer.base(x), layer(x, index)))
+                got[s].append((layer.base(tracked).detach(), layer(tracked, index).detach()))
+    torch.cuda.synchronize()
+    for s in range(2):
+        for base, adapted in got[s]:
+            assert torch.equal(base, sets[s][3]) and torch.equal(adapted, sets[s][4])

@@ -206,6 +206,20 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
     return out
 
 
+# ------------------------------------------------------- the layers' projection
+
+def project(x: torch.Tensor, weight, alpha: float, bias: Optional[torch.Tensor], out_dtype: torch.dtype) -> torch.Tensor:
+    """opq.linear of x [m, k] (bfloat16) on x's device, with a workspace of torch's allocator: a layer may
+    run on several streams at once, and opq.linear's own workspace is one stream's at a time."""
+    if not x.is_cuda:
+        return opq.linear(x, weight, alpha, bias=bias, out_dtype=out_dtype)   # refused there
+    bits = weight.bits if isinstance(weight, opq.BitsWeight) else 4
+    need = opq.linear_workspace_bytes(x.shape[0], *weight.shape, bits)
+    with torch.cuda.device(x.device):
+        room = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        return opq.linear(x, weight, alpha, bias=bias, workspace=room, out_dtype=out_dtype)
+
+
 # ------------------------------------------------------------------ autograd
 
 def _dy(dy: torch.Tensor) -> torch.Tensor:
@@ -229,7 +243,7 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, alpha, bias, out_dtype):
         ctx.save_for_backward(*_watched(weight))
         ctx.how = (weight, alpha, x.dtype)
-        return opq.linear(x.to(torch.bfloat16).contiguous(), weight, alpha, bias=bias, out_dtype=out_dtype)
+        return project(x.to(torch.bfloat16).contiguous(), weight, alpha, bias, out_dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -246,7 +260,7 @@ class _Adapted(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, alpha, bias, down, up, scale, index, out_dtype):
         xb = x.to(torch.bfloat16).contiguous()
-        y = opq.linear(xb, weight, alpha, bias=bias, out_dtype=out_dtype)
+        y = project(xb, weight, alpha, bias, out_dtype)
         lowrank_add(y, xb, Adapters(down, up, scale), index, out=y)
         ctx.save_for_backward(xb, down, up, scale, index, *_watched(weight))
         ctx.how = (weight, alpha, x.dtype)

@@ -134,7 +134,7 @@ class OPQLinear(nn.Module):
             y = adapters.apply_linear(x.reshape(-1, self.in_features), self.qweight(), self.alpha, self.bias)
             return y.reshape(*lead, self.out_features)
         x2 = x.reshape(-1, self.in_features).to(torch.bfloat16).contiguous()
-        y = opq.linear(x2, self.qweight(), self.alpha, bias=self.bias, out_dtype=x.dtype)
+        y = adapters.project(x2, self.qweight(), self.alpha, self.bias, x.dtype)
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self) -> str:
@@ -212,7 +212,7 @@ class AdaptedLinear(nn.Module):
             y = adapters.apply_adapted(x2, base.qweight(), base.alpha, base.bias, self.stack(), index)
         else:
             x2 = x2.to(torch.bfloat16).contiguous()
-            y = opq.linear(x2, base.qweight(), base.alpha, bias=base.bias, out_dtype=x.dtype)
+            y = adapters.project(x2, base.qweight(), base.alpha, base.bias, x.dtype)
             with torch.no_grad():
                 adapters.lowrank_add(y, x2, self.stack(), index, out=y)
         return y.reshape(*lead, base.out_features)
