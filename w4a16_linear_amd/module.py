@@ -29,6 +29,7 @@ from torch import nn
 from . import adapters, opq
 
 FORMAT = "opq-int4/1"
+FORMAT_ADAPTED = "opq-int4/2"   # with adapters, which a reader of the first would leave out
 _META_KEY = "opq"
 
 
@@ -303,50 +304,77 @@ def use_adapters(model: nn.Module, index: Optional[torch.Tensor]) -> None:
 # ---------------------------------------------------------------- save / load
 
 def _opq_layers(model: nn.Module):
+    """(name, OPQLinear, the AdaptedLinear that holds it or None); an adapted layer under its own name."""
     seen = set()
     for name, mod in model.named_modules():
-        if isinstance(mod, OPQLinear) and id(mod) not in seen:
+        if isinstance(mod, AdaptedLinear):
+            seen.add(id(mod.base))
+            yield name, mod.base, mod
+        elif isinstance(mod, OPQLinear) and id(mod) not in seen:
             seen.add(id(mod))
-            yield name, mod
+            yield name, mod, None
 
 
 def save_opq(model: nn.Module, path: str) -> List[str]:
-    """Write every OPQLinear's buffers to a safetensors file; returns the
-    layer names saved.  The header records the format, and per layer its
-    shape, alpha, code width, group size and whether it has a bias.  A layer reached under several
-    names is saved once, under the first."""
+    """Write every OPQLinear's buffers, and the adapters of an AdaptedLinear beside its own, to a
+    safetensors file; returns the layer names saved.  The header records the format, and per layer its
+    shape, alpha, code width, group size, whether it has a bias, and its adapters' number and rank.  A
+    layer reached under several names is saved once, under the first; an AdaptedLinear and its
+    projection are one layer."""
     from safetensors.torch import save_file
 
     tensors: Dict[str, torch.Tensor] = {}
     layers = {}
-    for name, mod in _opq_layers(model):
+    for name, mod, adapted in _opq_layers(model):
         layers[name] = {"in": mod.in_features, "out": mod.out_features, "alpha": mod.alpha,
                         "bias": mod.bias is not None, "group": mod.group_size or 0,
                         "bits": mod.bits}
         for b in ("packed", "sign_packed", "mx") + (("bias",) if mod.bias is not None else ()):
             tensors[f"{name}.{b}"] = getattr(mod, b).detach().to("cpu").contiguous()
-    meta = {_META_KEY: json.dumps({"format": FORMAT, "layers": layers})}
+        if adapted is not None:
+            layers[name]["adapters"] = {"count": adapted.down.shape[0], "rank": adapted.rank}
+            for b in _ADAPTER_TENSORS:
+                tensors[f"{name}.{b}"] = getattr(adapted, b).detach().to("cpu").contiguous()
+    fmt = FORMAT_ADAPTED if any("adapters" in info for info in layers.values()) else FORMAT
+    meta = {_META_KEY: json.dumps({"format": fmt, "layers": layers})}
     save_file(tensors, path, metadata=meta)
     return list(layers)
 
 
+_ADAPTER_TENSORS = ("down", "up", "scale")
+
+
+def _fill(module: nn.Module, f, path: str, name: str, names: Iterable[str]) -> None:
+    """Copy the file's tensors `name`.* into the module's."""
+    with torch.no_grad():
+        for b in names:
+            t, dst = f.get_tensor(f"{name}.{b}"), getattr(module, b)
+            if t.shape != dst.shape or t.dtype != dst.dtype:
+                raise ValueError(f"{path}: {name}.{b} is {t.dtype}{tuple(t.shape)}, "
+                                 f"expected {dst.dtype}{tuple(dst.shape)}")
+            dst.copy_(t)
+
+
 def load_opq(model: nn.Module, path: str, device=None) -> List[str]:
     """Fill `model` from a file written by save_opq: each saved layer name must
-    name an nn.Linear (a skeleton: its weights are dropped) or an OPQLinear of
-    the same shape, which becomes an OPQLinear holding the saved buffers.  The
+    name an nn.Linear (a skeleton: its weights are dropped), an OPQLinear or an AdaptedLinear of
+    the same shape, which becomes an OPQLinear holding the saved buffers, or with saved adapters an
+    AdaptedLinear (the one that is there, if its stack is of the same shape).  Adapters that the
+    file has none for stay beside the projection that is replaced.  The
     buffers go to `device`, by default that of the module they replace.
     Returns the layer names loaded."""
     from safetensors import safe_open
 
     with safe_open(path, framework="pt", device="cpu") as f:
         meta = json.loads((f.metadata() or {}).get(_META_KEY, "null") or "null")
-        if not meta or meta.get("format") != FORMAT:
-            raise ValueError(f"{path}: not an OPQ file of format {FORMAT}")
+        if not meta or meta.get("format") not in (FORMAT, FORMAT_ADAPTED):
+            raise ValueError(f"{path}: not an OPQ file of format {FORMAT} or {FORMAT_ADAPTED}")
         layers = meta["layers"]
         for name, info in layers.items():
             parent_name, _, cname = name.rpartition(".")
             parent = model.get_submodule(parent_name) if parent_name else model
-            old = getattr(parent, cname, None)
+            held = getattr(parent, cname, None)
+            old = held.base if isinstance(held, AdaptedLinear) else held
             if isinstance(old, OPQLinear):
                 ref_dev = old.packed.device
             elif isinstance(old, nn.Linear):
@@ -360,16 +388,21 @@ def load_opq(model: nn.Module, path: str, device=None) -> List[str]:
             new = OPQLinear(info["in"], info["out"], bias=info["bias"], alpha=info["alpha"],
                             device=dev, group_size=info.get("group") or None,
                             bits=info.get("bits", 4))
-            for b in ("packed", "sign_packed", "mx") + (("bias",) if info["bias"] else ()):
-                t = f.get_tensor(f"{name}.{b}")
-                dst = getattr(new, b)
-                if t.shape != dst.shape or t.dtype != dst.dtype:
-                    raise ValueError(f"{path}: {name}.{b} is {t.dtype}{tuple(t.shape)}, "
-                                     f"expected {dst.dtype}{tuple(dst.shape)}")
-                dst.copy_(t)
+            _fill(new, f, path, name, ("packed", "sign_packed", "mx") + (("bias",) if info["bias"] else ()))
+            stack = info.get("adapters")
+            if stack is not None:
+                same = isinstance(held, AdaptedLinear) and held.rank == stack["rank"] and \
+                    held.down.shape[0] == stack["count"] and held.down.device == new.packed.device
+                layer = held if same else AdaptedLinear(new, stack["count"], stack["rank"])
+                _fill(layer, f, path, name, _ADAPTER_TENSORS)
+                if not same:
+                    layer.index = getattr(held, "index", None)
+                    old, new = held, layer
             # every slot holding the replaced module (a shared layer is saved once)
             for _, mod in list(model.named_modules()):
                 for slot, child in list(mod._modules.items()):
                     if child is old:
                         setattr(mod, slot, new)
+            if isinstance(held, AdaptedLinear) and held.base is new:
+                held.to(dev)   # adapters that stay follow their projection
     return list(layers)
