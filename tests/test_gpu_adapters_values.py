@@ -1,5 +1,5 @@
-"""What the adapters' sums hold: infinities as the definition has them, and bfloat16
-results that are the float32 ones rounded."""
+"""What the adapters' sums hold: infinities as the definition has them, bfloat16 results that are
+the float32 ones rounded, gradients that are differences to the last bit."""
 import pytest
 import torch
 
@@ -104,3 +104,56 @@ def test_a_bfloat16_result_is_the_float32_one_rounded(L, m, k, n, rank, count):
     got = L.lowrank_backward(dy, x, a, index, dx=dx, grad_dtype=torch.bfloat16)
     for name, r, e in zip(("dx", "d_down", "d_up"), got, exact):
         assert torch.equal(r, e.to(torch.bfloat16)), (name, int((r != e.to(torch.bfloat16)).sum()), r.numel())
+
+
+def test_gradients_are_differences_to_the_last_bit(L, gpu_lib):
+    """A layer whose weights, adapters, inputs and steps are small whole numbers: every sum is exact in
+    float32 and every gradient in bfloat16, and the output is linear in each tensor, so the
+    difference of two outputs is the gradient times the step, bit for bit."""
+    from w4a16_linear_amd.module import AdaptedLinear, OPQLinear
+    k, n, m, rank, count = 96, 64, 40, 8, 3
+    g = _gen(21)
+
+    def some(shape, share):                                 # -1, 0 and 1
+        return (torch.randint(-1, 2, shape, generator=g, device=DEV) *
+                (torch.rand(shape, generator=g, device=DEV) < share)).to(torch.bfloat16)
+
+    lin = torch.nn.Linear(k, n, bias=False).to(DEV)
+    with torch.no_grad():
+        w = some((n, k), 0.7)
+        w[:, 0] = 1                                         # the row's maximum: codes give -1, 0 and 1 back
+        lin.weight.copy_(w)
+    layer = AdaptedLinear(OPQLinear.from_linear(lin), count, rank)
+    assert torch.equal(layer.base.dequantized_weight(), w)
+    with torch.no_grad():
+        layer.down.copy_(some((count, rank, k), 0.6))
+        layer.up.copy_(some((count, rank, n), 0.6))
+        layer.scale.copy_(torch.tensor([0.5, 1.0, 2.0]))
+    index = _index("mixed", m, count, g)
+    assert {0, 1, 2} <= set(index.tolist())
+    c = some((m, n), 0.3).float()
+    x = some((m, k), 0.8).float().requires_grad_()
+
+    def loss():
+        return (layer(x, index).double() * c.double()).sum()
+
+    loss().backward()
+    for t, grad in ((layer.down, layer.down.grad), (layer.up, layer.up.grad), (x, x.grad)):
+        assert 4 < grad.abs().max() <= 128 and torch.equal(grad * 2, (grad * 2).round())    # halves: exact in bfloat16
+        steps = [some(t.shape, 0.5).to(t.dtype) for _ in range(6)]
+        for place in torch.randint(0, t.numel(), (20,), generator=g, device=DEV).tolist():  # and element by element
+            one = torch.zeros_like(t)
+            one.view(-1)[place] = 1
+            steps.append(one)
+        met = 0
+        for step in steps:
+            with torch.no_grad():
+                t.add_(step)
+                up = loss()
+                t.sub_(2 * step)
+                down = loss()
+                t.add_(step)
+            want = float((up - down) / 2)
+            assert float((grad.double() * step.double()).sum()) == want
+            met += want != 0
+        assert met >= 16, met                               # a gradient of zeros, or without one term, fails
