@@ -209,15 +209,12 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
 # ------------------------------------------------------- the layers' projection
 
 def project(x: torch.Tensor, weight, alpha: float, bias: Optional[torch.Tensor], out_dtype: torch.dtype) -> torch.Tensor:
-    """opq.linear of x [m, k] (bfloat16) on x's device, with a workspace of torch's allocator: a layer may
-    run on several streams at once, and opq.linear's own workspace is one stream's at a time."""
-    if not x.is_cuda:
-        return opq.linear(x, weight, alpha, bias=bias, out_dtype=out_dtype)   # refused there
-    bits = weight.bits if isinstance(weight, opq.BitsWeight) else 4
-    need = opq.linear_workspace_bytes(x.shape[0], *weight.shape, bits)
-    with torch.cuda.device(x.device):
-        room = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        return opq.linear(x, weight, alpha, bias=bias, workspace=room, out_dtype=out_dtype)
+    """opq.linear of x [m, k] (bfloat16) on x's device, with a workspace of the call's own: a layer may run
+    on several streams at once."""
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        with torch.cuda.device(x.device):
+            return opq.linear(x, weight, alpha, bias, None, opq.own_workspace, out_dtype)
+    return opq.linear(x, weight, alpha, bias, None, opq.own_workspace, out_dtype)
 
 
 # ------------------------------------------------------------------ autograd

@@ -367,8 +367,13 @@ def shared_workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor
     return ws
 
 
+def own_workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
+    """A workspace of torch's allocator for one call on the current stream (None for 0)."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
 def linear(x: torch.Tensor, qw, alpha: float, bias: Optional[torch.Tensor] = None,
-           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, workspace=None,
            out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """y[m, n] = x[m, k] W'^T (+ bias), W' made from qw: a QuantizedWeight or a
     GroupedWeight (decoded on chip) or a BitsWeight (3, 5 or 6 bits: decoded
@@ -377,7 +382,8 @@ def linear(x: torch.Tensor, qw, alpha: float, bias: Optional[torch.Tensor] = Non
     out_dtype is torch.float32 or torch.bfloat16 (the float32 result rounded
     to nearest even).  `workspace`, when given, must be a uint8 device tensor
     of at least linear_workspace_bytes(m, n, k) bytes (its contents are
-    overwritten); by default the per-device shared one is used.
+    overwritten), or a function of the device and the bytes that gives one
+    (own_workspace); by default the per-device shared one is used.
     """
     _need_cuda("x", x, torch.bfloat16, 2)
     m, k = x.shape
@@ -400,6 +406,8 @@ def linear(x: torch.Tensor, qw, alpha: float, bias: Optional[torch.Tensor] = Non
     need = linear_workspace_bytes(m, n, k, qw.bits if isinstance(qw, BitsWeight) else 4)
     if workspace is None:
         workspace = shared_workspace(x.device, need)
+    elif not isinstance(workspace, torch.Tensor):
+        workspace = workspace(x.device, need)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA (HIP) tensor")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
