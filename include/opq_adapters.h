@@ -102,14 +102,16 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
  * product makes dx.  Both are bf16 matrix-core products with float32 sums.
  *   dy     device, [m][n] bfloat16, dense;  dx  device out, [m][k] of dx_dtype, dense;
  *          it must not overlap the inputs
- *   workspace  at least opq_linear_backward_workspace_bytes(m, n, k) bytes, no
- *          initialisation; calls that may overlap need their own
+ *   workspace  at least opq_linear_backward_workspace_bytes(m, n, k) bytes, or for 4-bit codes
+ *          opq_linear_backward_codes_workspace_bytes(m, n, k), which are never more (both are
+ *          whole MiB); no initialisation; calls that may overlap need their own
  * The other arguments as in opq_linear, opq_linear_bits and opq_linear_grouped; n up to
  * 65536 (the sums of more rows are those of blocks of them, added), k up to 65536 and a multiple of 32, m up to 2^22, m * n and m * k up to 2^39.
  * Errors: OPQ_ERR_NULL, OPQ_ERR_SHAPE, OPQ_ERR_ALPHA, OPQ_ERR_ALIGN, OPQ_ERR_DTYPE,
  * OPQ_ERR_WORKSPACE, OPQ_ERR_UNSUPPORTED, OPQ_ERR_HIP.
  */
 size_t opq_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
+size_t opq_linear_backward_codes_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int opq_linear_backward(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
                         const float* scale, int64_t m, int64_t n, int64_t k, float alpha, void* dx,
                         int dx_dtype, void* workspace, size_t workspace_bytes, void* stream);

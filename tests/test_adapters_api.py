@@ -151,3 +151,24 @@ def test_in_place_means_the_same_rows(lib):
     assert add(3, 136, 1, 1) == UNSUPPORTED and add(3, 128, 0, 1) == UNSUPPORTED and add(1, 128, 1, 0) == UNSUPPORTED
     assert lib.opq_lowrank_backward(ctypes.byref(_stack()), FAKE, 128, FAKE, 64, FAKE, 3, FAKE, 72, 1, FAKE, 64, FAKE, FAKE, 0,
                                     FAKE, 1 << 40, None) == UNSUPPORTED
+
+
+def test_what_4_bit_codes_need(lib):
+    """W' is written for longer calls only, and once: what few tokens need are their split sums."""
+    every, codes = lib.opq_linear_backward_workspace_bytes, lib.opq_linear_backward_codes_workspace_bytes
+    for m in (1, 8, 64, 65, 333, 512):
+        for n, k in ((3840, 3840), (20480, 3840), (3840, 10240), (65536, 65536), (1000, 96)):
+            # at most 512 workgroups' planes, 128 columns each; dy with longer rows; whole MiB
+            assert codes(m, n, k) <= 512 * m * 128 * 4 + 2 * m * (n + 63) + (2 << 20), (m, n, k)
+    for m in (513, 4096):
+        for n, k in ((3840, 3840), (20480, 3840), (1001, 96)):
+            assert codes(m, n, k) >= n * k * 2 and every(m, n, k) >= codes(m, n, k) + n * k * 2 - (1 << 20)
+    for size in ((0, 64, 64), (4, 65537, 64), (4, 64, 65568), ((1 << 22) + 1, 64, 64), (4, 64, 40)):
+        assert every(*size) == codes(*size) == 0
+
+    def call(fn, m, n, k, wsb, extra=()):
+        return getattr(lib, "opq_linear_backward" + fn)(FAKE, FAKE, FAKE, FAKE, m, n, k, *extra, 0.73, FAKE, 1, FAKE, wsb, None)
+
+    for m, n, k in ((8, 20480, 3840), (600, 3840, 512)):
+        for fn, extra, need in (("", (), codes), ("_bits", (4,), codes), ("_grouped", (128,), codes), ("_bits", (5,), every)):
+            assert call(fn, m, n, k, need(m, n, k) - 1, extra) == WORKSPACE

@@ -199,3 +199,19 @@ def test_a_refused_call_wrote_nothing(L, gpu_lib, m):
     assert out._version == before and not out.any()
     L.linear_backward(dy, w, 0.73, out=out)
     assert out._version > before
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 33, 64), (8, 1000, 512), (64, 777, 128), (65, 2048, 256), (333, 1001, 768), (512, 96, 32),
+                                   (513, 1001, 64), (600, 2048, 512), (700, 40, 512)])
+@pytest.mark.parametrize("form", ["row", 32, "4b", "3b"])
+def test_the_workspace_is_enough(L, gpu_lib, m, n, k, form):
+    """What is asked for is all that is written, in every path and with every kind of padding."""
+    w = _weight(gpu_lib, n, k, form, 0.73)
+    dy = torch.randn((m, n), device=DEV).to(torch.bfloat16)
+    need = L.linear_backward_workspace_bytes(m, n, k, 3 if form == "3b" else 4)
+    held = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    got = L.linear_backward(dy, w, 0.73, out_dtype=torch.float32, workspace=held[:need])
+    assert (held[need:] == 77).all()
+    want = dy.double() @ gpu_lib.dequantize(w, 0.73).double()
+    bound = (n + 64) * 2.0 ** -24 * (dy.double().abs() @ gpu_lib.dequantize(w, 0.73).double().abs())
+    assert ((got.double() - want).abs() <= bound + 2.0 ** -24 * (want.abs() + bound)).all()

@@ -32,6 +32,7 @@ _SIGNATURES = {
     "opq_lowrank_backward_workspace_bytes": (_Z, [_L, _L, _L, _L, _L]),
     "opq_lowrank_backward": (_I, [_P, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _L, _P, _P, _I, _P, _Z, _P]),
     "opq_linear_backward_workspace_bytes": (_Z, [_L, _L, _L]),
+    "opq_linear_backward_codes_workspace_bytes": (_Z, [_L, _L, _L]),
     "opq_linear_backward": (_I, [_P, _P, _P, _P, _L, _L, _L, _F, _P, _I, _P, _Z, _P]),
     "opq_linear_backward_bits": (_I, [_P, _P, _P, _P, _L, _L, _L, _I, _F, _P, _I, _P, _Z, _P]),
     "opq_linear_backward_grouped": (_I, [_P, _P, _P, _P, _L, _L, _L, _L, _F, _P, _I, _P, _Z, _P]),
@@ -108,11 +109,15 @@ def lowrank_backward(dy: torch.Tensor, x: torch.Tensor, adapters: Adapters, inde
 _TOKENS, _ROWS = 1 << 22, 1 << 16
 
 
-def linear_backward_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Workspace bytes of linear_backward: of its largest block."""
+def linear_backward_workspace_bytes(m: int, n: int, k: int, bits: Optional[int] = None) -> int:
+    """Workspace bytes of linear_backward (its largest block's): enough for codes of any width, or of
+    `bits` bits, 4 of which need less."""
+    ask = load().opq_linear_backward_codes_workspace_bytes if bits == 4 else load().opq_linear_backward_workspace_bytes
+    if m <= _TOKENS and n <= _ROWS:
+        return ask(m, n, k)
     sizes = [(a, b) for a in {min(m, _TOKENS), m % _TOKENS if m > _TOKENS else 0}
              for b in {min(n, _ROWS), n % _ROWS if n > _ROWS else 0}]
-    return max(int(load().opq_linear_backward_workspace_bytes(a, b, k)) for a, b in sizes)
+    return max(ask(a, b, k) for a, b in sizes)
 
 
 def _check_rows(qw, n: int, k: int) -> None:
@@ -123,33 +128,28 @@ def _check_rows(qw, n: int, k: int) -> None:
         raise ValueError(f"weight buffers do not match n={n}, k={k}")
 
 
-def _backward_call(dy, weight, alpha, out, workspace) -> None:
+def _backward_call(name, dy, weight, alpha, out, k, workspace, room) -> None:
     """One call of the library, its tensors checked, on their device."""
-    (m, n), k = dy.shape, weight.shape[1]
-    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    name = "opq_linear_backward" + ("_bits" if isinstance(weight, opq.BitsWeight) else
-                                    "_grouped" if isinstance(weight, opq.GroupedWeight) else "")
+    m, n = dy.shape
     _check(name, getattr(load(), name)(
-        dy.data_ptr(), weight.packed.data_ptr(), weight.sign.data_ptr(), weight[2].data_ptr(), m, n, k, *weight[3:], alpha,
+        dy.data_ptr(), weight[0].data_ptr(), weight[1].data_ptr(), weight[2].data_ptr(), m, n, k, *weight[3:], alpha,
         out.data_ptr(), OPQ_BF16 if out.dtype == torch.bfloat16 else OPQ_F32, opq._ptr(workspace), room,
         opq._stream(dy.device)))
 
 
-def _backward_blocks(dy, weight, alpha, out, workspace) -> None:
-    """linear_backward, its tensors checked, as calls of the library."""
+def _backward_blocks(name, dy, weight, alpha, out, k, *space) -> None:
+    """The call of more tokens or rows than the library takes at once."""
     m, n = dy.shape
-    if m <= _TOKENS and n <= _ROWS:
-        return _backward_call(dy, weight, alpha, out, workspace)
     for t in range(0, m, _TOKENS):
         some, to = dy[t:t + _TOKENS], out[t:t + _TOKENS]
         if n <= _ROWS:
-            _backward_call(some, weight, alpha, to, workspace)
+            _backward_call(name, some, weight, alpha, to, k, *space)
             continue
         total = to if to.dtype == torch.float32 else torch.empty(to.shape, device=dy.device)
         part = torch.empty_like(total)
         for r in range(0, n, _ROWS):
             block = type(weight)(*(w[r:r + _ROWS] for w in weight[:3]), *weight[3:])
-            _backward_call(some[:, r:r + _ROWS].contiguous(), block, alpha, part if r else total, workspace)
+            _backward_call(name, some[:, r:r + _ROWS].contiguous(), block, alpha, part if r else total, k, *space)
             if r:
                 total.add_(part)
         if total is not to:
@@ -160,8 +160,8 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
                     out_dtype: torch.dtype = torch.bfloat16,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx [m, k] = dy [m, n] W', the gradient of opq.linear's x: dy bfloat16, weight any of
-    opq's stored forms.  `workspace`: a device tensor of linear_backward_workspace_bytes(m, n, k)
-    bytes (by default one of torch's allocator).  More than 65536 weight rows (a vocabulary's) are
+    opq's stored forms.  `workspace`: a device tensor of linear_backward_workspace_bytes(m, n, k,
+    bits) bytes (by default one of torch's allocator).  More than 65536 weight rows (a vocabulary's) are
     taken in blocks, whose float32 sums are added in order."""
     opq._need_cuda("dy", dy, torch.bfloat16, 2)
     if torch.is_grad_enabled() and dy.requires_grad:
@@ -188,19 +188,24 @@ def linear_backward(dy: torch.Tensor, weight, alpha: float, out: Optional[torch.
     for name, t in (("out", out), ("packed", weight.packed), ("sign", weight.sign), ("scale", weight[2])):
         if t.device != dy.device:
             raise ValueError(f"{name} must be on {dy.device}, got {t.device}")
+    name, bits = "opq_linear_backward", 4
     if isinstance(weight, opq.BitsWeight):
         opq._check_bits(weight, n, k)
+        name, bits = "opq_linear_backward_bits", weight.bits
     elif isinstance(weight, opq.GroupedWeight):
         opq._check_grouped(weight, n, k)
+        name = "opq_linear_backward_grouped"
     else:
         _check_rows(weight, n, k)
-    need = linear_backward_workspace_bytes(m, n, k)
+    need = linear_backward_workspace_bytes(m, n, k, bits)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
     elif workspace.device != dy.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dy.device}")
+    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    call = _backward_call if m <= _TOKENS and n <= _ROWS else _backward_blocks
     with torch.cuda.device(dy.device):
-        _backward_blocks(dy, weight, alpha, out, workspace)
+        call(name, dy, weight, alpha, out, k, workspace, room)
     if given and not out.is_inference():   # written, so autograd learns of it
         torch.autograd.graph.increment_version(out)
     return out

@@ -141,40 +141,54 @@ int opq_lowrank_backward(const opq_lowrank* adapters, const uint16_t* dy, int64_
 
 namespace {
 
-// The workspace's parts: W' transposed ([k][ld]), dy with rows of ld where its own are
-// shorter, the product's split sums, and (codes of other widths) W' as it is dequantized.
+// The workspace's parts, for 4-bit codes or for those of other widths: W' transposed ([k][ld]) at
+// its beginning and, for other widths, W' as it is dequantized, neither where few tokens take
+// 4-bit codes as they are; dy with rows of ld where its own are shorter than what is read; sums
+// that are split.  Sizes are whole MiB, one at least.
 struct BackwardSpace {
   int64_t ld;
   size_t padded, part, plain, bytes;
 };
-BackwardSpace backward_space(int64_t m, int64_t n, int64_t k) {
+BackwardSpace backward_space(int64_t m, int64_t n, int64_t k, bool codes) {
+  constexpr size_t kMiB = size_t(1) << 20;
+  const opq::BackwardShort few = opq::backward_short_plan(m, n, k);
+  const bool direct = codes && few.taken;
   BackwardSpace s;
   s.ld = n % 32 ? (n + 63) / 64 * 64 : n;  // padded rows: whole steps of the product
   size_t at = 0;
   auto take = [&](size_t bytes) {
+    const size_t here = at;
     at += (bytes + 255) & ~size_t(255);
-    return at;
+    return here;
   };
-  s.padded = take((size_t)k * s.ld * 2);
-  s.part = take(n < s.ld ? (size_t)m * s.ld * 2 : 0);
-  s.plain = take(std::max(opq::linear_dense_part_bytes(m, k, s.ld), opq::backward_short_plan(m, n, k).part_bytes));
-  s.bytes = take((size_t)n * k * 2);
+  take(direct ? 0 : (size_t)k * s.ld * 2);
+  s.padded = take((direct ? n % 8 != 0 : n < s.ld) ? (size_t)m * s.ld * 2 : 0);
+  s.part = take(direct ? few.part_bytes : opq::linear_dense_part_bytes(m, k, s.ld));
+  s.plain = take(codes ? 0 : (size_t)n * k * 2);
+  s.bytes = std::max(kMiB, (at + kMiB - 1) & ~(kMiB - 1));
   return s;
+}
+
+bool backward_sizes_ok(int64_t m, int64_t n, int64_t k) {
+  return m > 0 && n > 0 && k > 0 && k % 32 == 0 && m <= kMaxTokens && n <= kMaxLinear && k <= kMaxLinear;
 }
 
 }  // namespace
 
 size_t opq_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || n <= 0 || k <= 0 || k % 32 || m > kMaxTokens || n > kMaxLinear || k > kMaxLinear)
-    return 0;
-  return backward_space(m, n, k).bytes;
+  if (!backward_sizes_ok(m, n, k)) return 0;
+  return std::max(backward_space(m, n, k, true).bytes, backward_space(m, n, k, false).bytes);
+}
+
+size_t opq_linear_backward_codes_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return backward_sizes_ok(m, n, k) ? backward_space(m, n, k, true).bytes : 0;
 }
 
 // The checks of one storage form; `more` its own about shapes and types.
 static int backward_checks(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
                            const void* scale, int64_t m, int64_t n, int64_t k, float alpha,
-                           bool more_shape_ok, const void* dx, int dx_dtype, const void* workspace,
-                           size_t workspace_bytes) {
+                           bool more_shape_ok, bool codes, const void* dx, int dx_dtype,
+                           const void* workspace, size_t workspace_bytes) {
   if ((m > 0 && n > 0 && !dy) || (n > 0 && k > 0 && (!packed || !sign || !scale)) ||
       (m > 0 && k > 0 && !dx))
     return OPQ_ERR_NULL;
@@ -184,7 +198,8 @@ static int backward_checks(const uint16_t* dy, const uint32_t* packed, const uin
       !aligned16(dx) || !aligned16(workspace))
     return OPQ_ERR_ALIGN;
   if (!dtype_ok(dx_dtype)) return OPQ_ERR_DTYPE;
-  const size_t need = opq_linear_backward_workspace_bytes(m, n, k);
+  const size_t need = codes ? opq_linear_backward_codes_workspace_bytes(m, n, k)
+                            : opq_linear_backward_workspace_bytes(m, n, k);
   if (workspace_bytes < need || (need > 0 && !workspace)) return OPQ_ERR_WORKSPACE;
   if (m > kMaxTokens || n > kMaxLinear || k > kMaxLinear) return OPQ_ERR_UNSUPPORTED;
   return OPQ_OK;
@@ -203,9 +218,8 @@ static int backward_rows(const uint16_t** dy, int64_t* ldy, int64_t m, int64_t n
 }
 
 // The product, with W' transposed at the workspace's beginning (n > 0).
-static int backward_product(const uint16_t* dy, int64_t m, int64_t n, int64_t k, void* dx,
-                            int dx_dtype, char* ws, hipStream_t st) {
-  const BackwardSpace s = backward_space(m, n, k);
+static int backward_product(const uint16_t* dy, int64_t m, int64_t n, int64_t k, void* dx, int dx_dtype,
+                            const BackwardSpace& s, char* ws, hipStream_t st) {
   int64_t ldy;
   const int e = backward_rows(&dy, &ldy, m, n, s, ws, st);
   if (e != OPQ_OK) return e;
@@ -218,7 +232,7 @@ static int backward_product(const uint16_t* dy, int64_t m, int64_t n, int64_t k,
 static int backward_codes(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
                           const float* scale, const uint16_t* scale16, int64_t m, int64_t n, int64_t k,
                           int gs, const opq::Levels& lv, void* dx, int dx_dtype, char* ws, hipStream_t st) {
-  const BackwardSpace s = backward_space(m, n, k);
+  const BackwardSpace s = backward_space(m, n, k, true);
   if (opq::backward_short_plan(m, n, k).taken) {
     int64_t ldy = n;
     const int e = n % 8 ? backward_rows(&dy, &ldy, m, n, s, ws, st) : OPQ_OK;
@@ -229,7 +243,7 @@ static int backward_codes(const uint16_t* dy, const uint32_t* packed, const uint
   const int e = hip_status(opq::launch_dequantize_transposed(packed, sign, scale, scale16, n, k, gs, lv,
                                                              reinterpret_cast<uint16_t*>(ws), s.ld, st));
   if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, ws, st);
+  return backward_product(dy, m, n, k, dx, dx_dtype, s, ws, st);
 }
 
 // No rows of weights: sums of nothing.
@@ -240,7 +254,7 @@ static int no_rows(int64_t m, int64_t k, void* dx, int dx_dtype, hipStream_t st)
 int opq_linear_backward(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
                         const float* scale, int64_t m, int64_t n, int64_t k, float alpha, void* dx,
                         int dx_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, true, dx, dx_dtype, workspace,
+  int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, true, true, dx, dx_dtype, workspace,
                           workspace_bytes);
   if (e != OPQ_OK || m == 0 || k == 0) return e;
   const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -255,7 +269,7 @@ int opq_linear_backward_bits(const uint16_t* dy, const uint32_t* packed, const u
                              const float* scale, int64_t m, int64_t n, int64_t k, int bits,
                              float alpha, void* dx, int dx_dtype, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, bits >= 3 && bits <= 6, dx,
+  int e = backward_checks(dy, packed, sign, scale, m, n, k, alpha, bits >= 3 && bits <= 6, bits == 4, dx,
                           dx_dtype, workspace, workspace_bytes);
   if (e != OPQ_OK || m == 0 || k == 0) return e;
   if (bits == 4)
@@ -264,13 +278,13 @@ int opq_linear_backward_bits(const uint16_t* dy, const uint32_t* packed, const u
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (n == 0) return no_rows(m, k, dx, dx_dtype, st);
   char* ws = static_cast<char*>(workspace);
-  const BackwardSpace s = backward_space(m, n, k);
+  const BackwardSpace s = backward_space(m, n, k, false);
   uint16_t* w = reinterpret_cast<uint16_t*>(ws + s.plain);
   e = opq_dequantize_bits(packed, sign, scale, n, k, bits, alpha, w, stream);
   if (e != OPQ_OK) return e;
   e = hip_status(opq::launch_transpose(w, n, k, reinterpret_cast<uint16_t*>(ws), s.ld, st));
   if (e != OPQ_OK) return e;
-  return backward_product(dy, m, n, k, dx, dx_dtype, ws, st);
+  return backward_product(dy, m, n, k, dx, dx_dtype, s, ws, st);
 }
 
 int opq_linear_backward_grouped(const uint16_t* dy, const uint32_t* packed, const uint32_t* sign,
@@ -278,7 +292,7 @@ int opq_linear_backward_grouped(const uint16_t* dy, const uint32_t* packed, cons
                                 int64_t group, float alpha, void* dx, int dx_dtype,
                                 void* workspace, size_t workspace_bytes, void* stream) {
   const bool group_ok = (group == 32 || group == 64 || group == 128 || group == 256) && k % group == 0;
-  int e = backward_checks(dy, packed, sign, scale16, m, n, k, alpha, group_ok, dx, dx_dtype,
+  int e = backward_checks(dy, packed, sign, scale16, m, n, k, alpha, group_ok, true, dx, dx_dtype,
                           workspace, workspace_bytes);
   if (e != OPQ_OK || m == 0 || k == 0) return e;
   const hipStream_t st = static_cast<hipStream_t>(stream);
