@@ -161,3 +161,21 @@ def test_no_tokens(L):
     y = torch.randn((5, 32), device=DEV)
     at = torch.zeros(5, dtype=torch.int32, device=DEV)
     assert torch.equal(L.lowrank_add(y, torch.ones((5, 64), dtype=torch.bfloat16, device=DEV), none, at), y)
+
+
+# Long rows in few slices, so that a wave takes whole runs of steps, and tiles of every width: up to 16
+# tokens of an adapter, up to 32 and up to 64, each size of ranks, a block of tokens alone and many
+LONG = [(m, 2088, n, rank, count) for m, n in ((16400, 40), (64, 10248)) for rank in (8, 16, 24, 64, 128)
+        for count in ((5, 2, 1) if m > 64 else (60, 3, 1))]
+
+
+@pytest.mark.parametrize("m,k,n,rank,count", LONG)
+def test_long_rows(L, m, k, n, rank, count):
+    test_add(L, m, k, n, rank, count, "mixed", torch.bfloat16, torch.float32)
+    test_add(L, m, n, k, rank, count, "mixed", None, torch.float32)
+
+
+@pytest.mark.parametrize("m,k,n,rank,count", LONG + [(4096, 32, 11520, 16, 3), (2049, 4096, 4104, 8, 3), (20000, 24, 4096, 8, 3)])
+def test_gradients_of_long_rows(L, m, k, n, rank, count):
+    test_backward(L, m, k, n, rank, count, "mixed", torch.float32, torch.float32)
+    test_backward(L, m, n, k, rank, count, "mixed", torch.bfloat16, torch.bfloat16)

@@ -466,16 +466,15 @@ __global__ __launch_bounds__(W * kWave) void lowrank_shrink(ShrinkArgs a, PlanAr
                                                                   acc[h][i], 0, 0, 0);
         }
       };
+      // Whole runs first, then what is left, as two loops.  (As two branches of one they made the
+      // compiler copy the sums from turn to turn, for ranks up to 16 five wait states behind the
+      // matrix instruction that writes them, where eight are needed: it copied what was there before.)
       const int stop = min(end, whole);
       int at = begin + wave * run;
-      for (; at < end; at += kWaves * run) {
-        const int to = min(end, at + run);
-        if (at + kDepth <= stop && run == kDepth) {
-          some(at, std::integral_constant<int, kDepth>{}, true);
-        } else {
-          for (int u = at; u < to; ++u) some(u, std::integral_constant<int, 1>{}, u < whole);
-        }
-      }
+      if (run == kDepth)
+        for (; at + kDepth <= stop; at += kWaves * kDepth) some(at, std::integral_constant<int, kDepth>{}, true);
+      for (; at < end; at += kWaves * run)
+        for (int u = at; u < min(end, at + run); ++u) some(u, std::integral_constant<int, 1>{}, u < whole);
     };
     if (kParts > 2 && tile.size > 32) walk(std::integral_constant<int, kParts>{});
     else if (tile.size > 16) walk(std::integral_constant<int, 2>{});
