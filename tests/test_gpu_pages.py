@@ -212,3 +212,12 @@ def test_refusals(A):
         A.cache_copy_pages(cache, lens, lens[:2])
     with pytest.raises(ValueError):
         A.cache_copy_pages(cache, t, t)
+
+
+@pytest.mark.parametrize("rows,columns,pages", [(96, 5, 700), (97, 5, 700), (64, 256, 16384), (65, 256, 16384), (8, 9, 16384),
+                                                (8, 9, 16385), (200, 60, 16000), (300, 60, 16000)])
+def test_at_the_change_of_paths(A, rows, columns, pages):
+    for wild in (0.0, 0.1):
+        test_resize(A, rows, columns, pages, 16, wild)
+        test_fork(A, rows, columns, pages, 16, wild)
+        test_compact(A, rows, columns, pages, 16, wild)

@@ -54,8 +54,10 @@ hipError_t launch_lowrank_backward(const LowrankBackward& c, hipStream_t stream)
 // elements, n rounded up to 8 at least, zeros past n; part: the plan's bytes.  Up to 512 tokens,
 // the most that one workgroup holds sums of; a call takes (so / W' transposed and the dense product,
 // us) at 8, 64, 128, 333 and 512 tokens: 3840 x 3840 16/23, 26/29, 23/42, 34/41, 43/46; 11520 x 3840
-// 27/38, 43/51, 44/80, 64/88, 79/92; 20480 x 3840 38/73, 61/95, 67/143, 96/133, 119/142.  Two
-// workgroups' tokens decode twice: 1024 would take twice the 512, against 60, 120 and 217
+// 27/38, 43/51, 44/80, 64/88, 79/92; 20480 x 3840 38/73, 61/95, 67/143, 96/133, 119/142; with fewer
+// slices 3840 x 10240 23/38, 41/56, 39/92, 58/101, 72/103; 3840 x 20480 34/68, 67/102, 78/115,
+// 111/131, 135/133.  Two workgroups' tokens decode twice: 1024 would take twice the 512, against 60,
+// 120 and 217
 constexpr int64_t kBackwardShortTokens = 512;
 struct BackwardShort {
   bool taken;

@@ -22,10 +22,14 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 constexpr int kNoRow = 0x7FFFFFFF;
-// One workgroup: what it keeps lies in LDS.
+// One workgroup: what it keeps lies in LDS, which bounds the pages, and its sixteen waves take the rows in
+// turn, which bounds those.  One workgroup / four kernels, us in a graph, 64 columns and 4096
+// pages: 32 rows resized 6.2/10.1, forked 6.8/11.1; 96 rows 9.2/9.8, 11.0/11.5; 128 rows 10.9/9.9,
+// 13.2/11.5; 512 rows 32/10.6, 39/12.4 (launched one by one the four take 2 to 3 more).  A
+// compaction goes by entries: 4096 of them 6.5/10.3, 12288 9.7/10.4, 16384 11.2/10.4, 32768 17.4/10.6.
 constexpr int kOnePages = 16384;
-constexpr int64_t kOneEntries = 32768;
-constexpr int kOneRows = 2048;
+constexpr int64_t kOneEntries = 16384;
+constexpr int kOneRows = 96;
 
 struct Space {
   uint8_t* named;   // [words * 32] 1: pages named in full (fork), or named at all
@@ -312,7 +316,7 @@ size_t up256(size_t b) { return (b + 255u) & ~size_t(255); }
 template <PagesCall CALL>
 hipError_t launch(const PagesArgs& a, const Space& s, hipStream_t stream) {
   const int64_t entries = (int64_t)a.new_rows * a.columns;
-  if (a.pages <= kOnePages && entries <= kOneEntries && a.new_rows <= kOneRows) {
+  if (a.pages <= kOnePages && entries <= kOneEntries && (CALL == PagesCall::kCompact || a.new_rows <= kOneRows)) {
     hipLaunchKernelGGL(pages_one<CALL>, dim3(1), dim3(kPlanThreads), 0, stream, a, s);
     return hipGetLastError();
   }

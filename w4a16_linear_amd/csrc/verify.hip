@@ -324,7 +324,8 @@ struct VerifyPlan {
   bool small;
   int64_t pieces;
 };
-// Long pieces, unless they would make fewer than 512 workgroups.
+// Long pieces, unless they would make fewer than 512 workgroups (long / short, us in a graph: 8 rows of
+// 131072 9.9/9.0, 64 of 32000, 512 workgroups, 11.6/10.4, 128 of them 13.9/14.3, 64 of 131072 17.8/23.2).
 VerifyPlan verify_plan(int64_t batch, int64_t vocab) {
   const int64_t big = (vocab + kPiece - 1) / kPiece;
   if (batch * big >= 512 || vocab > (int64_t)kMaxPieces * kSmall) return {false, big};
