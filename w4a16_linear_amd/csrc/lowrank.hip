@@ -375,7 +375,7 @@ constexpr int shrink_tile(int64_t rank) { return rank > 32 ? kBlockTokens : kBlo
 // Workgroup (slice of d, share of the block's tiles, block of tokens).  A wave
 // takes its share of the slice's 32-wide steps for a tile, all tokens of the block that use
 // one adapter, and all rank rows; the waves' sums meet in LDS, the slices' in the
-// reader.  (The two sides of 4096 tokens, 3840 -> 11520, rank 16: 35 us, where reading the
+// reader.  (The two sides of 4096 tokens, 3840 -> 11520, rank 16: 33 us, where reading the
 // tokens alone takes 27.)
 // RT: 16-row tiles of the rank.  PLAN: the workgroup past the slices sorts the tokens for
 // the gradients, which wait for this launch anyway (9 us as a launch of its own).
@@ -580,7 +580,7 @@ struct ExpandShared {
 // and in every load and store sixteen lanes touch 256 bytes in a row.  What the tiles add
 // to is requested with the stack's block before the operands are made.  It and the result
 // pass the caches by, which are for the stack and c (4096 tokens, 3840 -> 20480, rank 64:
-// 111 us with ordinary loads and stores, 99 so); one block of tokens is small enough for both.
+// 113 us with ordinary loads and stores, 103 so); one block of tokens is small enough for both.
 template <int RS, bool BASE_BF16, bool OUT_BF16, bool SINGLE>
 __device__ __forceinline__ void expand(const ExpandArgs& a, ExpandShared<RS>& s, int bx, int by, int bz) {
   constexpr int kAhead = SINGLE ? 1 : RS > 1 && BASE_BF16 ? 4 : 2;  // by registers
@@ -758,7 +758,7 @@ struct FewArgs {
 // Every workgroup of a tile makes the tile's c anew, from rows of `down` that are in L2
 // after the first: workgroups of one tile are a multiple of 8 apart, on one XCD.
 // Bound by latency: index, rows, their sums, the product and the store follow one another
-// (3840 -> 3840, rank 8, 1 token: 7.7 us, of which the second round of loads is 2).
+// (3840 -> 3840, rank 8, 1 token: 8.1 us, of which the second round of loads is 2).
 template <int RT, bool BASE_BF16, bool OUT_BF16>
 __global__ __launch_bounds__(kFewThreads) void lowrank_add_few(FewArgs a) {
   constexpr int kDepth = BASE_BF16 ? 4 : 2;  // by registers
@@ -899,8 +899,10 @@ __global__ __launch_bounds__(kFewThreads) void lowrank_add_few(FewArgs a) {
 // ------------------------------------------------------------------ launches
 
 int64_t blocks_of(int64_t m) { return (m + kBlockTokens - 1) / kBlockTokens; }
-// One block of tokens: a workgroup a token, those that lead no tile end at once.  The
-// host does not know how many adapters a call meets; more blocks have work enough.
+// One block of tokens: a workgroup a token, those that lead no tile end at once.  More blocks have work
+// enough as long as a block meets few adapters (3840 -> 11520, rank 16: 128 tokens of one adapter
+// 14.5 us); tokens of as many adapters are walked tile by tile by few workgroups (65 to 256
+// of them 210 us, where calls of 64 take 24 to 63).
 bool single_block(int64_t m) { return m <= kBlockTokens; }
 
 struct ShrinkPlan {
@@ -912,7 +914,7 @@ struct ShrinkPlan {
 // begins.  Backward 512: dy comes from memory (8192 tokens of 10240, rank 64: 144 us, with 256
 // 237).  Forward 256, x was made a moment ago and is in cache; 128 past rank 32, where every
 // workgroup of the expand adds as many slices of longer rows (4096 tokens, 3840 -> 20480,
-// rank 64: 98 us, with 256 103; 2047 tokens, 10240 -> 3840, rank 32: 41, with 256 32).
+// rank 64: 102 us, with 256 104; 2047 tokens, 10240 -> 3840, rank 32: 42, with 256 33).
 constexpr int kBackwardGroups = 512;
 constexpr int forward_groups(int64_t rank) { return rank > 32 ? 128 : 256; }
 ShrinkPlan shrink_plan(int64_t m, int64_t d, int64_t rank, int64_t groups_wanted) {
@@ -980,8 +982,8 @@ namespace {
 
 // Adapters small enough to be read anew by every workgroup, and no more of those than the card
 // takes at once (calls in a graph, this kernel / both, us: 3840 -> 3840, rank 16, 1 token
-// 7.8/8.2, 48 tokens 9.1/11.3; 1024 -> 1024, 48 tokens 5.9/8.6; past the rules rank 32 of
-// 3840 -> 3840, 1 token 9.2/8.6, and 48 tokens of 3840 -> 11520, rank 16, 16.8/15.6).
+// 8.3/8.4, 48 tokens 9.2/10.9; 1024 -> 1024, 48 tokens 6.4/8.6; past the rules rank 32 of
+// 3840 -> 3840, 1 token 9.7/8.7, and 48 tokens of 3840 -> 11520, rank 16, 17.4/15.3).
 constexpr int64_t kFewElements = 1 << 16, kFewGroups = 256;
 bool few(int64_t m, int64_t k, int64_t n, int64_t rank) {
   return single_block(m) && rank <= 32 && k * rank <= kFewElements &&

@@ -50,7 +50,8 @@ class OPQLinear(nn.Module):
     when present, is float32.  x may be bfloat16 or float32 (it is rounded to
     bfloat16, the layer's activation type); y has x's dtype.  Gradients pass
     through to x (dx = dy W', dy rounded to bfloat16 as x is); the stored
-    weights take none."""
+    weights take none.  So y requires grad where x does, and calls that autograd
+    does not follow (attention's, say) refuse it but under torch.no_grad()."""
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True,
                  alpha: float = 0.73, device=None, group_size: Optional[int] = None,
@@ -150,7 +151,8 @@ class AdaptedLinear(nn.Module):
     stored; ``down`` [adapters, rank, in] and ``up`` [adapters, rank, out] (bfloat16) are the
     parameters to train, and one layer serves the requests of all of them at once.
 
-    A new stack changes nothing (``up`` starts as zeros).  The rank may be 1..128; it is kept as
+    y has x's dtype; in bfloat16 the projection's output is rounded before the adapters' is added, as
+    the gradient of x is between the two.  A new stack changes nothing (``up`` starts as zeros).  The rank may be 1..128; it is kept as
     the next multiple of 8, the rest zeros, which gradients leave zeros.  out_features must be
     a multiple of 8.  Types stay as they are made (bfloat16, scales float32): convert a model
     before its layers are quantized and adapted."""
@@ -295,7 +297,9 @@ def add_adapters(model: nn.Module, count: int, rank: int, scale: float = 1.0, sk
 
 def use_adapters(model: nn.Module, index: Optional[torch.Tensor]) -> None:
     """Which adapter each token (or sequence) uses in the forwards that follow, for every
-    AdaptedLinear of `model`; None: the base alone."""
+    AdaptedLinear of `model`; None: the base alone.  The layers keep it, whoever calls them: threads that
+    serve one model at once pass `index` to its layers instead, and a forward that is recomputed for
+    its backward pass (checkpointing) has that pass before the index changes."""
     for mod in model.modules():
         if isinstance(mod, AdaptedLinear):
             mod.index = index
