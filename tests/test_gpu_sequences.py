@@ -117,3 +117,54 @@ def test_steps_in_a_graph(A):
         want = step(other, *held)
         torch.cuda.synchronize()
         assert all(torch.equal(r, w) for r, w in zip(res, want)) and torch.equal(cache.k_scale, other.k_scale)
+
+
+@pytest.mark.parametrize("pages,columns", [(9, 4), (14, 3), (40, 6)])
+def test_rows_always_hold_their_tokens(A, pages, columns):
+    """Random steps in pools that run out at times: drafted, accepted, forked, dropped, compacted.  After
+    each, every row holds the tokens that a plain list of them says, and `lost` counts the others."""
+    import numpy as np
+    from w4a16_linear_amd.attention_module import PagedSequences, token_slots
+    rng = np.random.default_rng(pages)
+    rows, page, draft = 5, 16, 9
+    seqs, cache = PagedSequences(rows, columns, pages, page), A.new_cache(pages, 1, page, 64, "fp8")
+    tokens, lost, mark, short = [[] for _ in range(rows)], [0] * rows, 0, 0
+
+    def compare():
+        assert seqs.lens.tolist() == [len(t) for t in tokens] and seqs.lost.tolist() == lost
+        for row, want in enumerate(tokens):
+            assert _held(seqs, cache, row) == want
+
+    for step in range(60):
+        kind = rng.random()
+        if kind < 0.6:
+            short += int(seqs.room(draft)) > 0
+            places = seqs.lens[:, None] + torch.arange(draft, dtype=torch.int32, device=DEV)
+            slots = token_slots(seqs.page_table, places, page, pages)
+            marks = mark + torch.arange(rows * draft, device=DEV).view(rows, draft).float()
+            mark += rows * draft
+            cache.k_scale.view(-1)[slots[slots >= 0].long()] = marks[slots >= 0]
+            kept, count = np.full((rows, draft), -1, np.int32), rng.integers(0, draft + 1, rows).astype(np.int32)
+            for b in range(rows):
+                kept[b, :count[b]] = np.sort(rng.permutation(draft)[:count[b]])
+                has = slots[b].tolist()
+                stored = [float(marks[b, i]) for i in kept[b, :count[b]] if has[i] >= 0]
+                tokens[b] = tokens[b] + stored
+                lost[b] += int(count[b]) - len(stored)
+            seqs.accept([cache], torch.from_numpy(kept).to(DEV), torch.from_numpy(count).to(DEV))
+        elif kind < 0.9:
+            parents = rng.integers(-1, rows + 1, rows)
+            missing = int(seqs.fork([cache], torch.from_numpy(parents.astype(np.int32)).to(DEV)))
+            short += missing > 0
+            ended = seqs.lens.tolist()
+            old, new = [(tokens[a], lost[a]) if 0 <= a < rows else ([], 0) for a in parents], []
+            for (t, c), n in zip(old, ended):
+                assert n == len(t) or n == len(t) // page * page
+                missing -= n != len(t)
+                new.append((t[:n], c + len(t) - n))
+            assert missing == 0
+            tokens, lost = [t for t, _ in new], [c for _, c in new]
+        else:
+            seqs.compact([cache])
+        compare()
+    assert (short > 0) == (pages < rows * columns)
