@@ -1,4 +1,6 @@
 """AdaptedLinear and OPQLinear under autograd, streams and graphs on the GPU."""
+import copy
+
 import pytest
 import torch
 
@@ -378,3 +380,46 @@ def test_layers_share_no_workspace(L, gpu_lib, monkeypatch):
     for s in range(2):
         for base, adapted in got[s]:
             assert torch.equal(base, sets[s][3]) and torch.equal(adapted, sets[s][4])
+
+
+@pytest.mark.parametrize("m", [6, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_training_step_in_a_graph(L, gpu_lib, m, dtype):
+    """Two adapted layers, forward, backward and update captured together: replays on new inputs, with
+    eager work between, leave the parameters that eager steps leave."""
+    layers = [_layer(128, 256, 3, 8, seed=1, bits=5), _layer(256, 64, 3, 5, seed=2)]
+    eager, fresh = copy.deepcopy(layers), copy.deepcopy(layers)
+    x, dy = (torch.zeros((m, w), dtype=dtype, device=DEV) for w in (128, 64))
+    index = torch.zeros(m, dtype=torch.int32, device=DEV)
+
+    def step(layers):
+        h = torch.relu(layers[0](x, index))
+        layers[1](h, index).backward(dy)
+        with torch.no_grad():
+            for layer in layers:
+                for p in (layer.down, layer.up):
+                    p.sub_(0.01 * p.grad)
+        for layer in layers:
+            layer.down.grad = layer.up.grad = None
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(layers)                                                        # of zeros: the parameters stay
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(layers)
+    g = _gen(m)
+    for _ in range(4):
+        x.copy_(torch.randn(x.shape, generator=g, device=DEV))
+        dy.copy_(torch.randn(dy.shape, generator=g, device=DEV))
+        index.copy_(_index("mixed", m, 3, g))
+        graph.replay()
+        step(eager)
+        torch.cuda.synchronize()
+        for a, b in zip(layers, eager):
+            assert torch.equal(a.down, b.down) and torch.equal(a.up, b.up)
+    assert not torch.equal(layers[0].down, fresh[0].down) and not torch.equal(layers[1].up, fresh[1].up)
