@@ -168,3 +168,17 @@ def test_rows_always_hold_their_tokens(A, pages, columns):
             seqs.compact([cache])
         compare()
     assert (short > 0) == (pages < rows * columns)
+
+
+def test_a_refused_call_leaves_the_rows(A):
+    """A cache that cannot be copied in is refused before the table changes."""
+    seqs, cache = _filled(A, pages=8, rows=3, columns=3, lens=_ints(20, 9, 0))
+    before = [seqs.page_table, seqs.lens, seqs.lost]
+    host = A.new_cache(8, 1, 16, 64, "fp8", device="cpu")
+    for call in (lambda: seqs.fork([cache, host], _ints(0, 0, 1)), lambda: seqs.compact([cache, host]),
+                 lambda: seqs.fork([cache], _ints(0, 0, 1).long())):
+        with pytest.raises(ValueError):
+            call()
+        assert seqs.page_table is before[0] and seqs.lens is before[1] and seqs.lost is before[2]
+        for row, n in enumerate((20, 9, 0)):
+            assert _held(seqs, cache, row) == [1000.0 * (row + 1) + i for i in range(n)]

@@ -222,30 +222,30 @@ class PagedSequences:
         page by page but for a last page that is not full; returns `missing`, the rows that
         end with their last full page because no page was free."""
         self._caches(caches)
-        rows = self.lost.shape[0]
-        self.page_table, lens, src, dst, self.missing = A.pages_fork(
-            self.page_table, self.lens, parents, self.pages, self.page)
+        table, lens, src, dst, missing = A.pages_fork(self.page_table, self.lens, parents, self.pages, self.page)
         for cache in caches:
             A.cache_copy_pages(cache, src, dst)
+        rows = self.lost.shape[0]
         if rows:
             kept = self.lost[parents.clamp(0, rows - 1).long()]
-            self.lost = torch.where((parents >= 0) & (parents < rows), kept, 0)
+            lost = torch.where((parents >= 0) & (parents < rows), kept, 0)
         else:
-            self.lost = torch.zeros_like(lens)
-        if self.page_table.shape[1]:
+            lost = torch.zeros_like(lens)
+        if table.shape[1]:
             full = torch.div((lens - 1).clamp_min(0), self.page, rounding_mode="floor")   # pages before the last
-            last = torch.gather(self.page_table, 1, full[:, None].long())[:, 0]
+            last = torch.gather(table, 1, full[:, None].long())[:, 0]
             held = torch.where((lens > 0) & (last < 0), full * self.page, lens)
-            self.lost, lens = self.lost + (lens - held), held
-        self.lens = lens
-        return self.missing
+            lost, lens = lost + (lens - held), held
+        self.page_table, self.lens, self.lost, self.missing = table, lens, lost, missing
+        return missing
 
     def compact(self, caches: Sequence[A.PagedCache]) -> torch.Tensor:
         """Move the pages in use to the lowest ids; returns their number (int32 [1], on the device)."""
         self._caches(caches)
-        self.page_table, src, dst, used = A.pages_compact(self.page_table, self.pages)
+        table, src, dst, used = A.pages_compact(self.page_table, self.pages)
         for cache in caches:
             A.cache_copy_pages(cache, src, dst)
+        self.page_table = table
         return used
 
 
